@@ -46,6 +46,12 @@ _SIGS = {
                                     c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp,
                                     c_vp, c_vp, c_vp, c_vp, c_sz, c_vp]),
     "w4a4_mx8_quantize": (c_int, [c_vp, c_i64, c_int, c_vp, c_vp, c_vp, c_vp, c_i64, c_vp]),
+    "w4a4_mx_quantize_rows": (c_int, [c_i64, c_int, c_int, c_vp, c_i64, c_vp, c_vp, c_vp, c_vp]),
+    "w4a4_add_rmsnorm_fwd": (c_int, [c_i64, c_int, ctypes.c_float, c_vp, c_i64, c_vp, c_int, c_vp, c_int,
+                                     c_int, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp]),
+    "w4a4_add_rmsnorm_bwd": (c_int, [c_i64, c_int, c_vp, c_vp, c_int, c_vp, c_int, c_vp, c_vp,
+                                     c_vp, c_vp, c_vp, c_vp, c_sz, c_vp]),
+    "w4a4_mx_linear_fwd": (c_int, [c_i64, c_int, c_int, c_int, c_vp, c_vp, c_vp, c_vp, c_vp, c_i64, c_vp]),
     "w4a4_check_routing": (c_int, [c_vp, c_i64, c_int, c_int, c_vp, c_vp]),
     "w4a4_quantize_permute_noalloc": (c_int, [c_vp, c_i64, c_int, c_vp, c_int, c_int, c_int,
                                               c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp]),
@@ -58,6 +64,11 @@ _SIGS = {
 WS_QUANTIZE_PERMUTE, WS_FORWARD, WS_BACKWARD, WS_LINEAR_BACKWARD = 0, 1, 2, 3
 WS_QUANTIZE_PERMUTE_DOMAIN = 4
 WS_MX8_BACKWARD = 5
+WS_RMSNORM_BACKWARD = 6
+
+# Element formats of the MX calls (w4a4_mx_format) and types (w4a4_dtype)
+MX_NONE, MX_FP4, MX_FP8 = -1, 0, 1
+_DTYPES = {torch.bfloat16: 0, torch.float32: 1}
 
 
 class W4A4Error(RuntimeError):
@@ -404,6 +415,158 @@ def w4a4_mx_grouped_expert_fwd(xq, topk_w, w1q, w2q, T, H, I, E, k, row_align=1,
         _p(res["y"]), _p(res.get("h")), _p(res.get("a")), _p(res.get("fc1_f32")),
         _p(res.get("a_codes")), _p(res.get("a_scales")), _p(ws), ws.numel(), _stream()))
     return res
+
+
+# ------------------------------------------ pre-norm and the dense MX product
+# These calls launch on the current stream of their tensors' device (which is
+# made current for the call), and check types, shapes and layouts.
+def _ptr(t, name, shape, dtype, device, rows=False):
+    """Address of t (None: no tensor).  A dense tensor, or with `rows` one whose rows may be
+    further apart."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != shape or t.device != device:
+        raise W4A4Error(f"{name}: {dtype} {tuple(shape)} on {device} expected, "
+                        f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    if not t.is_contiguous() and not (rows and (t.stride(1) == 1 or t.shape[0] == 0)):
+        raise W4A4Error(f"{name} is not {'row-contiguous' if rows else 'contiguous'}")
+    return t.data_ptr()
+
+
+def _matrix(t, name, dtype=None):
+    if not isinstance(t, torch.Tensor) or t.dim() != 2 or not t.is_cuda or (dtype and t.dtype != dtype):
+        raise W4A4Error(f"{name} must be a 2-d {dtype or ''} tensor on the GPU")
+    return t.shape, t.device
+
+
+def _pitch(t):
+    """Elements between the rows of t (one row has no other pitch than its own length)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _dtype(t, name):
+    try:
+        return _DTYPES[t.dtype]
+    except KeyError:
+        raise W4A4Error(f"{name} must be bfloat16 or float32, got {t.dtype}") from None
+
+
+def _call(fn, device, *args):
+    stream = torch.cuda.current_stream(device).cuda_stream
+    if device.index == torch.cuda.current_device():
+        _check(fn(*args, stream))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, stream))
+
+
+def _code_shape(T, K, fmt):
+    if fmt not in (MX_FP4, MX_FP8):
+        raise W4A4Error(f"format {fmt} is neither MX_FP4 nor MX_FP8")
+    return (T, K // 2) if fmt == MX_FP4 else (T, K)
+
+
+def _mx_buffers(out, T, K, fmt, device):
+    """The code and scale buffers of `out`, allocated where it has none, and their addresses."""
+    cs, ss = _code_shape(T, K, fmt), (T, K // 32)
+    codes, scales = out.get("codes"), out.get("scales")
+    if codes is None:
+        codes = out["codes"] = torch.empty(cs, dtype=torch.uint8, device=device)
+    if scales is None:
+        scales = out["scales"] = torch.empty(ss, dtype=torch.uint8, device=device)
+    return (_ptr(codes, "codes", cs, torch.uint8, device), _ptr(scales, "scales", ss, torch.uint8, device))
+
+
+def w4a4_mx_quantize_rows(x, fmt, out=None):
+    """MXFP4 (fmt MX_FP4) or MXFP8 (MX_FP8) of the rows of x [T, K] bf16 (K % 32 == 0; a column slice
+    of a wider matrix will do).  Returns a dict: codes [T, K/2] or [T, K] u8, scales [T, K/32] u8
+    (the tensors of `out` where given).  An `offsets` tensor ([2] int32) in `out` receives {0, T}
+    for ``w4a4_linear_bwd``."""
+    (T, K), dev = _matrix(x, "x", torch.bfloat16)
+    res = {} if out is None else dict(out)
+    codes, scales = _mx_buffers(res, T, K, fmt, dev)
+    _call(load().w4a4_mx_quantize_rows, dev, T, K, fmt, _ptr(x, "x", x.shape, torch.bfloat16, dev, rows=True),
+          _pitch(x), codes, scales, _ptr(res.get("offsets"), "offsets", (2,), torch.int32, dev))
+    return res
+
+
+def w4a4_add_rmsnorm_fwd(x, gamma, eps=1e-6, residual=None, fmt=None, y=True, save=False, out=None):
+    """s = x + residual (rounded to the residual's type), y = bf16(s * rstd * gamma) with
+    rstd = (mean s^2 + eps)^-1/2, and the MX encoding of y.
+
+    x [T, H] bf16 (a column slice will do), residual [T, H] bf16 or float32 or None (s = x),
+    gamma [H] bf16 or float32; fmt: None, MX_FP4 or MX_FP8; y: whether the bf16 output is wanted;
+    save: whether rstd is (for the backward).  Returns a dict with what was asked for: sum (with a
+    residual), y, codes and scales (with fmt), rstd.  Tensors of `out` are used where given; its
+    `sum` may be the residual itself (in place), and its `offsets` ([2] int32) receives {0, T}."""
+    (T, H), dev = _matrix(x, "x", torch.bfloat16)
+    res = {} if out is None else dict(out)
+    total = res.get("sum")
+    if total is None and residual is not None:
+        total = res["sum"] = torch.empty(T, H, dtype=residual.dtype, device=dev)
+    stream = residual if residual is not None else total if total is not None else x
+    rt = _dtype(stream, "residual")
+    if y and res.get("y") is None:
+        res["y"] = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
+    if save and res.get("rstd") is None:
+        res["rstd"] = torch.empty(T, dtype=torch.float32, device=dev)
+    codes, scales = (None, None) if fmt is None else _mx_buffers(res, T, H, fmt, dev)
+    _call(load().w4a4_add_rmsnorm_fwd, dev, T, H, eps, _ptr(x, "x", x.shape, torch.bfloat16, dev, rows=True),
+          _pitch(x), _ptr(residual, "residual", x.shape, stream.dtype, dev), rt,
+          _ptr(gamma, "gamma", (H,), gamma.dtype, dev), _dtype(gamma, "gamma"), MX_NONE if fmt is None else fmt,
+          _ptr(total, "sum", x.shape, stream.dtype, dev), _ptr(res.get("y"), "y", x.shape, torch.bfloat16, dev),
+          codes, scales, _ptr(res.get("rstd"), "rstd", (T,), torch.float32, dev),
+          _ptr(res.get("offsets"), "offsets", (2,), torch.int32, dev))
+    return res
+
+
+def w4a4_add_rmsnorm_bwd(dy, sum, gamma, rstd, dsum=None, dgamma=True, out=None, workspace=None):
+    """Gradients of ``w4a4_add_rmsnorm_fwd`` for dy [T, H] bf16, the gradient of y, and dsum (optional,
+    the type of `sum`), the gradient that reaches the sum along the residual stream.
+
+    sum: the forward's (its x where there was no residual), rstd: the forward's.  Returns a dict:
+    dres [T, H] (the type of `sum`), the gradient of the residual and of x, and dgamma [H] float32
+    unless `dgamma` is false.  Tensors of `out` are used where given; a `dx` there ([T, H] bf16)
+    receives dres rounded to bf16."""
+    (T, H), dev = _matrix(dy, "dy", torch.bfloat16)
+    rt = _dtype(sum, "sum")
+    res = {} if out is None else dict(out)
+    if res.get("dres") is None:
+        res["dres"] = torch.empty(T, H, dtype=sum.dtype, device=dev)
+    nbytes = 0
+    if dgamma:
+        if res.get("dgamma") is None:
+            res["dgamma"] = torch.empty(H, dtype=torch.float32, device=dev)
+        nbytes = workspace_size(WS_RMSNORM_BACKWARD, T, H, 0, 1, 1)
+        workspace = _workspace(nbytes, dev, workspace)
+    _call(load().w4a4_add_rmsnorm_bwd, dev, T, H, _ptr(dy, "dy", dy.shape, torch.bfloat16, dev),
+          _ptr(sum, "sum", dy.shape, sum.dtype, dev), rt, _ptr(gamma, "gamma", (H,), gamma.dtype, dev),
+          _dtype(gamma, "gamma"), _ptr(rstd, "rstd", (T,), torch.float32, dev),
+          _ptr(dsum, "dsum", dy.shape, sum.dtype, dev), _ptr(res["dres"], "dres", dy.shape, sum.dtype, dev),
+          _ptr(res.get("dx"), "dx", dy.shape, torch.bfloat16, dev),
+          _ptr(res["dgamma"], "dgamma", (H,), torch.float32, dev) if dgamma else None,
+          workspace.data_ptr() if dgamma else None, workspace.numel() if dgamma else 0)
+    return res
+
+
+def w4a4_mx_linear_fwd(xq, wq, T, K, N, y=None):
+    """y [T, N] = x W^T on MX operands, bf16 out, FP32 accumulation.
+
+    xq: codes and scales of ``w4a4_add_rmsnorm_fwd`` or ``w4a4_mx_quantize_rows`` (MXFP8 or MXFP4, told
+    apart by the codes' width); wq: ``w4a4_mx_quantize_rows(w, MX_FP4)`` of the weight w [N, K].  K % 128 == 0, N % 8 == 0.  y: where to write (a column slice will do).
+    A row's bits do not depend on T or on the other rows."""
+    codes = xq["codes"]
+    _, dev = _matrix(codes, "xq codes", torch.uint8)
+    fmt = MX_FP8 if codes.shape[1] == K else MX_FP4
+    if y is None:
+        y = torch.empty(T, N, dtype=torch.bfloat16, device=dev)
+    _call(load().w4a4_mx_linear_fwd, dev, T, K, N, fmt,
+          _ptr(codes, "xq codes", _code_shape(T, K, fmt), torch.uint8, dev),
+          _ptr(xq["scales"], "xq scales", (T, K // 32), torch.uint8, dev),
+          _ptr(wq["codes"], "wq codes", (N, K // 2), torch.uint8, dev),
+          _ptr(wq["scales"], "wq scales", (N, K // 32), torch.uint8, dev),
+          _ptr(y, "y", (T, N), torch.bfloat16, dev, rows=True), _pitch(y))
+    return y
 
 
 def w4a4_profiler_enable(on=True):

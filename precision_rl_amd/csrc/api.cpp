@@ -249,6 +249,10 @@ size_t w4a4_workspace_size(int kind, int64_t T, int H, int I, int E, int k, int 
     if (H <= 0 || I <= 0 || H % 256 || I % 256) return 0;
     return round_up(linear_wgrad_schedule_ints(H, I) * 4);
   }
+  if (kind == W4A4_WS_RMSNORM_BACKWARD) {
+    if (T < 0 || H <= 0 || H > kMaxRowLen) return 0;
+    return round_up(static_cast<size_t>(norm_bwd_blocks(T, H)) * H * 4);
+  }
   const int64_t cap = w4a4_rows_capacity(T, k, E, row_align);
   if (cap < 0 || H <= 0) return 0;
   switch (kind) {
@@ -733,6 +737,150 @@ w4a4_status w4a4_mx8_quantize(const void* x, int64_t R, int C, uint8_t* q_rows, 
   REQUIRE_PTR(x); REQUIRE_PTR(q_rows); REQUIRE_PTR(s_rows); REQUIRE_PTR(q_cols); REQUIRE_PTR(s_cols);
   if (!launch_q8_dual(static_cast<const uint16_t*>(x), nullptr, R, C, 0, nullptr, 0, pitch, q_rows, s_rows, q_cols,
                       s_cols, "mx8_quant_dual", static_cast<hipStream_t>(stream)))
+    return W4A4_ERR_LAUNCH;
+  return W4A4_OK;
+}
+
+namespace {
+constexpr int64_t kMaxRows = (int64_t{1} << 31) - 1;
+
+bool valid_dtype(int d) { return d == W4A4_BF16 || d == W4A4_F32; }
+
+// Size checks shared by the dense MX calls.
+w4a4_status check_rows(int64_t T, int K, int multiple) {
+  if (T < 0 || K <= 0)
+    return fail(W4A4_ERR_INVALID_ARG, "bad size (T=%lld, row length %d)", static_cast<long long>(T), K);
+  if (K % multiple) return fail(W4A4_ERR_INVALID_ARG, "row length %d is not a multiple of %d", K, multiple);
+  if (T > kMaxRows) return fail(W4A4_ERR_UNSUPPORTED, "T=%lld exceeds int32 row indices", static_cast<long long>(T));
+  return W4A4_OK;
+}
+w4a4_status check_stride(const char* what, int64_t stride, int64_t width) {
+  if (stride < width || stride % 8 || stride > (int64_t{1} << 40))
+    return fail(W4A4_ERR_INVALID_ARG, "%s=%lld must be a multiple of 8 and at least the row length %lld", what,
+                static_cast<long long>(stride), static_cast<long long>(width));
+  return W4A4_OK;
+}
+}  // namespace
+
+w4a4_status w4a4_mx_quantize_rows(int64_t T, int K, int format, const void* x, int64_t x_stride, uint8_t* codes,
+                                  uint8_t* scales, int32_t* offsets, void* stream) {
+  g_last_error.clear();
+  w4a4_status st = check_rows(T, K, 32);
+  if (st != W4A4_OK) return st;
+  if (format != W4A4_MX_FP4 && format != W4A4_MX_FP8)
+    return fail(W4A4_ERR_INVALID_ARG, "format %d is neither W4A4_MX_FP4 nor W4A4_MX_FP8", format);
+  if ((st = check_stride("x_stride", x_stride, K)) != W4A4_OK) return st;
+  if (T > 0) {
+    REQUIRE_PTR(x);
+    REQUIRE_PTR(codes);
+    REQUIRE_PTR(scales);
+  }
+  OPTIONAL_PTR(offsets);
+  if (T == 0 && offsets == nullptr) return W4A4_OK;
+  if (!launch_mx_quantize_rows(static_cast<const uint16_t*>(x), x_stride, T, K, format, codes, scales, offsets,
+                               static_cast<hipStream_t>(stream)))
+    return W4A4_ERR_LAUNCH;
+  return W4A4_OK;
+}
+
+w4a4_status w4a4_add_rmsnorm_fwd(int64_t T, int H, float eps, const void* x, int64_t x_stride, const void* residual,
+                                 int residual_dtype, const void* gamma, int gamma_dtype, int format, void* sum,
+                                 void* y, uint8_t* codes, uint8_t* scales, float* rstd, int32_t* offsets,
+                                 void* stream) {
+  g_last_error.clear();
+  if (format != W4A4_MX_NONE && format != W4A4_MX_FP4 && format != W4A4_MX_FP8)
+    return fail(W4A4_ERR_INVALID_ARG, "unknown format %d", format);
+  w4a4_status st = check_rows(T, H, format == W4A4_MX_NONE ? 8 : 32);
+  if (st != W4A4_OK) return st;
+  if (H > kMaxRowLen) return fail(W4A4_ERR_UNSUPPORTED, "H=%d > %d", H, kMaxRowLen);
+  if (!valid_dtype(residual_dtype) || !valid_dtype(gamma_dtype))
+    return fail(W4A4_ERR_INVALID_ARG, "unknown element type (residual_dtype=%d, gamma_dtype=%d)", residual_dtype,
+                gamma_dtype);
+  if (!(eps > 0.0f) || eps > 3.4028235e38f)
+    return fail(W4A4_ERR_INVALID_ARG, "eps=%g must be positive and finite", static_cast<double>(eps));
+  if ((st = check_stride("x_stride", x_stride, H)) != W4A4_OK) return st;
+  if (format == W4A4_MX_NONE && (codes != nullptr || scales != nullptr))
+    return fail(W4A4_ERR_INVALID_ARG, "codes and scales need a format");
+  if (T > 0) {
+    REQUIRE_PTR(x);
+    REQUIRE_PTR(gamma);
+    if (format != W4A4_MX_NONE) {
+      REQUIRE_PTR(codes);
+      REQUIRE_PTR(scales);
+    }
+    if (sum != nullptr && sum == x && (residual_dtype != W4A4_BF16 || x_stride != H))
+      return fail(W4A4_ERR_INVALID_ARG, "sum may be x only where x is dense and the residual stream bf16");
+  }
+  OPTIONAL_PTR(residual);
+  OPTIONAL_PTR(sum);
+  OPTIONAL_PTR(y);
+  OPTIONAL_PTR(rstd);
+  OPTIONAL_PTR(offsets);
+  if (T == 0 && offsets == nullptr) return W4A4_OK;
+  const NormFwdArgs a{T, H, eps, static_cast<const uint16_t*>(x), x_stride, residual, T > 0 ? gamma : nullptr,
+                      gamma_dtype == W4A4_F32, sum, static_cast<uint16_t*>(y), codes, scales, rstd, offsets};
+  if (!launch_add_rmsnorm(a, residual_dtype == W4A4_F32, format, static_cast<hipStream_t>(stream)))
+    return W4A4_ERR_LAUNCH;
+  return W4A4_OK;
+}
+
+w4a4_status w4a4_add_rmsnorm_bwd(int64_t T, int H, const void* dy, const void* sum, int residual_dtype,
+                                 const void* gamma, int gamma_dtype, const float* rstd, const void* dsum, void* dres,
+                                 void* dx, float* dgamma, void* workspace, size_t workspace_bytes, void* stream) {
+  g_last_error.clear();
+  w4a4_status st = check_rows(T, H, 8);
+  if (st != W4A4_OK) return st;
+  if (H > kMaxRowLen) return fail(W4A4_ERR_UNSUPPORTED, "H=%d > %d", H, kMaxRowLen);
+  if (!valid_dtype(residual_dtype) || !valid_dtype(gamma_dtype))
+    return fail(W4A4_ERR_INVALID_ARG, "unknown element type (residual_dtype=%d, gamma_dtype=%d)", residual_dtype,
+                gamma_dtype);
+  if (T > 0) {
+    REQUIRE_PTR(dy);
+    REQUIRE_PTR(sum);
+    REQUIRE_PTR(gamma);
+    REQUIRE_PTR(rstd);
+    REQUIRE_PTR(dres);
+    if (dres == dy && residual_dtype != W4A4_BF16)
+      return fail(W4A4_ERR_INVALID_ARG, "dres may be dy only where the residual stream is bf16");
+  }
+  OPTIONAL_PTR(dsum);
+  OPTIONAL_PTR(dx);
+  OPTIONAL_PTR(dgamma);
+  if (dgamma != nullptr && T > 0) {
+    const size_t need = w4a4_workspace_size(W4A4_WS_RMSNORM_BACKWARD, T, H, 0, 1, 1, 1);
+    if (workspace == nullptr || workspace_bytes < need)
+      return fail(W4A4_ERR_WORKSPACE, "workspace needs %zu bytes", need);
+    REQUIRE_PTR(workspace);
+  }
+  const NormBwdArgs a{T, H, static_cast<const uint16_t*>(dy), sum, gamma, gamma_dtype == W4A4_F32, rstd, dsum, dres,
+                      static_cast<uint16_t*>(dx), dgamma != nullptr ? static_cast<float*>(workspace) : nullptr};
+  if (!launch_add_rmsnorm_bwd(a, residual_dtype == W4A4_F32, dgamma, static_cast<hipStream_t>(stream)))
+    return W4A4_ERR_LAUNCH;
+  return W4A4_OK;
+}
+
+w4a4_status w4a4_mx_linear_fwd(int64_t T, int K, int N, int format, const uint8_t* x_codes, const uint8_t* x_scales,
+                               const uint8_t* w_codes, const uint8_t* w_scales, void* y, int64_t y_stride,
+                               void* stream) {
+  g_last_error.clear();
+  w4a4_status st = check_rows(T, K, 32);
+  if (st != W4A4_OK) return st;
+  if (N <= 0) return fail(W4A4_ERR_INVALID_ARG, "N=%d", N);
+  if (format != W4A4_MX_FP4 && format != W4A4_MX_FP8)
+    return fail(W4A4_ERR_INVALID_ARG, "format %d is neither W4A4_MX_FP4 nor W4A4_MX_FP8", format);
+  if (K % 128 || N % 8)
+    return fail(W4A4_ERR_UNSUPPORTED, "kernels need K %% 128 == 0 and N %% 8 == 0 (K=%d N=%d)", K, N);
+  if (K > 65536) return fail(W4A4_ERR_UNSUPPORTED, "K=%d > 65536", K);
+  if ((st = check_stride("y_stride", y_stride, N)) != W4A4_OK) return st;
+  if (T > 0) {
+    REQUIRE_PTR(x_codes);
+    REQUIRE_PTR(x_scales);
+    REQUIRE_PTR(w_codes);
+    REQUIRE_PTR(w_scales);
+    REQUIRE_PTR(y);
+  }
+  if (!launch_mx_linear(T, K, N, format == W4A4_MX_FP8, x_codes, x_scales, w_codes, w_scales,
+                        static_cast<uint16_t*>(y), y_stride, static_cast<hipStream_t>(stream)))
     return W4A4_ERR_LAUNCH;
   return W4A4_OK;
 }

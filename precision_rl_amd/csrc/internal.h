@@ -179,6 +179,56 @@ bool launch_linear_dgrad(int64_t T, int K, int N, const int32_t* offsets, const 
 bool launch_linear_wgrad(int64_t T, int K, int N, const int32_t* offsets, const uint16_t* dy,
                          const uint16_t* x, uint16_t* dw, int32_t* sched, hipStream_t s);
 
+// ------------------------------------------- pre-norm and the dense MX product
+// Residual addition + RMS norm + MX encoding of the output (rmsnorm.hip).
+// `residual` and `sum` are bf16 or, with res_f32, float; optional pointers may
+// be null.  format: kMxNone (no codes), kMxFp4, kMxFp8 as in w4a4_mx_format;
+// H % 8 == 0 (% 32 with a format), H <= 8192.
+struct NormFwdArgs {
+  int64_t T;
+  int H;
+  float eps;
+  const uint16_t* x;
+  int64_t x_stride;
+  const void* residual;
+  const void* gamma;
+  bool gamma_f32;
+  void* sum;
+  uint16_t* y;
+  uint8_t* codes;
+  uint8_t* scales;
+  float* rstd;
+  int32_t* offsets;
+};
+bool launch_add_rmsnorm(const NormFwdArgs& a, bool res_f32, int format, hipStream_t s);
+
+// Its backward.  part: norm_bwd_blocks(T, H) rows of H floats of scratch, or
+// null where dgamma is.
+struct NormBwdArgs {
+  int64_t T;
+  int H;
+  const uint16_t* dy;
+  const void* sum;
+  const void* gamma;
+  bool gamma_f32;
+  const float* rstd;
+  const void* dsum;
+  void* dres;
+  uint16_t* dx;
+  float* part;
+};
+int norm_bwd_blocks(int64_t T, int H);
+bool launch_add_rmsnorm_bwd(const NormBwdArgs& a, bool res_f32, float* dgamma, hipStream_t s);
+
+// MXFP4 / MXFP8 of T bf16 rows of K elements (K % 32 == 0), x_stride elements apart.
+bool launch_mx_quantize_rows(const uint16_t* x, int64_t x_stride, int64_t T, int K, int format, uint8_t* codes,
+                             uint8_t* scales, int32_t* offsets, hipStream_t s);
+
+// y[t, n] = bf16(sum_k x w), x MXFP8 or MXFP4, w MXFP4 (mx_linear.hip).
+// K % 128 == 0, N % 8 == 0, y rows y_stride elements apart.
+bool launch_mx_linear(int64_t T, int K, int N, bool x_fp8, const uint8_t* x, const uint8_t* xs, const uint8_t* w,
+                      const uint8_t* ws, uint16_t* y, int64_t y_stride, hipStream_t s);
+
 // dX gather-sum: dX[t] = bf16(sum_j dXp[row_map[t,j]]).
 bool launch_gather_sum(int64_t T, int H, int k, const uint16_t* dXp, const int32_t* row_map,
                        uint16_t* dx, hipStream_t s);

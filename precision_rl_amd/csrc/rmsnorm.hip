@@ -1,0 +1,461 @@
+// The layer's pre-norm on gfx950: residual addition, RMS norm and the MX
+// encoding of its output in one pass, its backward, and the MX encoding of
+// bf16 rows alone.
+//
+//   s = rnd(x + r);  rstd = (mean_h s^2 + eps)^-1/2;  y = bf16(s rstd gamma);
+//   codes, scales = MX(y)
+//   n = s rstd;  dres = rstd (dy gamma - n mean_h(dy gamma n)) + dsum;
+//   dgamma = sum_t dy n
+//
+// The codes are those of the bf16 y (not of the FP32 product), so that the
+// fused call gives the bytes of the norm followed by the quantiser and the
+// straight-through backward sees the operand that was quantised.  Sums,
+// products and rstd are FP32.  All calls are bound by HBM: every tensor is
+// read or written once.
+
+#include <algorithm>
+
+#include "internal.h"
+#include "mx_encode.h"
+
+namespace w4a4 {
+namespace {
+
+typedef float floatx4_t __attribute__((ext_vector_type(4)));
+
+constexpr int kNormThreads = 256;
+constexpr int kBwdThreads = 512;
+
+// 8 consecutive elements as floats.
+template <typename T>
+struct Vec8;
+template <>
+struct Vec8<uint16_t> {   // bf16
+  u32x4_t w;
+  __device__ __forceinline__ void load(const uint16_t* p) {
+    w = *reinterpret_cast<const u32x4_t*>(p);
+  }
+  __device__ __forceinline__ float get(int i) const {
+    return __uint_as_float((i & 1) ? (w[i >> 1] & 0xFFFF0000u) : (w[i >> 1] << 16));
+  }
+  __device__ __forceinline__ void zero() { w = u32x4_t{0u, 0u, 0u, 0u}; }
+  // values rounded to bf16
+  __device__ __forceinline__ void put(const float (&v)[8]) {
+#pragma unroll
+    for (int d = 0; d < 4; ++d) w[d] = pack_bf16x2(v[2 * d], v[2 * d + 1]);
+  }
+  __device__ __forceinline__ void store(uint16_t* p) const { *reinterpret_cast<u32x4_t*>(p) = w; }
+};
+template <>
+struct Vec8<float> {
+  floatx4_t w[2];
+  __device__ __forceinline__ void load(const float* p) {
+    w[0] = reinterpret_cast<const floatx4_t*>(p)[0];
+    w[1] = reinterpret_cast<const floatx4_t*>(p)[1];
+  }
+  __device__ __forceinline__ float get(int i) const { return w[i >> 2][i & 3]; }
+  __device__ __forceinline__ void zero() { w[0] = w[1] = floatx4_t{0.0f, 0.0f, 0.0f, 0.0f}; }
+  __device__ __forceinline__ void put(const float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i >> 2][i & 3] = v[i];
+  }
+  __device__ __forceinline__ void store(float* p) const {
+    reinterpret_cast<floatx4_t*>(p)[0] = w[0];
+    reinterpret_cast<floatx4_t*>(p)[1] = w[1];
+  }
+};
+
+// Sum over the TEAM lanes of a row, the same in each of them, in an order
+// that depends on TEAM alone.  TEAM > 64: the waves' sums meet in LDS, in one
+// of two sets of slots taken in turn, so that one barrier per sum is enough (a
+// wave can be at most one sum ahead of a wave that still reads).
+template <int TEAM>
+__device__ __forceinline__ float team_sum(float v, float* slots, int& turn) {
+  constexpr int kLanes = TEAM < kWave ? TEAM : kWave;
+#pragma unroll
+  for (int off = kLanes / 2; off > 0; off >>= 1) v += __shfl_xor(v, off, kWave);
+  if constexpr (TEAM > kWave) {
+    constexpr int kWaves = TEAM / kWave;
+    const int wave = threadIdx.x / kWave, first = wave / kWaves * kWaves;
+    float* mine = slots + turn * (kBwdThreads / kWave);
+    turn ^= 1;
+    if (threadIdx.x % kWave == 0) mine[wave] = v;
+    __syncthreads();
+    v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) v += mine[first + w];
+  }
+  return v;
+}
+
+template <int P>
+__device__ __forceinline__ void load_gamma(float (&g)[P][8], const void* gamma, bool gamma_f32, int lane, int team,
+                                           int chunks) {
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    const int c = lane + p * team;
+    if (c >= chunks) continue;
+    if (gamma_f32) {
+      Vec8<float> v;
+      v.load(static_cast<const float*>(gamma) + c * 8);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) g[p][i] = v.get(i);
+    } else {
+      Vec8<uint16_t> v;
+      v.load(static_cast<const uint16_t*>(gamma) + c * 8);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) g[p][i] = v.get(i);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ forward
+// TEAM lanes per row, lane l the 8-element chunks l, l + TEAM, ... (P of
+// them): the row stays in registers between the sum of squares and the
+// output.  Teams stride over the rows; gamma is loaded once per team.
+template <int TEAM, int P, typename RES, int FMT>
+__global__ void __launch_bounds__(kNormThreads)
+norm_fwd_kernel(NormFwdArgs a) {
+  __shared__ float slots[2 * (kBwdThreads / kWave)];
+  int turn = 0;
+  const int lane = threadIdx.x % TEAM, chunks = a.H / 8;
+  constexpr int kTeams = kNormThreads / TEAM;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kTeams;
+  const RES* residual = static_cast<const RES*>(a.residual);
+  RES* sum = static_cast<RES*>(a.sum);
+  float g[P][8];
+  load_gamma<P>(g, a.gamma, a.gamma_f32, lane, TEAM, chunks);
+  if (a.offsets != nullptr && blockIdx.x == 0 && threadIdx.x < 2)
+    a.offsets[threadIdx.x] = threadIdx.x == 0 ? 0 : static_cast<int32_t>(a.T);
+
+  // TEAM > 64 has a barrier in its sum: one team per workgroup, whose waves
+  // run the same iterations
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kTeams + threadIdx.x / TEAM; t < a.T; t += step) {
+    Vec8<RES> s[P];
+    float ss = 0.0f;
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const int c = lane + p * TEAM;
+      s[p].zero();
+      if (c < chunks) {
+        Vec8<uint16_t> x;
+        x.load(a.x + t * a.x_stride + c * 8);
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = x.get(i);
+        if (residual != nullptr) {
+          Vec8<RES> r;
+          r.load(residual + t * a.H + c * 8);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] += r.get(i);
+        }
+        s[p].put(v);
+      }
+    }
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const int c = lane + p * TEAM;
+      if (sum != nullptr && c < chunks) s[p].store(sum + t * a.H + c * 8);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss = fmaf(s[p].get(i), s[p].get(i), ss);
+    }
+    ss = team_sum<TEAM>(ss, slots, turn);
+    float rstd = 1.0f / sqrtf(ss / static_cast<float>(a.H) + a.eps);
+    if (!(ss <= 3.4028235e38f)) {
+      // the squares overflow FP32 (values above about 1e19, an infinity or a
+      // NaN; the same in every lane of the row): on values scaled by 2^-80,
+      // beside which eps vanishes
+      float sc = 0.0f;
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float v = s[p].get(i) * 0x1p-80f;
+          sc = fmaf(v, v, sc);
+        }
+      sc = team_sum<TEAM>(sc, slots, turn);
+      rstd = 0x1p-80f / sqrtf(sc / static_cast<float>(a.H));
+    }
+    if (a.rstd != nullptr && lane == 0) a.rstd[t] = rstd;
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const int c = lane + p * TEAM;
+      if (c >= chunks) continue;
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = s[p].get(i) * rstd * g[p][i];
+      Vec8<uint16_t> y;
+      y.put(v);
+      if (a.y != nullptr) y.store(a.y + t * a.H + c * 8);
+      if constexpr (FMT != kMxNone) {   // H % 32 == 0: a quad's lanes are all here or all past the row
+        uint32_t code[2];
+        const uint32_t byte = mx_encode8<FMT>(y.w, code);
+        mx_store8<FMT>(a.codes, a.scales, t * chunks + c, code, byte);
+      }
+    }
+  }
+}
+
+// ----------------------------------------------------------------- backward
+// As the forward, 512 threads; DG: each lane sums dy n of its columns over
+// its rows in FP32, the workgroup's teams add theirs in LDS in team order and
+// write one row of `part`, which dgamma_kernel adds in workgroup order.
+template <int TEAM, int P, typename RES, bool DG>
+__global__ void __launch_bounds__(kBwdThreads)
+norm_bwd_kernel(NormBwdArgs a) {
+  extern __shared__ __attribute__((aligned(16))) float dg_lds[];   // DG: [teams][H]
+  __shared__ float slots[2 * (kBwdThreads / kWave)];
+  int turn = 0;
+  const int lane = threadIdx.x % TEAM, team = threadIdx.x / TEAM, chunks = a.H / 8;
+  constexpr int kTeams = kBwdThreads / TEAM;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kTeams;
+  const RES* s_in = static_cast<const RES*>(a.sum);
+  const RES* dsum = static_cast<const RES*>(a.dsum);
+  RES* dres = static_cast<RES*>(a.dres);
+  float g[P][8], dg[P][8];
+  load_gamma<P>(g, a.gamma, a.gamma_f32, lane, TEAM, chunks);
+#pragma unroll
+  for (int p = 0; p < P; ++p)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dg[p][i] = 0.0f;
+
+  // TEAM > 64 has a barrier in its sum: every team of the workgroup runs the
+  // same iterations, those past the last row without loads or stores
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTeams;
+  for (int64_t tb = t0; tb < a.T; tb += step) {
+    const int64_t t = tb + team;
+    const bool live = t < a.T;
+    const float rstd = live ? a.rstd[t] : 0.0f;
+    Vec8<RES> s[P], ds[P];
+    Vec8<uint16_t> dy[P];
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const int c = lane + p * TEAM;
+      s[p].zero();
+      ds[p].zero();
+      dy[p].zero();
+      if (live && c < chunks) {
+        dy[p].load(a.dy + t * a.H + c * 8);
+        s[p].load(s_in + t * a.H + c * 8);
+        if (dsum != nullptr) ds[p].load(dsum + t * a.H + c * 8);
+      }
+    }
+    float inner = 0.0f;
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      if (lane + p * TEAM >= chunks) continue;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float n = s[p].get(i) * rstd, d = dy[p].get(i);
+        inner = fmaf(d * g[p][i], n, inner);
+        if constexpr (DG) dg[p][i] = fmaf(d, n, dg[p][i]);
+      }
+    }
+    inner = team_sum<TEAM>(inner, slots, turn) / static_cast<float>(a.H);
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const int c = lane + p * TEAM;
+      if (!live || c >= chunks) continue;
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float n = s[p].get(i) * rstd;
+        v[i] = fmaf(rstd, dy[p].get(i) * g[p][i] - n * inner, ds[p].get(i));
+      }
+      Vec8<RES> o;
+      o.put(v);
+      o.store(dres + t * a.H + c * 8);
+      if (a.dx != nullptr) {
+        Vec8<uint16_t> ox;
+        ox.put(v);
+        ox.store(a.dx + t * a.H + c * 8);
+      }
+    }
+  }
+  if constexpr (DG) {
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const int c = lane + p * TEAM;
+      if (c >= chunks) continue;
+      floatx4_t* d = reinterpret_cast<floatx4_t*>(dg_lds + team * a.H + c * 8);
+      d[0] = floatx4_t{dg[p][0], dg[p][1], dg[p][2], dg[p][3]};
+      d[1] = floatx4_t{dg[p][4], dg[p][5], dg[p][6], dg[p][7]};
+    }
+    __syncthreads();
+    float* out = a.part + static_cast<int64_t>(blockIdx.x) * a.H;
+    for (int h = threadIdx.x; h < a.H; h += kBwdThreads) {
+      float v = dg_lds[h];
+#pragma unroll
+      for (int w = 1; w < kTeams; ++w) v += dg_lds[w * a.H + h];
+      out[h] = v;
+    }
+  }
+}
+
+// dgamma[h] = sum of the G partial rows, wave w of a workgroup rows w, w +
+// 16, ... of 64 columns, the waves' sums added in wave order.
+constexpr int kDgThreads = 1024;
+__global__ void __launch_bounds__(kDgThreads)
+dgamma_kernel(const float* __restrict__ part, int G, int H, float* __restrict__ dgamma) {
+  __shared__ float sums[kDgThreads];
+  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  const int h = blockIdx.x * kWave + lane;
+  float v = 0.0f;
+  if (h < H) {
+#pragma unroll 8
+    for (int r = wave; r < G; r += kDgThreads / kWave) v += part[static_cast<int64_t>(r) * H + h];
+  }
+  sums[threadIdx.x] = v;
+  __syncthreads();
+  if (wave == 0 && h < H) {
+#pragma unroll
+    for (int w = 1; w < kDgThreads / kWave; ++w) v += sums[w * kWave + lane];
+    dgamma[h] = v;
+  }
+}
+
+__global__ void __launch_bounds__(kNormThreads)
+zero_f32_kernel(float* p, int n) {
+  const int i = blockIdx.x * kNormThreads + threadIdx.x;
+  if (i < n) p[i] = 0.0f;
+}
+
+// ------------------------------------------------------------ MX quantiser
+// Output chunks are flat (K % 32 == 0: the code and scale index of a chunk
+// does not depend on the row length); the input position moves by a fixed
+// (rows, columns) step per iteration.
+template <int FMT>
+__global__ void __launch_bounds__(kNormThreads)
+quantize_rows_kernel(const uint16_t* __restrict__ x, int64_t x_stride, int64_t total, int chunks, int64_t step_rows,
+                     int step_cols, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, int32_t* offsets,
+                     int64_t T) {
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kNormThreads;
+  int64_t i = static_cast<int64_t>(blockIdx.x) * kNormThreads + threadIdx.x;
+  if (offsets != nullptr && i < 2) offsets[i] = i == 0 ? 0 : static_cast<int32_t>(T);
+  int64_t row = i / chunks;
+  int col = static_cast<int>(i - row * chunks);
+  for (; i < total; i += step) {   // total % 4 == 0: the lanes of a quad leave together
+    const u32x4_t v = *reinterpret_cast<const u32x4_t*>(x + row * x_stride + col * 8);
+    uint32_t code[2];
+    const uint32_t byte = mx_encode8<FMT>(v, code);
+    mx_store8<FMT>(codes, scales, i, code, byte);
+    row += step_rows;
+    col += step_cols;
+    if (col >= chunks) {
+      col -= chunks;
+      ++row;
+    }
+  }
+}
+
+template <int TEAM, int P, typename RES, int FMT>
+void launch_fwd_variant(const NormFwdArgs& a, hipStream_t s) {
+  constexpr int kTeams = kNormThreads / TEAM;
+  const int64_t need = (a.T + kTeams - 1) / kTeams;
+  const int64_t most = static_cast<int64_t>(device_cu_count()) * 8;
+  launch_kernel("add_rmsnorm", norm_fwd_kernel<TEAM, P, RES, FMT>,
+                dim3(static_cast<unsigned>(std::max<int64_t>(1, std::min(need, most)))), dim3(kNormThreads), 0, s, a);
+}
+
+template <int TEAM, int P>
+void launch_fwd_shape(const NormFwdArgs& a, bool res_f32, int format, hipStream_t s) {
+  auto fmt = [&](auto res) {
+    using RES = decltype(res);
+    if (format == kMxFp8) launch_fwd_variant<TEAM, P, RES, kMxFp8>(a, s);
+    else if (format == kMxFp4) launch_fwd_variant<TEAM, P, RES, kMxFp4>(a, s);
+    else launch_fwd_variant<TEAM, P, RES, kMxNone>(a, s);
+  };
+  if (res_f32) fmt(float{});
+  else fmt(uint16_t{});
+}
+
+template <int TEAM, int P, typename RES, bool DG>
+bool launch_bwd_variant(const NormBwdArgs& a, int blocks, hipStream_t s) {
+  const uint32_t lds = DG ? static_cast<uint32_t>(kBwdThreads / TEAM) * a.H * 4u : 0u;
+  if constexpr (DG) {
+    static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&norm_bwd_kernel<TEAM, P, RES, DG>),
+                                                       hipFuncAttributeMaxDynamicSharedMemorySize,
+                                                       kBwdThreads * P * 32);
+    if (attr != hipSuccess) return launch_ok("add_rmsnorm_bwd") && false;
+  }
+  launch_kernel("add_rmsnorm_bwd", norm_bwd_kernel<TEAM, P, RES, DG>, dim3(static_cast<unsigned>(blocks)),
+                dim3(kBwdThreads), lds, s, a);
+  return true;
+}
+
+template <int TEAM, int P>
+bool launch_bwd_shape(const NormBwdArgs& a, bool res_f32, int blocks, hipStream_t s) {
+  if (res_f32)
+    return a.part ? launch_bwd_variant<TEAM, P, float, true>(a, blocks, s)
+                  : launch_bwd_variant<TEAM, P, float, false>(a, blocks, s);
+  return a.part ? launch_bwd_variant<TEAM, P, uint16_t, true>(a, blocks, s)
+                : launch_bwd_variant<TEAM, P, uint16_t, false>(a, blocks, s);
+}
+
+// Lanes per row: a row's chunks fit its team's registers (P <= 4), and short
+// rows share a wave.
+int norm_team(int H) { return H <= 256 ? 16 : H <= 2048 ? 64 : 256; }
+
+}  // namespace
+
+int norm_bwd_blocks(int64_t T, int H) {
+  const int teams = kBwdThreads / norm_team(H);
+  const int64_t need = (T + teams - 1) / teams;
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(need, 512)));
+}
+
+bool launch_add_rmsnorm(const NormFwdArgs& a, bool res_f32, int format, hipStream_t s) {
+  const int H = a.H;
+  if (H <= 128) launch_fwd_shape<16, 1>(a, res_f32, format, s);
+  else if (H <= 256) launch_fwd_shape<16, 2>(a, res_f32, format, s);
+  else if (H <= 512) launch_fwd_shape<64, 1>(a, res_f32, format, s);
+  else if (H <= 1024) launch_fwd_shape<64, 2>(a, res_f32, format, s);
+  else if (H <= 2048) launch_fwd_shape<64, 4>(a, res_f32, format, s);
+  else if (H <= 4096) launch_fwd_shape<256, 2>(a, res_f32, format, s);
+  else if (H <= 8192) launch_fwd_shape<256, 4>(a, res_f32, format, s);
+  else return false;
+  return launch_ok("add_rmsnorm");
+}
+
+bool launch_add_rmsnorm_bwd(const NormBwdArgs& a, bool res_f32, float* dgamma, hipStream_t s) {
+  const int H = a.H;
+  if (a.T == 0) {
+    if (dgamma == nullptr) return true;
+    launch_kernel("add_rmsnorm_dgamma", zero_f32_kernel, dim3((H + kNormThreads - 1) / kNormThreads),
+                  dim3(kNormThreads), 0, s, dgamma, H);
+    return launch_ok("add_rmsnorm_dgamma");
+  }
+  const int blocks = norm_bwd_blocks(a.T, H);
+  bool ok = false;
+  if (H <= 128) ok = launch_bwd_shape<16, 1>(a, res_f32, blocks, s);
+  else if (H <= 256) ok = launch_bwd_shape<16, 2>(a, res_f32, blocks, s);
+  else if (H <= 512) ok = launch_bwd_shape<64, 1>(a, res_f32, blocks, s);
+  else if (H <= 1024) ok = launch_bwd_shape<64, 2>(a, res_f32, blocks, s);
+  else if (H <= 2048) ok = launch_bwd_shape<64, 4>(a, res_f32, blocks, s);
+  else if (H <= 4096) ok = launch_bwd_shape<256, 2>(a, res_f32, blocks, s);
+  else if (H <= 8192) ok = launch_bwd_shape<256, 4>(a, res_f32, blocks, s);
+  if (!ok || !launch_ok("add_rmsnorm_bwd")) return false;
+  if (dgamma == nullptr) return true;
+  launch_kernel("add_rmsnorm_dgamma", dgamma_kernel, dim3((H + kWave - 1) / kWave), dim3(kDgThreads), 0, s,
+                static_cast<const float*>(a.part), blocks, H, dgamma);
+  return launch_ok("add_rmsnorm_dgamma");
+}
+
+bool launch_mx_quantize_rows(const uint16_t* x, int64_t x_stride, int64_t T, int K, int format, uint8_t* codes,
+                             uint8_t* scales, int32_t* offsets, hipStream_t s) {
+  const int chunks = K / 8;
+  const int64_t total = T * chunks;
+  const int64_t need = (total + kNormThreads - 1) / kNormThreads;
+  const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>(need, static_cast<int64_t>(device_cu_count()) * 16));
+  const int64_t step = blocks * kNormThreads;
+  const dim3 grid(static_cast<unsigned>(blocks));
+  if (format == kMxFp8)
+    launch_kernel("mx_quantize_rows", quantize_rows_kernel<kMxFp8>, grid, dim3(kNormThreads), 0, s, x, x_stride,
+                  total, chunks, step / chunks, static_cast<int>(step % chunks), codes, scales, offsets, T);
+  else
+    launch_kernel("mx_quantize_rows", quantize_rows_kernel<kMxFp4>, grid, dim3(kNormThreads), 0, s, x, x_stride,
+                  total, chunks, step / chunks, static_cast<int>(step % chunks), codes, scales, offsets, T);
+  return launch_ok("mx_quantize_rows");
+}
+
+}  // namespace w4a4

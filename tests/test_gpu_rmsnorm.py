@@ -1,0 +1,264 @@
+"""GPU parity of the pre-norm (residual addition, RMS norm, MX encoding), its
+backward and the MX row quantiser.
+
+The sum is compared bit for bit with the rounded FP32 sum, the codes and scale
+bytes with the oracle's encoding of the GPU's own bf16 y.  Bounds of the rest,
+with u = 2^-24 and bf16 results off by at most half a step (2^-8):
+  rstd    a lane adds at most 32 squares, a tree of at most 6 + 4 steps joins
+          the lanes; then division, addition, square root, reciprocal:
+          (42 + 4) u / 2 through the square root, below 32 u.
+  y       rstd's bound and two products: 34 u, and the rounding.
+  dres    every product and sum a rounding; the inner mean's error is bounded
+          by its terms' magnitudes (at most 32 + 10 additions, 3 roundings a term).
+  dgamma  as many additions as rows a lane takes plus the joins; 2 roundings a term.
+"""
+import numpy as np
+import pytest
+
+from oracle import mxfp4, nvfp4 as q, rmsnorm
+from gpu_util import bf16_host, u8, print_case
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+U = 2.0 ** -24
+STEP = torch.finfo(torch.bfloat16).eps / 2
+TINY = 2.0 ** -126
+
+
+@pytest.fixture(scope="module")
+def b():
+    from precision_rl_amd import binding
+    return binding
+
+
+def _dev(v, dtype):
+    return torch.from_numpy(np.asarray(v, dtype=np.float32)).to(dtype).cuda()
+
+
+def _f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def _inputs(T, H, res, gdt, seed):
+    rng = np.random.default_rng(seed)
+    x = _dev(rng.standard_normal((T, H)), torch.bfloat16)
+    r = None if res is None else _dev(3 * rng.standard_normal((T, H)) * np.exp(rng.standard_normal(H)), res)
+    return x, r, _dev(1 + 0.3 * rng.standard_normal(H), gdt)
+
+
+def _check_codes(b, y, codes, scales, fmt):
+    """The encoding of the bf16 rows y, byte for byte."""
+    v = bf16_host(y)
+    if fmt == b.MX_FP8:
+        vals, sc = mxfp4.quantize_rows_mx8(v)
+        ref = mxfp4.e4m3_bytes(vals)
+    else:
+        c, sc = mxfp4.quantize_rows_mx(v)
+        ref = q.pack_codes(c)
+    assert np.array_equal(u8(scales), sc)
+    assert np.array_equal(u8(codes), ref)
+
+
+def _check_norm(b, x, r, gamma, eps, out, fmt):
+    s = x if r is None else (x.float() + r.float()).to(r.dtype)
+    if "sum" in out:
+        assert torch.equal(out["sum"], s.to(out["sum"].dtype))
+    y64, r64 = rmsnorm.forward(_f64(s), _f64(gamma), eps)
+    if "rstd" in out:
+        assert np.all(np.abs(_f64(out["rstd"]) - r64) <= 32 * U * r64)
+    assert np.all(np.abs(bf16_host(out["y"]) - y64) <= (STEP + 34 * U) * np.abs(y64) + TINY)
+    if fmt is not None:
+        _check_codes(b, out["y"], out["codes"], out["scales"], fmt)
+
+
+# every team shape and its edges (rows of 16, 64 and 256 lanes, 1 to 4 chunks
+# a lane), one row, fewer rows than a workgroup, rows in several rounds
+@pytest.mark.parametrize("T,H", [(1, 32), (5, 96), (3, 128), (131, 160), (7, 256), (2, 288), (9, 512), (4, 1024),
+                                 (1, 2048), (33, 2048), (5, 2080), (3, 4096), (2, 4128), (3, 8192), (9000, 64)])
+@pytest.mark.parametrize("res,fmt", [("bf16", "fp8"), ("f32", "fp4"), (None, "fp4"), ("f32", None)])
+def test_norm_forward(b, T, H, res, fmt):
+    rt = {"bf16": torch.bfloat16, "f32": torch.float32, None: None}[res]
+    f = {"fp8": b.MX_FP8, "fp4": b.MX_FP4, None: None}[fmt]
+    x, r, g = _inputs(T, H, rt, torch.bfloat16 if T % 2 else torch.float32, 10 * T + H)
+    print_case("norm_forward", T=T, H=H, res=res, fmt=fmt)
+    out = b.w4a4_add_rmsnorm_fwd(x, g, 1e-6, residual=r, fmt=f, save=True)
+    _check_norm(b, x, r, g, 1e-6, out, f)
+
+
+@pytest.mark.parametrize("H", [8, 24, 136, 1000, 2056, 8184])
+def test_norm_without_codes_takes_rows_of_eight(b, H):
+    x, r, g = _inputs(6, H, torch.bfloat16, torch.float32, H)
+    print_case("norm_rows_of_eight", H=H)
+    out = b.w4a4_add_rmsnorm_fwd(x, g, 1e-5, residual=r, save=True)
+    _check_norm(b, x, r, g, 1e-5, out, None)
+
+
+def test_norm_in_place_slices_and_rows_behind(b):
+    """The sum over the residual, x a column slice, and nothing written past the
+    last row."""
+    T, H, behind = 21, 512, 5
+    x, r, g = _inputs(T, H, torch.bfloat16, torch.bfloat16, 3)
+    wide = torch.zeros(T, H + 264, dtype=torch.bfloat16, device="cuda")
+    wide[:, 256:256 + H] = x
+    big = {n: torch.full((T + behind, w), 77, dtype=t, device="cuda")
+           for n, w, t in (("codes", H, torch.uint8), ("scales", H // 32, torch.uint8), ("y", H, torch.bfloat16))}
+    rs = torch.full((T + behind,), 77.0, device="cuda")
+    stream = torch.cat([r, torch.full((behind, H), 77.0, dtype=r.dtype, device="cuda")])
+    off = torch.zeros(2, dtype=torch.int32, device="cuda")
+    print_case("norm_in_place")
+    out = b.w4a4_add_rmsnorm_fwd(wide[:, 256:256 + H], g, 1e-6, residual=stream[:T], fmt=b.MX_FP8, save=True,
+                                 out=dict({n: v[:T] for n, v in big.items()}, rstd=rs[:T], sum=stream[:T], offsets=off))
+    _check_norm(b, x, r, g, 1e-6, out, b.MX_FP8)
+    assert off.tolist() == [0, T]
+    for v in (*big.values(), rs, stream):
+        assert bool((v[T:] == 77).all())
+
+
+def test_norm_extreme_rows(b):
+    """Squares beyond FP32, an infinity, a NaN, a zero row, tiny rows; each row
+    as it would be alone."""
+    H = 2048
+    rng = np.random.default_rng(5)
+    base = rng.standard_normal((7, H))
+    rows = np.stack([base[0] * 1e25, base[1] * 3e37 / np.abs(base[1]).max(), base[2], base[3], np.zeros(H),
+                     base[5] * 1e-30, base[6]])
+    rows[2, 5], rows[3, 9] = np.inf, np.nan
+    x, g = _dev(rows, torch.bfloat16), torch.ones(H, device="cuda")
+    print_case("norm_extreme")
+    out = b.w4a4_add_rmsnorm_fwd(x, g, 1e-6, fmt=b.MX_FP8, save=True)
+    y, v = bf16_host(out["y"]), bf16_host(x)
+    for t in (0, 1, 4, 5, 6):
+        y64, r64 = rmsnorm.forward(v[t:t + 1], np.ones(H), 1e-6)
+        assert abs(_f64(out["rstd"])[t] - r64[0]) <= 32 * U * r64[0]
+        assert np.all(np.abs(y[t] - y64[0]) <= (STEP + 34 * U) * np.abs(y64[0]) + TINY)
+        one = b.w4a4_add_rmsnorm_fwd(x[t:t + 1], g, 1e-6, fmt=b.MX_FP8, save=True)
+        for n in ("y", "codes", "scales", "rstd"):
+            assert torch.equal(one[n][0], out[n][t]), (t, n)
+    assert np.isnan(y[2, 5]) and not y[2, :5].any() and np.isnan(y[3]).all()
+    # an infinity's block and every block of the NaN row: scale 255, codes 0; the
+    # infinite row's other elements are zeros, which keep their signs (0x80)
+    s, c = u8(out["scales"]), u8(out["codes"])
+    assert s[2, 0] == 255 and (s[2, 1:] == 0).all() and not c[2, :32].any() and not (c[2] & 0x7F).any()
+    assert (s[3] == 255).all() and not c[3].any()
+    _check_codes(b, out["y"][[0, 1, 4, 5, 6]], out["codes"][[0, 1, 4, 5, 6]], out["scales"][[0, 1, 4, 5, 6]], b.MX_FP8)
+
+
+@pytest.mark.parametrize("T,H", [(1, 32), (5, 96), (3, 128), (131, 256), (2, 288), (9, 512), (4, 1000), (1, 2048),
+                                 (61, 2048), (5, 2080), (3, 4096), (2, 8192), (5000, 64), (9000, 160)])
+@pytest.mark.parametrize("res", ["bf16", "f32"])
+def test_norm_backward(b, T, H, res):
+    rt = torch.bfloat16 if res == "bf16" else torch.float32
+    rng = np.random.default_rng(T + H)
+    s = _dev(2 * rng.standard_normal((T, H)), rt)
+    g = _dev(1 + 0.3 * rng.standard_normal(H), torch.float32 if T % 2 else torch.bfloat16)
+    dy = _dev(rng.standard_normal((T, H)), torch.bfloat16)
+    ds = _dev(rng.standard_normal((T, H)), rt) if H != 512 else None
+    r = torch.from_numpy(rmsnorm.rstd(_f64(s), 1e-6).astype(np.float32)).cuda()
+    print_case("norm_backward", T=T, H=H, res=res)
+    dx = torch.empty(T, H, dtype=torch.bfloat16, device="cuda")
+    out = b.w4a4_add_rmsnorm_bwd(dy, s, g, r, dsum=ds, out=dict(dx=dx))
+    s64, g64, dy64, r64 = _f64(s), _f64(g), _f64(dy), _f64(r)
+    ds64 = None if ds is None else _f64(ds)
+    want, wantg = rmsnorm.backward(dy64, s64, g64, r64, ds64)
+    n = s64 * r64[:, None]
+    d = np.abs(dy64 * g64)
+    mean_abs = np.mean(d * np.abs(n), axis=1, keepdims=True)
+    c = np.abs(np.mean(dy64 * g64 * n, axis=1, keepdims=True))
+    # d g: 1, n: 1, n c: 1 more and c's own error; difference, product with rstd, dsum: 1 each
+    calc = U * r64[:, None] * (4 * d + np.abs(n) * (6 * c + (42 + 4) * mean_abs)) + U * np.abs(want)
+    half = STEP if res == "bf16" else U
+    assert np.all(np.abs(_f64(out["dres"]) - want) <= calc * (1 + half) + half * np.abs(want) + TINY)
+    assert np.all(np.abs(bf16_host(dx) - want) <= calc * (1 + STEP) + STEP * np.abs(want) + TINY)
+    blocks = b.workspace_size(b.WS_RMSNORM_BACKWARD, T, H, 0, 1, 1) // (4 * H) + 1
+    adds = -(-T // blocks) + 32 + blocks // 16 + 1 + 16 + 3
+    assert np.all(np.abs(_f64(out["dgamma"]) - wantg) <= adds * U * np.sum(np.abs(dy64 * n), axis=0) + TINY)
+
+
+def test_norm_backward_in_place_without_dgamma_and_empty(b):
+    T, H = 19, 256
+    rng = np.random.default_rng(8)
+    s, dy, ds = (_dev(rng.standard_normal((T, H)), torch.bfloat16) for _ in range(3))
+    g, r = torch.ones(H, device="cuda"), torch.rand(T, device="cuda") + 0.5
+    print_case("norm_backward_in_place")
+    ref = b.w4a4_add_rmsnorm_bwd(dy, s, g, r, dsum=ds)
+    again = b.w4a4_add_rmsnorm_bwd(dy, s, g, r, dsum=ds)
+    assert torch.equal(ref["dres"], again["dres"]) and torch.equal(ref["dgamma"], again["dgamma"])
+    over = ds.clone()
+    got = b.w4a4_add_rmsnorm_bwd(dy, s, g, r, dsum=over, dgamma=False, out=dict(dres=over))
+    assert "dgamma" not in got and torch.equal(over, ref["dres"])
+    over = dy.clone()
+    b.w4a4_add_rmsnorm_bwd(over, s, g, r, dsum=ds, out=dict(dres=over))
+    assert torch.equal(over, ref["dres"])
+    none = b.w4a4_add_rmsnorm_bwd(dy[:0], s[:0], g, r[:0], out=dict(dgamma=torch.full((H,), 7.0, device="cuda")))
+    assert none["dres"].shape == (0, H) and not none["dgamma"].any()
+
+
+# ------------------------------------------------------------- MX quantiser
+def _edge_rows():
+    """Rows of 64: ties and their neighbours at several exponents, zeros of both
+    signs, subnormals, the largest values."""
+    rng = np.random.default_rng(0)
+    ties = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 5.5, 7.5, -0.25, -1.25, 6.0, 7.0, 0.0, -0.0, 4.0])
+    rows = []
+    for e in (-120, -20, 0, 30, 120):
+        row = np.concatenate([ties * 2.0 ** e, rng.standard_normal(48) * 2.0 ** e])
+        rows.append(row)
+    rows.append(np.full(64, -0.0))
+    rows.append(np.where(np.arange(64) % 2, 2.0 ** -133, -(2.0 ** -130)))
+    rows.append(np.where(np.arange(64) < 32, 3.3e38, 1e-38))
+    rows.append(448.0 * (1 + np.arange(64) / 512.0))
+    rows.append(np.linspace(-260, 260, 64))
+    return np.array(rows)
+
+
+@pytest.mark.parametrize("fmt", ["fp4", "fp8"])
+def test_quantize_rows_edges(b, fmt):
+    x = _dev(_edge_rows(), torch.bfloat16)
+    print_case("quantize_rows_edges", fmt=fmt)
+    f = b.MX_FP8 if fmt == "fp8" else b.MX_FP4
+    out = b.w4a4_mx_quantize_rows(x, f)
+    _check_codes(b, x, out["codes"], out["scales"], f)
+
+
+@pytest.mark.parametrize("T,K,pad", [(1, 32, 0), (3, 96, 8), (37, 768, 0), (65, 1056, 24), (300, 4096, 1024),
+                                     (2, 16384, 0), (4000, 2080, 0)])
+@pytest.mark.parametrize("fmt", ["fp4", "fp8"])
+def test_quantize_rows(b, T, K, pad, fmt):
+    rng = np.random.default_rng(T)
+    wide = _dev(rng.standard_normal((T, K + pad)) * np.exp(2 * rng.standard_normal((T, 1))), torch.bfloat16)
+    x = wide[:, pad:]
+    f = b.MX_FP8 if fmt == "fp8" else b.MX_FP4
+    off = torch.zeros(2, dtype=torch.int32, device="cuda")
+    print_case("quantize_rows", T=T, K=K, pad=pad, fmt=fmt)
+    width = K if fmt == "fp8" else K // 2
+    codes = torch.full((T + 3, width), 9, dtype=torch.uint8, device="cuda")
+    scales = torch.full((T + 3, K // 32), 9, dtype=torch.uint8, device="cuda")
+    out = b.w4a4_mx_quantize_rows(x, f, out=dict(codes=codes[:T], scales=scales[:T], offsets=off))
+    _check_codes(b, x.contiguous(), out["codes"], out["scales"], f)
+    assert off.tolist() == [0, T]
+    assert bool((codes[T:] == 9).all()) and bool((scales[T:] == 9).all())
+
+
+def test_quantize_rows_matches_the_other_mx_quantisers(b):
+    x = _dev(np.random.default_rng(4).standard_t(3, (256, 512)), torch.bfloat16)
+    print_case("quantize_rows_same_bytes")
+    four, perm = b.w4a4_mx_quantize_rows(x, b.MX_FP4), b.w4a4_mx_quantize_permute(x, None, 1)
+    assert torch.equal(four["codes"], perm["codes"]) and torch.equal(four["scales"], perm["scales"])
+    eight, dual = b.w4a4_mx_quantize_rows(x, b.MX_FP8), b.w4a4_mx8_quantize(x)
+    assert torch.equal(eight["codes"], dual["q_rows"]) and torch.equal(eight["scales"], dual["s_rows"])
+
+
+def test_quantize_rows_infinities_nan_and_empty(b):
+    x = torch.ones(2, 96, dtype=torch.bfloat16, device="cuda")
+    x[0, 40], x[1, 0], x[1, 95] = float("inf"), float("nan"), float("-inf")
+    print_case("quantize_rows_nonfinite")
+    for f in (b.MX_FP4, b.MX_FP8):
+        out = b.w4a4_mx_quantize_rows(x, f)
+        sc = u8(out["scales"])
+        assert (sc == 255).tolist() == [[False, True, False], [True, False, True]]
+        c = u8(out["codes"]).reshape(2, 3, -1)
+        assert not c[sc == 255].any() and c[sc != 255].all()
+        off = torch.full((2,), 5, dtype=torch.int32, device="cuda")
+        empty = b.w4a4_mx_quantize_rows(x[:0], f, out=dict(offsets=off))
+        assert empty["codes"].shape[0] == 0 and off.tolist() == [0, 0]
