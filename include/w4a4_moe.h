@@ -452,7 +452,9 @@ w4a4_status w4a4_mx8_quantize(
  * without codes), T >= 0 of any size below 2^31 with T = 0 allowed (tensors
  * of T rows may then be NULL), and never touch rows at or past T.
  * `offsets` (optional, [2] int32 out) receives {0, T}, as w4a4_linear_bwd
- * reads it.
+ * reads it.  Tensors are 16-byte aligned, as everywhere; scales, rstd, dgamma
+ * and offsets only to their element (the product reads scales by 4 bytes), so
+ * that any rows of a batch can be passed alone.
  */
 
 /*

@@ -754,6 +754,14 @@ w4a4_status check_rows(int64_t T, int K, int multiple) {
   if (T > kMaxRows) return fail(W4A4_ERR_UNSUPPORTED, "T=%lld exceeds int32 row indices", static_cast<long long>(T));
   return W4A4_OK;
 }
+// Outputs and inputs that the kernels touch by element, so that the rows of a
+// batch can be passed apart: scales, rstd, gradients of gamma, offsets.
+w4a4_status check_element_ptr(const char* what, const void* p, size_t align, bool required) {
+  if (p == nullptr) return required ? fail(W4A4_ERR_INVALID_ARG, "%s is NULL", what) : W4A4_OK;
+  if (reinterpret_cast<uintptr_t>(p) % align)
+    return fail(W4A4_ERR_INVALID_ARG, "%s is not %zu-byte aligned", what, align);
+  return W4A4_OK;
+}
 w4a4_status check_stride(const char* what, int64_t stride, int64_t width) {
   if (stride < width || stride % 8 || stride > (int64_t{1} << 40))
     return fail(W4A4_ERR_INVALID_ARG, "%s=%lld must be a multiple of 8 and at least the row length %lld", what,
@@ -773,9 +781,9 @@ w4a4_status w4a4_mx_quantize_rows(int64_t T, int K, int format, const void* x, i
   if (T > 0) {
     REQUIRE_PTR(x);
     REQUIRE_PTR(codes);
-    REQUIRE_PTR(scales);
+    if ((st = check_element_ptr("scales", scales, 1, true)) != W4A4_OK) return st;
   }
-  OPTIONAL_PTR(offsets);
+  if ((st = check_element_ptr("offsets", offsets, 4, false)) != W4A4_OK) return st;
   if (T == 0 && offsets == nullptr) return W4A4_OK;
   if (!launch_mx_quantize_rows(static_cast<const uint16_t*>(x), x_stride, T, K, format, codes, scales, offsets,
                                static_cast<hipStream_t>(stream)))
@@ -806,7 +814,7 @@ w4a4_status w4a4_add_rmsnorm_fwd(int64_t T, int H, float eps, const void* x, int
     REQUIRE_PTR(gamma);
     if (format != W4A4_MX_NONE) {
       REQUIRE_PTR(codes);
-      REQUIRE_PTR(scales);
+      if ((st = check_element_ptr("scales", scales, 1, true)) != W4A4_OK) return st;
     }
     if (sum != nullptr && sum == x && (residual_dtype != W4A4_BF16 || x_stride != H))
       return fail(W4A4_ERR_INVALID_ARG, "sum may be x only where x is dense and the residual stream bf16");
@@ -814,8 +822,8 @@ w4a4_status w4a4_add_rmsnorm_fwd(int64_t T, int H, float eps, const void* x, int
   OPTIONAL_PTR(residual);
   OPTIONAL_PTR(sum);
   OPTIONAL_PTR(y);
-  OPTIONAL_PTR(rstd);
-  OPTIONAL_PTR(offsets);
+  if ((st = check_element_ptr("rstd", rstd, 4, false)) != W4A4_OK) return st;
+  if ((st = check_element_ptr("offsets", offsets, 4, false)) != W4A4_OK) return st;
   if (T == 0 && offsets == nullptr) return W4A4_OK;
   const NormFwdArgs a{T, H, eps, static_cast<const uint16_t*>(x), x_stride, residual, T > 0 ? gamma : nullptr,
                       gamma_dtype == W4A4_F32, sum, static_cast<uint16_t*>(y), codes, scales, rstd, offsets};
@@ -838,14 +846,14 @@ w4a4_status w4a4_add_rmsnorm_bwd(int64_t T, int H, const void* dy, const void* s
     REQUIRE_PTR(dy);
     REQUIRE_PTR(sum);
     REQUIRE_PTR(gamma);
-    REQUIRE_PTR(rstd);
+    if ((st = check_element_ptr("rstd", rstd, 4, true)) != W4A4_OK) return st;
     REQUIRE_PTR(dres);
     if (dres == dy && residual_dtype != W4A4_BF16)
       return fail(W4A4_ERR_INVALID_ARG, "dres may be dy only where the residual stream is bf16");
   }
   OPTIONAL_PTR(dsum);
   OPTIONAL_PTR(dx);
-  OPTIONAL_PTR(dgamma);
+  if ((st = check_element_ptr("dgamma", dgamma, 4, false)) != W4A4_OK) return st;
   if (dgamma != nullptr && T > 0) {
     const size_t need = w4a4_workspace_size(W4A4_WS_RMSNORM_BACKWARD, T, H, 0, 1, 1, 1);
     if (workspace == nullptr || workspace_bytes < need)
@@ -874,10 +882,10 @@ w4a4_status w4a4_mx_linear_fwd(int64_t T, int K, int N, int format, const uint8_
   if ((st = check_stride("y_stride", y_stride, N)) != W4A4_OK) return st;
   if (T > 0) {
     REQUIRE_PTR(x_codes);
-    REQUIRE_PTR(x_scales);
     REQUIRE_PTR(w_codes);
-    REQUIRE_PTR(w_scales);
     REQUIRE_PTR(y);
+    if ((st = check_element_ptr("x_scales", x_scales, 4, true)) != W4A4_OK) return st;
+    if ((st = check_element_ptr("w_scales", w_scales, 4, true)) != W4A4_OK) return st;
   }
   if (!launch_mx_linear(T, K, N, format == W4A4_MX_FP8, x_codes, x_scales, w_codes, w_scales,
                         static_cast<uint16_t*>(y), y_stride, static_cast<hipStream_t>(stream)))

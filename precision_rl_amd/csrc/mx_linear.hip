@@ -1,18 +1,18 @@
 // Dense product of MX operands on gfx950: y[t, n] = bf16(sum_k (c 2^X)_x (c 2^X)_w)
 // with x MXFP8 (E4M3) or MXFP4 (E2M1) and w MXFP4, one E8M0 scale per 32 of K,
-// on v_mfma_scale_f32_16x16x128_f8f6f4 with FP32 accumulation.
+// on v_mfma_scale_f32_32x32x64_f8f6f4 with FP32 accumulation.
 //
 // The weights are the matrix instruction's A operand and the activations its B
-// operand, so that a lane's four accumulators are consecutive columns of one
-// row of y.  Every output element is one chain of these instructions over K in
-// ascending steps of 128, whatever the tile: the bits of a token's result
+// operand, so that a lane's accumulators are consecutive columns of one row of
+// y.  Every output element is one chain of these instructions over K in
+// ascending steps of 64, whatever the tile: the bits of a token's result
 // depend neither on the batch size nor on the other tokens, and no variant
 // splits K.
 //
 // Operand lanes (checked on the device with one-hot inputs): lane l holds row
-// l % 16.  FP4: elements 32 (l / 16) .. +31 of the 128; FP8: elements 16 (l /
-// 16) .. +15 and 64 + 16 (l / 16) .. +15.  In both the lane supplies the scale
-// of its row's 32-block l / 16.
+// l % 32, half h = l / 32.  FP4: elements 32 h .. +31 of the 64; FP8: elements
+// 16 h .. +15 and 32 + 16 h .. +15.  In both the lane supplies the scale of its
+// row's 32-block h.
 
 #include <algorithm>
 
@@ -22,57 +22,86 @@
 namespace w4a4 {
 namespace {
 
-typedef float floatx4_t __attribute__((ext_vector_type(4)));
+constexpr int kStep = 128;        // K per step: two matrix instructions, four scale bytes a row
+constexpr int kScaleSteps = 4;    // scales are copied for four steps at a time
 
-constexpr int kLinBK = 128;   // K per stage: one matrix instruction
-
-// A tile of BM tokens x BN columns by WM x WN waves, a ring of S stages.
-template <bool X8_, int BM_, int BN_, int WM_, int WN_, int S_, int OCC_>
+// A tile of BM tokens x BN columns by WM x WN waves, a ring of S stages of SK
+// steps each.  AHEAD: a part of a stage is read into registers while the matrix
+// instructions of the part before it run (a second set of operand registers).
+template <bool X8_, int BM_, int BN_, int WM_, int WN_, int S_, int OCC_, int SK_ = 2, bool AHEAD_ = true>
 struct LinCfg {
-  static constexpr bool X8 = X8_;
+  static constexpr bool X8 = X8_, AHEAD = AHEAD_;
+  static constexpr int SK = SK_;
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, S = S_, OCC = OCC_;
   static constexpr int kWaves = WM * WN, kThreads = kWaves * kWave;
   static constexpr int TM = BM / WM, TN = BN / WN;   // a wave's tokens and columns
-  static constexpr int FT = TM / 16, FN = TN / 16;   // its 16-wide operand blocks
-  static constexpr int kXRow = X8 ? 128 : 64, kWRow = 64;   // bytes per staged row
+  static constexpr int FT = TM / 32, FN = TN / 32;   // its 32-wide operand blocks
+  static constexpr int kXRow = (X8 ? 128 : 64) * SK, kWRow = 64 * SK;   // bytes per staged row
+  static constexpr int kXLanes = kXRow / 16, kWLanes = kWRow / 16;   // lanes that copy one row
   // 1 KB pieces (one copy of a wave) per stage and per wave; where there are
   // fewer pieces than waves, some waves copy the same piece (the same bytes
-  // to the same place), so that every wave has the same count outstanding
-  static constexpr int NX = BM * kXRow / 1024, NW = BN * kWRow / 1024, NS = (BM + BN + 63) / 64;
+  // to the same place), so that every wave has the same count outstanding.
+  // Scales: 64 rows x 4 bytes per copy and step.
+  static constexpr int kRowBlocks = (BM + BN + 63) / 64;
+  static constexpr int NX = BM * kXRow / 1024, NW = BN * kWRow / 1024, NS = kRowBlocks * kScaleSteps;
   static constexpr int PX = (NX + kWaves - 1) / kWaves, PW = (NW + kWaves - 1) / kWaves,
                        PS = (NS + kWaves - 1) / kWaves;
-  static constexpr int kCopies = PX + PW + PS;
-  static constexpr int kW = BM * kXRow, kScales = kW + BN * kWRow, kStage = kScales + NS * 256;
-  static constexpr int kLds = S * kStage;
-  static_assert(NX * 1024 == BM * kXRow && NW * 1024 == BN * kWRow, "whole pieces");
-  static_assert((S - 1) * kCopies <= 63, "the vector-memory counter has six bits");
-  static_assert(FN == 1 || FN % 2 == 0, "columns are paired");
+  static constexpr int kCopies = PX + PW;
+  static constexpr int kW = BM * kXRow, kStage = kW + BN * kWRow;
+  // Scales: a ring of groups of kScaleSteps steps, GS stages.  Those of a
+  // group are copied when the stage S before its first has been read, by
+  // when the last stage of the group kScaleGroups before it has been, too.
+  static constexpr int GS = kScaleSteps / SK, kScaleGroups = (S + 2 * GS - 2) / GS;
+  static constexpr int kScales = S * kStage, kScaleStep = kRowBlocks * 256;
+  static constexpr int kLds = kScales + kScaleGroups * kScaleSteps * kScaleStep;
+  static_assert(FT >= 1 && FN >= 1 && FT * 32 * WM == BM && FN * 32 * WN == BN, "whole blocks");
+  static_assert(kLds <= 160 * 1024, "LDS of a compute unit");
+  static_assert((S - 2) * kCopies + ((S - 2) / GS + 1) * PS + (AHEAD ? kCopies + PS : 0) <= 63, "the vector-memory counter has six bits");
 };
 
 // 16-byte chunk slot of chunk c of staged row r: the 16 rows that one phase of
 // a 16-byte read touches lie in distinct banks.
-template <class C>
-__device__ __forceinline__ int x_slot(int r, int c) {
-  return C::X8 ? c ^ ((r >> 1) & 7) : c ^ ((r >> 2) & 3);
-}
-template <class C>
-__device__ __forceinline__ int w_slot(int r, int c) {
-  return C::FN == 1 ? c ^ ((r >> 2) & 3) : c ^ ((r >> 3) & 3);
-}
-// Column (within the wave's TN) of row i of column block f.  Blocks come in
-// pairs: a lane's accumulators of the two are 8 consecutive columns, a 16-byte
-// store, and the four lane groups of a row together store 64 bytes.
-template <class C>
-__device__ __forceinline__ int col_of(int f, int i) {
-  return C::FN == 1 ? i : 32 * (f / 2) + 8 * (i / 4) + 4 * (f % 2) + i % 4;
+template <int ROW>
+__device__ __forceinline__ int slot_of(int r, int c) {
+  return c ^ (ROW == 256 ? r & 15 : ROW == 128 ? (r >> 1) & 7 : (r >> 2) & 3);
 }
 
-template <int P, int MAX>
-__device__ __forceinline__ void wait_stages(int later) {   // at most `later` later stages outstanding
+// Column (within a block of 32) of the matrix instruction's row i = 8 a + 4 h + b:
+// a lane of half h holds the columns 8 h .. +7 (a = 0, 1) and 16 + 8 h .. +7 (a =
+// 2, 3), two 16-byte stores.
+__device__ __forceinline__ int col_of(int i) { return 16 * (i / 16) + 8 * (i / 4 % 2) + 4 * (i / 8 % 2) + i % 4; }
+
+// A per-lane LDS address as one register, so that the reads from it differ in
+// their constant offsets alone.
+__device__ __forceinline__ uint32_t opaque_vgpr(uint32_t v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
+__device__ __forceinline__ __attribute__((address_space(3))) u32x4_t* lds_out(uint32_t a) {
+  return reinterpret_cast<__attribute__((address_space(3))) u32x4_t*>(static_cast<uintptr_t>(a));
+}
+
+// Every LDS operation of this wave is done.  The builtin, not assembly: the
+// compiler has to know it, or it would wait for the following stage's reads
+// before the matrix instructions.
+__device__ __forceinline__ void wait_lds() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0) alone
+  asm volatile("" ::: "memory");
+}
+__device__ __forceinline__ void barrier() { asm volatile("s_barrier" ::: "memory"); }
+
+// Waits until everything up to a stage has landed, `later` stages (at most
+// MAX) having been issued after it: COPIES copies each, and SCALES more for
+// every GS-th, one more of those if `extra`.
+template <int MAX, int COPIES, int SCALES, int GS>
+__device__ __forceinline__ void wait_stages(int later, bool extra) {
   if (later >= MAX) {
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(P * MAX) : "memory");
+    if (extra) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(MAX * COPIES + (MAX / GS + 1) * SCALES) : "memory");
+    else asm volatile("s_waitcnt vmcnt(%0)" ::"n"(MAX * COPIES + MAX / GS * SCALES) : "memory");
   } else if constexpr (MAX > 0) {
-    wait_stages<P, MAX - 1>(later);
+    wait_stages<MAX - 1, COPIES, SCALES, GS>(later, extra);
   }
 }
 
@@ -92,7 +121,7 @@ mx_linear_kernel(LinArgs a) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave % C::WM, wn = wave / C::WM;
-  const int r16 = lane & 15, g = lane >> 4;
+  const int r32 = lane & 31, h = lane >> 5;
 
   // Tiles are dealt to the XCDs in contiguous runs; within a run, groups of
   // up to 8 token tiles with the column tiles running over them, so that the
@@ -115,80 +144,131 @@ mx_linear_kernel(LinArgs a) {
   const int cols = static_cast<int>(min<int64_t>(C::BN, a.N - n0));
 
   const int x_pitch = C::X8 ? a.K : a.K / 2, w_pitch = a.K / 2, s_pitch = a.K / 32;
+  const int steps = a.K / kStep, stages = (steps + C::SK - 1) / C::SK;
   const uint8_t* x_base = a.x + m0 * x_pitch;
   const uint8_t* w_base = a.w + n0 * w_pitch;
-  // Copy sources; rows past the operand are clamped to its last (they feed
-  // only outputs that are not stored).
-  uint32_t x_off[C::PX], w_off[C::PW];
+  // Copy sources and destinations; rows past the operand are clamped to its
+  // last (they feed only outputs that are not stored).
+  const uint32_t lds0 = lds_addr(lds);
+  uint32_t x_off[C::PX], w_off[C::PW], x_dst[C::PX], w_dst[C::PW], s_dst[C::PS];
   const uint8_t* s_src[C::PS];
+  int s_step[C::PS];
+  uint32_t x_upper = 0, w_upper = 0;   // bit j: the lane's chunk of copy j lies in the stage's second step
 #pragma unroll
   for (int j = 0; j < C::PX; ++j) {
-    const int piece = (wave + j * C::kWaves) % C::NX;
-    const int row = C::X8 ? 8 * piece + (lane >> 3) : 16 * piece + (lane >> 2);
-    const int chunk = x_slot<C>(row, C::X8 ? lane & 7 : lane & 3);
+    const int piece = (wave + j * C::kWaves) % C::NX, row = piece * (kWave / C::kXLanes) + lane / C::kXLanes;
+    const int chunk = slot_of<C::kXRow>(row, lane % C::kXLanes);
     x_off[j] = static_cast<uint32_t>(min(row, rows - 1)) * static_cast<uint32_t>(x_pitch) + chunk * 16;
+    x_dst[j] = lds0 + piece * 1024;
+    x_upper |= (chunk >= C::kXLanes / 2 ? 1u : 0u) << j;
   }
 #pragma unroll
   for (int j = 0; j < C::PW; ++j) {
-    const int row = 16 * ((wave + j * C::kWaves) % C::NW) + (lane >> 2);
-    w_off[j] = static_cast<uint32_t>(min(row, cols - 1)) * static_cast<uint32_t>(w_pitch) +
-               w_slot<C>(row, lane & 3) * 16;
+    const int piece = (wave + j * C::kWaves) % C::NW, row = piece * (kWave / C::kWLanes) + lane / C::kWLanes;
+    const int chunk = slot_of<C::kWRow>(row, lane % C::kWLanes);
+    w_off[j] = static_cast<uint32_t>(min(row, cols - 1)) * static_cast<uint32_t>(w_pitch) + chunk * 16;
+    w_dst[j] = lds0 + C::kW + piece * 1024;
+    w_upper |= (chunk >= C::kWLanes / 2 ? 1u : 0u) << j;
   }
 #pragma unroll
   for (int j = 0; j < C::PS; ++j) {
-    const int q = 64 * ((wave + j * C::kWaves) % C::NS) + lane;
+    // the copies of a row's four steps run one after the other (in one wave or
+    // in neighbouring ones), on one cache line
+    const int piece = (wave + j * C::kWaves) % C::NS, block = piece / kScaleSteps, q = block * 64 + lane;
     s_src[j] = q < C::BM ? a.xs + (m0 + min(q, rows - 1)) * s_pitch
                          : a.ws + (n0 + min(q - C::BM, cols - 1)) * s_pitch;
+    s_step[j] = piece % kScaleSteps;
+    s_dst[j] = lds0 + C::kScales + s_step[j] * C::kScaleStep + block * 256;
   }
-  const uint32_t lds0 = lds_addr(lds);
-  auto issue = [&](int kt) {
-    const uint32_t st = lds0 + (kt % C::S) * C::kStage;
+  // Issues the copies of the next stage (stages are issued in order).
+  int next = 0;
+  uint32_t next_slot = 0, next_group = 0;
+  auto issue = [&]() {
+    if (next % C::GS == 0) {
 #pragma unroll
-    for (int j = 0; j < C::PX; ++j)
-      dma16_off(x_base + static_cast<int64_t>(kt) * C::kXRow, x_off[j], st + ((wave + j * C::kWaves) % C::NX) * 1024);
+      for (int j = 0; j < C::PS; ++j)
+        dma4(s_src[j] + min(next * C::SK + s_step[j], steps - 1) * 4, s_dst[j] + next_group);
+      next_group += kScaleSteps * C::kScaleStep;
+      if (next_group == C::kScaleGroups * kScaleSteps * C::kScaleStep) next_group = 0;
+    }
+    const uint8_t* xb = x_base + static_cast<int64_t>(next) * C::kXRow;
+    const uint8_t* wb = w_base + static_cast<int64_t>(next) * C::kWRow;
+    if (C::SK == 2 && next * 2 + 1 == steps) {
+      // an odd number of steps: the last stage's second half lies behind the
+      // row and is filled from the first (never multiplied)
 #pragma unroll
-    for (int j = 0; j < C::PW; ++j)
-      dma16_off(w_base + static_cast<int64_t>(kt) * C::kWRow, w_off[j],
-                st + C::kW + ((wave + j * C::kWaves) % C::NW) * 1024);
+      for (int j = 0; j < C::PX; ++j)
+        dma16_off(xb, (x_upper >> j) & 1u ? x_off[j] - C::kXRow / 2 : x_off[j], x_dst[j] + next_slot);
 #pragma unroll
-    for (int j = 0; j < C::PS; ++j)
-      dma4(s_src[j] + kt * 4, st + C::kScales + ((wave + j * C::kWaves) % C::NS) * 256);
+      for (int j = 0; j < C::PW; ++j)
+        dma16_off(wb, (w_upper >> j) & 1u ? w_off[j] - C::kWRow / 2 : w_off[j], w_dst[j] + next_slot);
+    } else {
+#pragma unroll
+      for (int j = 0; j < C::PX; ++j) dma16_off(xb, x_off[j], x_dst[j] + next_slot);
+#pragma unroll
+      for (int j = 0; j < C::PW; ++j) dma16_off(wb, w_off[j], w_dst[j] + next_slot);
+    }
+    ++next;
+    next_slot += C::kStage;
+    if (next_slot == C::S * C::kStage) next_slot = 0;
+  };
+  // Stage st has landed in this wave: at most the stages issued after it, up
+  // to `next`, are outstanding.
+  auto wait_stage = [&](int st, auto most) {
+    constexpr int kMost = decltype(most)::value;
+    if constexpr (kMost == 0) {
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    } else {
+      const int later = min(kMost, stages - 1 - st);
+      wait_stages<kMost, C::kCopies, C::PS, C::GS>(later, (st + later) / C::GS - st / C::GS > later / C::GS);
+    }
   };
 
-  floatx4_t acc[C::FN][C::FT];
+  floatx16_t acc[C::FN][C::FT];
 #pragma unroll
   for (int f = 0; f < C::FN; ++f)
 #pragma unroll
-    for (int t = 0; t < C::FT; ++t) acc[f][t] = floatx4_t{0.0f, 0.0f, 0.0f, 0.0f};
-
-  // The lane's LDS offsets within a stage.  Blocks lie 16 rows (a pair of
-  // column blocks: 32) apart, where the slots repeat.
-  const int xr = wm * C::TM + r16;
-  const int x_lane = xr * C::kXRow + x_slot<C>(xr, g) * 16;
-  const int x_lane_hi = xr * C::kXRow + x_slot<C>(xr, 4 + g) * 16;   // FP8: the upper 64 of K
-  const int wr0 = wn * C::TN + col_of<C>(0, r16), wr1 = wn * C::TN + (C::FN == 1 ? 0 : col_of<C>(1, r16));
-  const int w_lane[2] = {C::kW + wr0 * C::kWRow + w_slot<C>(wr0, g) * 16,
-                         C::kW + wr1 * C::kWRow + w_slot<C>(wr1, g) * 16};
-  const int xs_lane = C::kScales + xr * 4 + g;
-  const int ws_lane[2] = {C::kScales + (C::BM + wr0) * 4 + g, C::kScales + (C::BM + wr1) * 4 + g};
-
-  struct Frags {
-    u32x4_t x[C::FT][C::X8 ? 2 : 1];
-    u32x4_t w[C::FN];
-    int xs[C::FT], ws[C::FN];
-  };
-  auto read = [&](int kt, Frags& f) {
-    const uint32_t st = opaque_sgpr(lds0 + (kt % C::S) * C::kStage);
+    for (int t = 0; t < C::FT; ++t)
 #pragma unroll
-    for (int t = 0; t < C::FT; ++t) {
-      f.x[t][0] = *lds_ptr<u32x4_t>(st + x_lane + t * 16 * C::kXRow);
-      if constexpr (C::X8) f.x[t][1] = *lds_ptr<u32x4_t>(st + x_lane_hi + t * 16 * C::kXRow);
-      f.xs[t] = *lds_ptr<uint8_t>(st + xs_lane + t * 16 * 4);
-    }
+      for (int v = 0; v < 16; ++v) acc[f][t][v] = 0.0f;
+
+  // The lane's rows, and its LDS offsets within a stage per step and matrix
+  // instruction (and for FP8 per half of its 32 bytes).  Blocks lie 32 rows
+  // apart, where the slots repeat.
+  const int xr = wm * C::TM + r32, wr = wn * C::TN + col_of(r32);
+  const uint32_t x_row = xr * C::kXRow, w_row = C::kW + wr * C::kWRow;
+  const uint32_t xs_lane = C::kScales + xr * 4 + h, ws_lane = C::kScales + (C::BM + wr) * 4 + h;
+
+  struct Frags {   // one matrix instruction's worth of K
+    u32x4_t x[C::FT][C::X8 ? 2 : 1], w[C::FN];
+    int sx[C::FT], sw[C::FN];
+  };
+  uint32_t slot = 0, sc = 0;   // LDS offsets of the stage being read and of its first step's scales
+  auto advance = [&]() {
+    slot += C::kStage;
+    if (slot == C::S * C::kStage) slot = 0;
+    sc += C::SK * C::kScaleStep;
+    if (sc == C::kScaleGroups * kScaleSteps * C::kScaleStep) sc = 0;
+  };
+  auto read = [&](auto part, Frags& f) {   // part of the stage: step part / 2, instruction part % 2
+    constexpr int kSub = decltype(part)::value / 2, kHalf = decltype(part)::value % 2;
+    const uint32_t st = lds0 + slot;
+    const uint32_t xs = opaque_vgpr(lds0 + sc + xs_lane), ws = opaque_vgpr(lds0 + sc + ws_lane);
+    const uint32_t wa = opaque_vgpr(st + w_row + slot_of<C::kWRow>(wr, 4 * kSub + 2 * kHalf + h) * 16);
+    const uint32_t xa = opaque_vgpr(
+        st + x_row + slot_of<C::kXRow>(xr, C::X8 ? 8 * kSub + 4 * kHalf + h : 4 * kSub + 2 * kHalf + h) * 16);
+    const uint32_t xb =
+        C::X8 ? opaque_vgpr(st + x_row + slot_of<C::kXRow>(xr, 8 * kSub + 4 * kHalf + 2 + h) * 16) : 0u;
 #pragma unroll
     for (int n = 0; n < C::FN; ++n) {
-      f.w[n] = *lds_ptr<u32x4_t>(st + w_lane[n % 2] + (n / 2) * 32 * C::kWRow);
-      f.ws[n] = *lds_ptr<uint8_t>(st + ws_lane[n % 2] + (n / 2) * 32 * 4);
+      f.sw[n] = *lds_ptr<uint8_t>(ws + kSub * C::kScaleStep + n * 32 * 4 + 2 * kHalf);
+      f.w[n] = *lds_ptr<u32x4_t>(wa + n * 32 * C::kWRow);
+    }
+#pragma unroll
+    for (int t = 0; t < C::FT; ++t) {
+      f.sx[t] = *lds_ptr<uint8_t>(xs + kSub * C::kScaleStep + t * 32 * 4 + 2 * kHalf);
+      f.x[t][0] = *lds_ptr<u32x4_t>(xa + t * 32 * C::kXRow);
+      if constexpr (C::X8) f.x[t][1] = *lds_ptr<u32x4_t>(xb + t * 32 * C::kXRow);
     }
   };
   auto multiply = [&](const Frags& f) {
@@ -205,52 +285,99 @@ mx_linear_kernel(LinArgs a) {
         const i32x8_t wv = {static_cast<int>(f.w[n][0]), static_cast<int>(f.w[n][1]), static_cast<int>(f.w[n][2]),
                             static_cast<int>(f.w[n][3]), 0, 0, 0, 0};
         // formats: 4 = FP4 E2M1, 0 = FP8 E4M3; scale bytes in bits 7:0
-        acc[n][t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wv, xv, acc[n][t], 4, C::X8 ? 0 : 4, 0,
-                                                                     f.ws[n], 0, f.xs[t]);
+        acc[n][t] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wv, xv, acc[n][t], 4, C::X8 ? 0 : 4, 0, f.sw[n], 0,
+                                                                    f.sx[t]);
       }
     }
   };
+  constexpr std::integral_constant<int, 0> p0{};
+  constexpr std::integral_constant<int, 1> p1{};
+  constexpr std::integral_constant<int, 2> p2{};
+  constexpr std::integral_constant<int, 3> p3{};
+  const bool odd_steps = C::SK == 2 && steps % 2 != 0;
 
-  // Stage kt + 1 is read into registers while the matrix instructions of
-  // stage kt run; a stage's slot is free once every wave holds it in
-  // registers, at the barrier of the step that multiplies it.
-  const int nk = a.K / kLinBK;
-  for (int s = 0; s < C::S && s < nk; ++s) issue(s);
-  Frags even, odd;
-  wait_stages<C::kCopies, C::S - 1>(min(C::S, nk) - 1);
-  read(0, even);
-  auto step = [&](int kt, const Frags& cur, Frags& next) {
-    if (kt + 1 < nk) {
-      wait_stages<C::kCopies, C::S - 2>(min(C::S - 2, nk - 2 - kt));
-      if (kt + C::S < nk) issue(kt + C::S);
-      read(kt + 1, next);
+  if constexpr (C::AHEAD) {
+    // A stage's slot is free once every wave has its last part in registers:
+    // at the barrier in front of that part's matrix instructions.
+    Frags even, odd;
+    for (int s = 0; s < C::S && s < stages; ++s) issue();
+    wait_stage(0, std::integral_constant<int, C::S - 1>{});
+    barrier();
+    read(p0, even);
+    for (int st = 0; st < stages; ++st) {
+      read(p1, odd);
+      multiply(even);
+      if constexpr (C::SK == 2) {
+        if (!odd_steps || st + 1 < stages) {
+          read(p2, even);
+          multiply(odd);
+          read(p3, odd);
+          multiply(even);
+        }
+      }
+      wait_lds();
+      if (st + 1 < stages) {
+        wait_stage(st + 1, std::integral_constant<int, C::S - 2>{});
+        barrier();
+        if (next < stages) issue();
+        advance();
+        read(p0, even);
+      }
+      multiply(odd);
     }
-    multiply(cur);
-  };
-  for (int kt = 0; kt < nk; kt += 2) {
-    step(kt, even, odd);
-    if (kt + 1 < nk) step(kt + 1, odd, even);
+  } else {
+    for (int s = 0; s < C::S - 1 && s < stages; ++s) issue();
+    for (int st = 0; st < stages; ++st) {
+      // stage st has landed in every wave, and every wave is past stage st - 1
+      wait_stage(st, std::integral_constant<int, C::S - 2>{});
+      barrier();
+      if (next < stages) issue();
+      Frags f;
+      read(p0, f);
+      multiply(f);
+      read(p1, f);
+      multiply(f);
+      if constexpr (C::SK == 2) {
+        if (!odd_steps || st + 1 < stages) {
+          read(p2, f);
+          multiply(f);
+          read(p3, f);
+          multiply(f);
+        }
+      }
+      advance();
+    }
   }
 
+  // The wave's results, rounded, go through its own part of the ring 32 rows
+  // at a time and leave as whole rows of its columns (16-byte chunks, slots as
+  // the operands'): against 16-byte stores from the accumulators, of which two
+  // make 32 bytes of a row, 4 to 10% of the time of 8192 x 2048 columns.
+  // Non-temporal: y is not read again here, and the operands stay in the L2.
+  constexpr int kOutRow = C::TN * 2, kOutChunks = kOutRow / 16, kOutRows = kWave / kOutChunks;
+  static_assert(C::kWaves * 32 * kOutRow <= C::kScales, "the staged rows fit in the ring");
+  barrier();   // every wave is past its last read of the ring, and every copy has landed
+  const uint32_t out = lds0 + wave * (32 * kOutRow);
+  const int out_row = lane / kOutChunks, out_chunk = lane % kOutChunks;
+  const int n = wn * C::TN + out_chunk * 8;
 #pragma unroll
   for (int t = 0; t < C::FT; ++t) {
-    const int tr = wm * C::TM + 16 * t + r16;
-    if (tr >= rows) continue;
-    uint16_t* yr = a.y + (m0 + tr) * a.y_stride + n0;
-    if constexpr (C::FN == 1) {
-      const int n = wn * C::TN + 4 * g;
-      if (n < cols)
-        *reinterpret_cast<u32x2_t*>(yr + n) =
-            u32x2_t{pack_bf16x2(acc[0][t][0], acc[0][t][1]), pack_bf16x2(acc[0][t][2], acc[0][t][3])};
-    } else {
 #pragma unroll
-      for (int f = 0; f < C::FN; f += 2) {
-        const int n = wn * C::TN + 16 * f + 8 * g;
-        if (n < cols)
-          *reinterpret_cast<u32x4_t*>(yr + n) =
-              u32x4_t{pack_bf16x2(acc[f][t][0], acc[f][t][1]), pack_bf16x2(acc[f][t][2], acc[f][t][3]),
-                      pack_bf16x2(acc[f + 1][t][0], acc[f + 1][t][1]), pack_bf16x2(acc[f + 1][t][2], acc[f + 1][t][3])};
+    for (int f = 0; f < C::FN; ++f)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const floatx16_t& v = acc[f][t];
+        *lds_out(out + r32 * kOutRow + slot_of<kOutRow>(r32, 4 * f + 2 * q + h) * 16) =
+            u32x4_t{pack_bf16x2(v[8 * q], v[8 * q + 1]), pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
+                    pack_bf16x2(v[8 * q + 4], v[8 * q + 5]), pack_bf16x2(v[8 * q + 6], v[8 * q + 7])};
       }
+    wait_lds();
+#pragma unroll
+    for (int p = 0; p < 32 / kOutRows; ++p) {
+      const int row = p * kOutRows + out_row, tr = wm * C::TM + 32 * t + row;
+      const u32x4_t o = *lds_ptr<u32x4_t>(out + row * kOutRow + slot_of<kOutRow>(row, out_chunk) * 16);
+      if (tr < rows && n < cols)
+        __builtin_nontemporal_store(o, reinterpret_cast<u32x4_t*>(a.y + (m0 + tr) * a.y_stride + n0 + n));
     }
   }
 }
@@ -267,11 +394,47 @@ bool launch_cfg(LinArgs a, hipStream_t s) {
   return launch_ok("mx_linear");
 }
 
+// Tiles of BM x BN in a product.
+int64_t tiles_of(const LinArgs& a, int bm, int bn) {
+  return (a.T + bm - 1) / bm * static_cast<int64_t>((a.N + bn - 1) / bn);
+}
+
+// The tile: the larger, the fewer bytes a product copies, but every CU wants
+// one.
+//   32 x 32 up to 640 tiles (2.5 a CU), then 64 x 64 up to 640 of those: T =
+//     100, N = 4096, K = 2048: 5.6 us against 5.8 with 64 x 64; T = 200: 7.1
+//     against 6.1; T = 500: 7.4 (64 x 64) against 9.3 (128 x 128); T = 1024:
+//     12.5 against 10.6 (FP4; FP8 alike).
+//   64 x 128 for at most 64 tokens beyond that, half of whose rows a tile of
+//     128 would leave empty: T = 48, N = 65536: 13.4 us as 64 x 64 with FP4,
+//     14.4 against 16.9 with FP8.
+//   128 x 128 or 256 x 256 by rounds over the chip: two of the former run on a
+//     CU at once, and a round of 512 takes 1 / 1.6 of a round of 256 of the
+//     latter, its last one 0.65 of that where it has at most one tile a CU.  T
+//     = 5001, K = 4096, N = 2048 (1.25 against 0.6 rounds): 36 against 30 us;
+//     T = 10000, K = 2048 (2.5 against 1.25): 32 against 38; T = 1500, N =
+//     4096: 14 against 17; T = 16384: 100 against 92 (FP4).
 template <bool X8>
 bool launch_format(const LinArgs& a, hipStream_t s) {
-  if (a.T <= 16) return launch_cfg<LinCfg<X8, 16, 16, 1, 1, 8, 1>>(a, s);
-  if (a.T <= 64) return launch_cfg<LinCfg<X8, 64, 64, 1, 4, 4, 1>>(a, s);
-  return launch_cfg<LinCfg<X8, 128, 128, 2, 2, 4, 1>>(a, s);
+  if (tiles_of(a, 32, 32) <= 640) return launch_cfg<LinCfg<X8, 32, 32, 1, 1, 2, 2>>(a, s);
+  if (tiles_of(a, 64, 64) <= 640) return launch_cfg<LinCfg<X8, 64, 64, 2, 2, 2, 2>>(a, s);
+  if (a.T <= 64) return launch_cfg<LinCfg<X8, 64, 128, 2, 2, 2, 2>>(a, s);
+  const int64_t n128 = tiles_of(a, 128, 128), n256 = tiles_of(a, 256, 256);
+  const double rounds128 = static_cast<double>(n128 / 512) + (n128 % 512 > 256 ? 1.0 : n128 % 512 > 0 ? 0.65 : 0.0);
+  if (rounds128 <= 1.6 * static_cast<double>((n256 + 255) / 256)) {
+    if constexpr (X8) {
+      // stages of one step, so that two workgroups fit on a CU; of two steps
+      // (whole cache lines of w) where there is one at most: 256 tiles 12.7
+      // us against 14.9, 384 tiles 21.5 against 19.6
+      if (n128 <= 256) return launch_cfg<LinCfg<true, 128, 128, 4, 2, 2, 2>>(a, s);
+      return launch_cfg<LinCfg<true, 128, 128, 2, 2, 2, 2, 1>>(a, s);
+    } else {
+      return launch_cfg<LinCfg<false, 128, 128, 2, 2, 2, 2>>(a, s);
+    }
+  }
+  // 16 waves of 64 x 64, whose registers a second set of operands would not
+  // fit in; with FP8 stages of one step, for the ring to fit in LDS
+  return launch_cfg<LinCfg<X8, 256, 256, 4, 4, 2, 1, X8 ? 1 : 2, false>>(a, s);
 }
 
 }  // namespace

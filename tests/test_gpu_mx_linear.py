@@ -72,11 +72,14 @@ def _fmt(b, name):
     return b.MX_FP8 if name == "fp8" else b.MX_FP4
 
 
-# every tile variant, one row, ragged rows and columns, one stage, an odd
-# number of stages, fewer and more stages than a ring
+# one row, ragged rows and columns, one step, odd numbers of steps, fewer and
+# more stages than a ring; the last six reach the tiles that larger products
+# take (64 x 128, 128 x 128 with either count of tiles, 256 x 256)
 @pytest.mark.parametrize("T,K,N", [(1, 128, 8), (1, 2048, 256), (3, 384, 40), (16, 640, 1000), (17, 1024, 136),
                                    (32, 4096, 72), (33, 256, 264), (48, 2048, 512), (64, 1152, 2048), (65, 128, 128),
-                                   (127, 896, 520), (300, 1024, 776), (513, 2048, 256), (1000, 256, 1032)])
+                                   (127, 896, 520), (300, 1024, 776), (513, 2048, 256), (1000, 256, 1032),
+                                   (40, 128, 41000), (64, 384, 41224), (1200, 384, 2312), (2100, 640, 2568),
+                                   (4999, 384, 2056), (5121, 128, 2048)])
 @pytest.mark.parametrize("fmt", FORMATS)
 def test_linear(b, T, K, N, fmt):
     f = _fmt(b, fmt)
@@ -86,7 +89,8 @@ def test_linear(b, T, K, N, fmt):
     _check(b, y, xq, wq, f, K)
 
 
-@pytest.mark.parametrize("T,K,N", [(1, 2048, 64), (16, 256, 48), (50, 1280, 200), (200, 768, 328), (700, 2048, 512)])
+@pytest.mark.parametrize("T,K,N", [(1, 2048, 64), (16, 256, 48), (50, 1280, 200), (200, 768, 328), (700, 2048, 512),
+                                   (50, 256, 41000), (1300, 384, 2312), (2100, 256, 2568), (5001, 384, 2056)])
 @pytest.mark.parametrize("fmt", FORMATS)
 def test_linear_exact_sums(b, T, K, N, fmt):
     """Elements and scales whose products are multiples of 2^-4 and whose sums
@@ -114,16 +118,22 @@ def test_linear_exact_sums(b, T, K, N, fmt):
     assert np.array_equal(bf16_host(y), q.round_bf16(want))
 
 
+@pytest.mark.parametrize("T,K,N,parts", [
+    (2100, 2048, 520, ((0, 1), (5, 2), (100, 16), (7, 17), (40, 33), (3, 64), (11, 65), (128, 300), (1000, 1100))),
+    (5001, 1152, 2056, ((17, 1), (60, 70), (1000, 400), (100, 1300), (2900, 2100))),
+    (2100, 384, 2568, ((4, 3), (7, 200), (500, 1300))),
+    (64, 640, 41000, ((9, 1), (30, 33)))])
 @pytest.mark.parametrize("fmt", FORMATS)
-def test_linear_bits_do_not_depend_on_the_batch(b, fmt):
-    """The same rows alone, in small and in large batches: the same bits."""
-    K, N, f = 2048, 520, _fmt(b, fmt)
-    xq, wq = _operands(b, 2100, K, N, f, 9)
-    print_case("mx_linear_batch_bits", fmt=fmt)
-    full = b.w4a4_mx_linear_fwd(xq, wq, 2100, K, N)
-    for t0, T in ((0, 1), (5, 2), (100, 16), (7, 17), (40, 33), (3, 64), (11, 65), (128, 300), (1000, 1100)):
-        part = {n: v[t0:t0 + T].contiguous() for n, v in xq.items()}
-        assert torch.equal(b.w4a4_mx_linear_fwd(part, wq, T, K, N), full[t0:t0 + T]), (t0, T)
+def test_linear_bits_do_not_depend_on_the_batch(b, T, K, N, parts, fmt):
+    """The same rows alone, in small and in large batches (every tile of the
+    product): the same bits."""
+    f = _fmt(b, fmt)
+    xq, wq = _operands(b, T, K, N, f, 9)
+    print_case("mx_linear_batch_bits", T=T, K=K, N=N, fmt=fmt)
+    full = b.w4a4_mx_linear_fwd(xq, wq, T, K, N)
+    for t0, n in parts:
+        part = {name: v[t0:t0 + n].contiguous() for name, v in xq.items()}
+        assert torch.equal(b.w4a4_mx_linear_fwd(part, wq, n, K, N), full[t0:t0 + n]), (t0, n)
 
 
 @pytest.mark.parametrize("T", [5, 200])

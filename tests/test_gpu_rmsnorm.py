@@ -194,6 +194,28 @@ def test_norm_backward_in_place_without_dgamma_and_empty(b):
     assert none["dres"].shape == (0, H) and not none["dgamma"].any()
 
 
+def test_rows_of_a_batch_apart(b):
+    """Any rows of a batch (whose scales and rstd then start at odd addresses)
+    give what they give in it."""
+    T, H = 40, 288
+    x, r, g = _inputs(T, H, torch.bfloat16, torch.float32, 12)
+    dy = _dev(np.random.default_rng(1).standard_normal((T, H)), torch.bfloat16)
+    print_case("rows_apart")
+    for fmt in (b.MX_FP4, b.MX_FP8):
+        full = b.w4a4_add_rmsnorm_fwd(x, g, 1e-6, residual=r, fmt=fmt, save=True)
+        quant = b.w4a4_mx_quantize_rows(x, fmt)
+        back = b.w4a4_add_rmsnorm_bwd(dy, full["sum"], g, full["rstd"], dgamma=False)
+        for t0, t1 in ((0, 1), (1, 4), (7, 40)):
+            out = {n: torch.zeros_like(v)[t0:t1] for n, v in full.items()}
+            b.w4a4_add_rmsnorm_fwd(x[t0:t1], g, 1e-6, residual=r[t0:t1], fmt=fmt, save=True, out=out)
+            assert all(torch.equal(out[n], v[t0:t1]) for n, v in full.items())
+            out = {n: torch.zeros_like(v)[t0:t1] for n, v in quant.items()}
+            b.w4a4_mx_quantize_rows(x[t0:t1], fmt, out=out)
+            assert all(torch.equal(out[n], v[t0:t1]) for n, v in quant.items())
+            part = b.w4a4_add_rmsnorm_bwd(dy[t0:t1], full["sum"][t0:t1], g, full["rstd"][t0:t1], dgamma=False)
+            assert torch.equal(part["dres"], back["dres"][t0:t1])
+
+
 # ------------------------------------------------------------- MX quantiser
 def _edge_rows():
     """Rows of 64: ties and their neighbours at several exponents, zeros of both

@@ -44,7 +44,7 @@ def test_quantize_rows_refusals(lib, p):
     assert q(stride=68) == INVALID                 # rows off the 16-byte grid
     assert q(x=None) == INVALID and q(codes=None) == INVALID and q(scales=None) == INVALID
     assert q(x=_off(p)) == INVALID and q(codes=_off(p)) == INVALID
-    assert q(offsets=_off(p, 8)) == INVALID
+    assert q(offsets=_off(p)) == INVALID
     assert q(T=1 << 31) == UNSUPPORTED
     assert "int32" in lib.w4a4_last_error().decode()
     assert q(T=0, x=None, codes=None, scales=None) == 0   # nothing to do, nothing launched
@@ -67,7 +67,7 @@ def test_norm_refusals(lib, p):
     assert f(fmt=NONE) == INVALID                  # codes without a format
     assert f(codes=None) == INVALID and f(x=None) == INVALID and f(gamma=None) == INVALID
     assert f(res=_off(p)) == INVALID and f(total=_off(p)) == INVALID and f(y=_off(p)) == INVALID
-    assert f(rstd=_off(p, 4)) == INVALID
+    assert f(rstd=_off(p)) == INVALID
     assert f(total=p, rdt=F32) == INVALID          # a float sum over a bf16 x
     assert f(total=p, stride=128) == INVALID       # a dense sum over a slice
     assert f(T=1 << 31) == UNSUPPORTED
@@ -106,7 +106,7 @@ def test_linear_refusals(lib, p):
     assert f(fmt=NONE) == INVALID
     assert f(stride=56) == INVALID and f(stride=68) == INVALID
     assert f(x=None) == INVALID and f(xs=None) == INVALID and f(w=None) == INVALID and f(ws=None) == INVALID
-    assert f(y=None) == INVALID and f(y=_off(p)) == INVALID and f(w=_off(p)) == INVALID
+    assert f(y=None) == INVALID and f(y=_off(p)) == INVALID and f(w=_off(p)) == INVALID and f(xs=_off(p)) == INVALID
     assert f(T=1 << 31) == UNSUPPORTED
     assert f(T=0, x=None, xs=None, w=None, ws=None, y=None) == 0
 
