@@ -218,7 +218,7 @@ def _own(s):
         return _values(q["codes"], q["scales"])
     if op == "linear":
         xq = s["xq"]
-        if s["x"] != "codes":
+        if not isinstance(s["x"], str):
             xq = b.w4a4_mx_quantize_rows(s["x"], b.MX_FP8 if s["fmt"] == "fp8" else b.MX_FP4, out=xq)
         return {"y": b.w4a4_mx_linear_fwd(xq, s["wq"], s["T"], s["K"], s["N"], y=s["y"])}
     if op == "norm":
