@@ -826,7 +826,7 @@ w4a4_status w4a4_add_rmsnorm_fwd(int64_t T, int H, float eps, const void* x, int
   if ((st = check_element_ptr("offsets", offsets, 4, false)) != W4A4_OK) return st;
   if (T == 0 && offsets == nullptr) return W4A4_OK;
   const NormFwdArgs a{T, H, eps, static_cast<const uint16_t*>(x), x_stride, residual, T > 0 ? gamma : nullptr,
-                      gamma_dtype == W4A4_F32, sum, static_cast<uint16_t*>(y), codes, scales, rstd, offsets};
+                      gamma_dtype == W4A4_F32, sum, static_cast<uint16_t*>(y), codes, scales, rstd, offsets, false};
   if (!launch_add_rmsnorm(a, residual_dtype == W4A4_F32, format, static_cast<hipStream_t>(stream)))
     return W4A4_ERR_LAUNCH;
   return W4A4_OK;
@@ -861,7 +861,7 @@ w4a4_status w4a4_add_rmsnorm_bwd(int64_t T, int H, const void* dy, const void* s
     REQUIRE_PTR(workspace);
   }
   const NormBwdArgs a{T, H, static_cast<const uint16_t*>(dy), sum, gamma, gamma_dtype == W4A4_F32, rstd, dsum, dres,
-                      static_cast<uint16_t*>(dx), dgamma != nullptr ? static_cast<float*>(workspace) : nullptr};
+                      static_cast<uint16_t*>(dx), dgamma != nullptr ? static_cast<float*>(workspace) : nullptr, false};
   if (!launch_add_rmsnorm_bwd(a, residual_dtype == W4A4_F32, dgamma, static_cast<hipStream_t>(stream)))
     return W4A4_ERR_LAUNCH;
   return W4A4_OK;

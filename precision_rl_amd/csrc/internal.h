@@ -199,6 +199,7 @@ struct NormFwdArgs {
   uint8_t* scales;
   float* rstd;
   int32_t* offsets;
+  bool stream;   // set by the launch: non-temporal loads
 };
 bool launch_add_rmsnorm(const NormFwdArgs& a, bool res_f32, int format, hipStream_t s);
 
@@ -216,6 +217,7 @@ struct NormBwdArgs {
   void* dres;
   uint16_t* dx;
   float* part;
+  bool stream;   // set by the launch: non-temporal loads
 };
 int norm_bwd_blocks(int64_t T, int H);
 bool launch_add_rmsnorm_bwd(const NormBwdArgs& a, bool res_f32, float* dgamma, hipStream_t s);

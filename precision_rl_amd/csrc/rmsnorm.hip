@@ -9,9 +9,13 @@
 //
 // The codes are those of the bf16 y (not of the FP32 product), so that the
 // fused call gives the bytes of the norm followed by the quantiser and the
-// straight-through backward sees the operand that was quantised.  Sums,
-// products and rstd are FP32.  All calls are bound by HBM: every tensor is
-// read or written once.
+// straight-through backward sees the operand that was quantised.
+//
+// The forward sums the squares in FP64 and multiplies by rstd as the sum of
+// two floats, so that y differs from the rounded exact value only where an FP32
+// rounding next to a midpoint tips it; neither costs time beside HBM, and no
+// row's squares overflow or underflow.  Everything else is FP32.  All calls
+// are bound by HBM: every tensor is read or written once.
 
 #include <algorithm>
 
@@ -26,14 +30,26 @@ typedef float floatx4_t __attribute__((ext_vector_type(4)));
 constexpr int kNormThreads = 256;
 constexpr int kBwdThreads = 512;
 
-// 8 consecutive elements as floats.
+// Whether a call's loads are non-temporal: where it moves more than three
+// quarters of the 256 MiB memory-side cache, its inputs cannot all still lie
+// there, and loads that leave the cache alone are faster (16384 rows of 2048,
+// forward with FP8 codes, 236 MB: 46.7 us against 49.0, backward, 268 MB: 50.8
+// against 53.6); below, they would miss what the producer left (2000 rows of
+// 8192, 115 MB: 28 against 22).
+bool streams(double bytes) { return bytes > 0.75 * 256 * 1024 * 1024; }
+
+// 8 consecutive elements as floats.  Stores are non-temporal (no output is
+// read again by its call): 16384 rows of 2048 with all outputs 66 to 63 us,
+// 2000 rows of 8192 38 to 25.
 template <typename T>
 struct Vec8;
 template <>
 struct Vec8<uint16_t> {   // bf16
   u32x4_t w;
+  template <bool NT = false>
   __device__ __forceinline__ void load(const uint16_t* p) {
-    w = *reinterpret_cast<const u32x4_t*>(p);
+    if constexpr (NT) w = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(p));
+    else w = *reinterpret_cast<const u32x4_t*>(p);
   }
   __device__ __forceinline__ float get(int i) const {
     return __uint_as_float((i & 1) ? (w[i >> 1] & 0xFFFF0000u) : (w[i >> 1] << 16));
@@ -44,14 +60,20 @@ struct Vec8<uint16_t> {   // bf16
 #pragma unroll
     for (int d = 0; d < 4; ++d) w[d] = pack_bf16x2(v[2 * d], v[2 * d + 1]);
   }
-  __device__ __forceinline__ void store(uint16_t* p) const { *reinterpret_cast<u32x4_t*>(p) = w; }
+  __device__ __forceinline__ void store(uint16_t* p) const {
+    __builtin_nontemporal_store(w, reinterpret_cast<u32x4_t*>(p));
+  }
 };
 template <>
 struct Vec8<float> {
   floatx4_t w[2];
+  template <bool NT = false>
   __device__ __forceinline__ void load(const float* p) {
-    w[0] = reinterpret_cast<const floatx4_t*>(p)[0];
-    w[1] = reinterpret_cast<const floatx4_t*>(p)[1];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if constexpr (NT) w[h] = __builtin_nontemporal_load(reinterpret_cast<const floatx4_t*>(p) + h);
+      else w[h] = reinterpret_cast<const floatx4_t*>(p)[h];
+    }
   }
   __device__ __forceinline__ float get(int i) const { return w[i >> 2][i & 3]; }
   __device__ __forceinline__ void zero() { w[0] = w[1] = floatx4_t{0.0f, 0.0f, 0.0f, 0.0f}; }
@@ -60,30 +82,29 @@ struct Vec8<float> {
     for (int i = 0; i < 8; ++i) w[i >> 2][i & 3] = v[i];
   }
   __device__ __forceinline__ void store(float* p) const {
-    reinterpret_cast<floatx4_t*>(p)[0] = w[0];
-    reinterpret_cast<floatx4_t*>(p)[1] = w[1];
+    __builtin_nontemporal_store(w[0], reinterpret_cast<floatx4_t*>(p));
+    __builtin_nontemporal_store(w[1], reinterpret_cast<floatx4_t*>(p) + 1);
   }
 };
 
 // Sum over the TEAM lanes of a row, the same in each of them, in an order
-// that depends on TEAM alone.  TEAM > 64: the waves' sums meet in LDS, in one
-// of two sets of slots taken in turn, so that one barrier per sum is enough (a
-// wave can be at most one sum ahead of a wave that still reads).
-template <int TEAM>
-__device__ __forceinline__ float team_sum(float v, float* slots, int& turn) {
+// that depends on TEAM alone.  TEAM > 64: the waves' sums meet in `slots` (LDS,
+// one per wave of the workgroup); a kernel that sums again takes two sets in
+// turn, so that one barrier per sum is enough (a wave can be at most one sum
+// ahead of a wave that still reads).
+template <int TEAM, typename T>
+__device__ __forceinline__ T team_sum(T v, T* slots) {
   constexpr int kLanes = TEAM < kWave ? TEAM : kWave;
 #pragma unroll
   for (int off = kLanes / 2; off > 0; off >>= 1) v += __shfl_xor(v, off, kWave);
   if constexpr (TEAM > kWave) {
     constexpr int kWaves = TEAM / kWave;
     const int wave = threadIdx.x / kWave, first = wave / kWaves * kWaves;
-    float* mine = slots + turn * (kBwdThreads / kWave);
-    turn ^= 1;
-    if (threadIdx.x % kWave == 0) mine[wave] = v;
+    if (threadIdx.x % kWave == 0) slots[wave] = v;
     __syncthreads();
-    v = 0.0f;
+    v = slots[first];
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) v += mine[first + w];
+    for (int w = 1; w < kWaves; ++w) v += slots[first + w];
   }
   return v;
 }
@@ -112,86 +133,79 @@ __device__ __forceinline__ void load_gamma(float (&g)[P][8], const void* gamma, 
 // ------------------------------------------------------------------ forward
 // TEAM lanes per row, lane l the 8-element chunks l, l + TEAM, ... (P of
 // them): the row stays in registers between the sum of squares and the
-// output.  Teams stride over the rows; gamma is loaded once per team.
+// output.  One row per team and a workgroup per 256 / TEAM rows: workgroups
+// that stride over the rows, loading the next row beside the current one's
+// output, took 2 to 12% longer on large batches.
 template <int TEAM, int P, typename RES, int FMT>
 __global__ void __launch_bounds__(kNormThreads)
 norm_fwd_kernel(NormFwdArgs a) {
-  __shared__ float slots[2 * (kBwdThreads / kWave)];
-  int turn = 0;
+  __shared__ double slots[kNormThreads / kWave];
   const int lane = threadIdx.x % TEAM, chunks = a.H / 8;
   constexpr int kTeams = kNormThreads / TEAM;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kTeams;
   const RES* residual = static_cast<const RES*>(a.residual);
   RES* sum = static_cast<RES*>(a.sum);
-  float g[P][8];
-  load_gamma<P>(g, a.gamma, a.gamma_f32, lane, TEAM, chunks);
   if (a.offsets != nullptr && blockIdx.x == 0 && threadIdx.x < 2)
     a.offsets[threadIdx.x] = threadIdx.x == 0 ? 0 : static_cast<int32_t>(a.T);
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kTeams + threadIdx.x / TEAM;
+  if (t >= a.T) return;   // TEAM > 64: the whole workgroup
 
-  // TEAM > 64 has a barrier in its sum: one team per workgroup, whose waves
-  // run the same iterations
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kTeams + threadIdx.x / TEAM; t < a.T; t += step) {
-    Vec8<RES> s[P];
-    float ss = 0.0f;
+  // every load of the row in flight before the first is used
+  Vec8<uint16_t> x[P];
+  Vec8<RES> s[P];
+  auto load = [&](auto nt) {
+    constexpr bool NT = decltype(nt)::value;
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       const int c = lane + p * TEAM;
+      x[p].zero();
       s[p].zero();
       if (c < chunks) {
-        Vec8<uint16_t> x;
-        x.load(a.x + t * a.x_stride + c * 8);
-        float v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = x.get(i);
-        if (residual != nullptr) {
-          Vec8<RES> r;
-          r.load(residual + t * a.H + c * 8);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] += r.get(i);
-        }
-        s[p].put(v);
+        x[p].template load<NT>(a.x + t * a.x_stride + c * 8);
+        if (residual != nullptr) s[p].template load<NT>(residual + t * a.H + c * 8);
       }
     }
+  };
+  if (a.stream) load(std::true_type{});
+  else load(std::false_type{});
+  float g[P][8];
+  load_gamma<P>(g, a.gamma, a.gamma_f32, lane, TEAM, chunks);
+  double ss = 0.0;
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-      const int c = lane + p * TEAM;
-      if (sum != nullptr && c < chunks) s[p].store(sum + t * a.H + c * 8);
+  for (int p = 0; p < P; ++p) {
+    const int c = lane + p * TEAM;
+    float v[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(s[p].get(i), s[p].get(i), ss);
+    for (int i = 0; i < 8; ++i) v[i] = residual != nullptr ? x[p].get(i) + s[p].get(i) : x[p].get(i);
+    s[p].put(v);
+    if (sum != nullptr && c < chunks) s[p].store(sum + t * a.H + c * 8);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const double w = s[p].get(i);
+      ss = fma(w, w, ss);
     }
-    ss = team_sum<TEAM>(ss, slots, turn);
-    float rstd = 1.0f / sqrtf(ss / static_cast<float>(a.H) + a.eps);
-    if (!(ss <= 3.4028235e38f)) {
-      // the squares overflow FP32 (values above about 1e19, an infinity or a
-      // NaN; the same in every lane of the row): on values scaled by 2^-80,
-      // beside which eps vanishes
-      float sc = 0.0f;
+  }
+  ss = team_sum<TEAM>(ss, slots);
+  const double r64 = 1.0 / sqrt(ss / a.H + static_cast<double>(a.eps));
+  const float rstd = static_cast<float>(r64), rlow = static_cast<float>(r64 - static_cast<double>(rstd));
+  if (a.rstd != nullptr && lane == 0) a.rstd[t] = rstd;
 #pragma unroll
-      for (int p = 0; p < P; ++p)
+  for (int p = 0; p < P; ++p) {
+    const int c = lane + p * TEAM;
+    if (c >= chunks) continue;
+    float v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float v = s[p].get(i) * 0x1p-80f;
-          sc = fmaf(v, v, sc);
-        }
-      sc = team_sum<TEAM>(sc, slots, turn);
-      rstd = 0x1p-80f / sqrtf(sc / static_cast<float>(a.H));
+    for (int i = 0; i < 8; ++i) {
+      // s (rstd + rlow) = n + low, and its product with gamma rounded once
+      const float x = s[p].get(i), n = x * rstd, low = fmaf(x, rlow, fmaf(x, rstd, -n));
+      v[i] = fmaf(n, g[p][i], low * g[p][i]);
     }
-    if (a.rstd != nullptr && lane == 0) a.rstd[t] = rstd;
-#pragma unroll
-    for (int p = 0; p < P; ++p) {
-      const int c = lane + p * TEAM;
-      if (c >= chunks) continue;
-      float v[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = s[p].get(i) * rstd * g[p][i];
-      Vec8<uint16_t> y;
-      y.put(v);
-      if (a.y != nullptr) y.store(a.y + t * a.H + c * 8);
-      if constexpr (FMT != kMxNone) {   // H % 32 == 0: a quad's lanes are all here or all past the row
-        uint32_t code[2];
-        const uint32_t byte = mx_encode8<FMT>(y.w, code);
-        mx_store8<FMT>(a.codes, a.scales, t * chunks + c, code, byte);
-      }
+    Vec8<uint16_t> y;
+    y.put(v);
+    if (a.y != nullptr) y.store(a.y + t * a.H + c * 8);
+    if constexpr (FMT != kMxNone) {   // H % 32 == 0: a quad's lanes are all here or all past the row
+      uint32_t code[2];
+      const uint32_t byte = mx_encode8<FMT>(y.w, code);
+      mx_store8<FMT>(a.codes, a.scales, t * chunks + c, code, byte);
     }
   }
 }
@@ -204,8 +218,7 @@ template <int TEAM, int P, typename RES, bool DG>
 __global__ void __launch_bounds__(kBwdThreads)
 norm_bwd_kernel(NormBwdArgs a) {
   extern __shared__ __attribute__((aligned(16))) float dg_lds[];   // DG: [teams][H]
-  __shared__ float slots[2 * (kBwdThreads / kWave)];
-  int turn = 0;
+  __shared__ float slots[2][kBwdThreads / kWave];
   const int lane = threadIdx.x % TEAM, team = threadIdx.x / TEAM, chunks = a.H / 8;
   constexpr int kTeams = kBwdThreads / TEAM;
   const int64_t step = static_cast<int64_t>(gridDim.x) * kTeams;
@@ -213,45 +226,48 @@ norm_bwd_kernel(NormBwdArgs a) {
   const RES* dsum = static_cast<const RES*>(a.dsum);
   RES* dres = static_cast<RES*>(a.dres);
   float g[P][8], dg[P][8];
-  load_gamma<P>(g, a.gamma, a.gamma_f32, lane, TEAM, chunks);
 #pragma unroll
   for (int p = 0; p < P; ++p)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) dg[p][i] = 0.0f;
+    for (int i = 0; i < 8; ++i) g[p][i] = dg[p][i] = 0.0f;
+  load_gamma<P>(g, a.gamma, a.gamma_f32, lane, TEAM, chunks);
 
   // TEAM > 64 has a barrier in its sum: every team of the workgroup runs the
   // same iterations, those past the last row without loads or stores
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTeams;
-  for (int64_t tb = t0; tb < a.T; tb += step) {
-    const int64_t t = tb + team;
+  int turn = 0;
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kTeams + team; t - team < a.T; t += step) {
     const bool live = t < a.T;
     const float rstd = live ? a.rstd[t] : 0.0f;
     Vec8<RES> s[P], ds[P];
     Vec8<uint16_t> dy[P];
+    auto load = [&](auto nt) {
+      constexpr bool NT = decltype(nt)::value;
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-      const int c = lane + p * TEAM;
-      s[p].zero();
-      ds[p].zero();
-      dy[p].zero();
-      if (live && c < chunks) {
-        dy[p].load(a.dy + t * a.H + c * 8);
-        s[p].load(s_in + t * a.H + c * 8);
-        if (dsum != nullptr) ds[p].load(dsum + t * a.H + c * 8);
+      for (int p = 0; p < P; ++p) {
+        const int c = lane + p * TEAM;
+        s[p].zero();
+        ds[p].zero();
+        dy[p].zero();
+        if (live && c < chunks) {
+          dy[p].template load<NT>(a.dy + t * a.H + c * 8);
+          s[p].template load<NT>(s_in + t * a.H + c * 8);
+          if (dsum != nullptr) ds[p].template load<NT>(dsum + t * a.H + c * 8);
+        }
       }
-    }
+    };
+    if (a.stream) load(std::true_type{});
+    else load(std::false_type{});
     float inner = 0.0f;
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-      if (lane + p * TEAM >= chunks) continue;
+    for (int p = 0; p < P; ++p)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float n = s[p].get(i) * rstd, d = dy[p].get(i);
         inner = fmaf(d * g[p][i], n, inner);
         if constexpr (DG) dg[p][i] = fmaf(d, n, dg[p][i]);
       }
-    }
-    inner = team_sum<TEAM>(inner, slots, turn) / static_cast<float>(a.H);
+    inner = team_sum<TEAM>(inner, slots[turn]) / static_cast<float>(a.H);
+    turn ^= 1;
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       const int c = lane + p * TEAM;
@@ -324,7 +340,7 @@ zero_f32_kernel(float* p, int n) {
 // Output chunks are flat (K % 32 == 0: the code and scale index of a chunk
 // does not depend on the row length); the input position moves by a fixed
 // (rows, columns) step per iteration.
-template <int FMT>
+template <int FMT, bool NT>
 __global__ void __launch_bounds__(kNormThreads)
 quantize_rows_kernel(const uint16_t* __restrict__ x, int64_t x_stride, int64_t total, int chunks, int64_t step_rows,
                      int step_cols, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, int32_t* offsets,
@@ -335,9 +351,10 @@ quantize_rows_kernel(const uint16_t* __restrict__ x, int64_t x_stride, int64_t t
   int64_t row = i / chunks;
   int col = static_cast<int>(i - row * chunks);
   for (; i < total; i += step) {   // total % 4 == 0: the lanes of a quad leave together
-    const u32x4_t v = *reinterpret_cast<const u32x4_t*>(x + row * x_stride + col * 8);
+    Vec8<uint16_t> v;
+    v.load<NT>(x + row * x_stride + col * 8);
     uint32_t code[2];
-    const uint32_t byte = mx_encode8<FMT>(v, code);
+    const uint32_t byte = mx_encode8<FMT>(v.w, code);
     mx_store8<FMT>(codes, scales, i, code, byte);
     row += step_rows;
     col += step_cols;
@@ -351,10 +368,9 @@ quantize_rows_kernel(const uint16_t* __restrict__ x, int64_t x_stride, int64_t t
 template <int TEAM, int P, typename RES, int FMT>
 void launch_fwd_variant(const NormFwdArgs& a, hipStream_t s) {
   constexpr int kTeams = kNormThreads / TEAM;
-  const int64_t need = (a.T + kTeams - 1) / kTeams;
-  const int64_t most = static_cast<int64_t>(device_cu_count()) * 8;
-  launch_kernel("add_rmsnorm", norm_fwd_kernel<TEAM, P, RES, FMT>,
-                dim3(static_cast<unsigned>(std::max<int64_t>(1, std::min(need, most)))), dim3(kNormThreads), 0, s, a);
+  const int64_t blocks = std::max<int64_t>(1, (a.T + kTeams - 1) / kTeams);
+  launch_kernel("add_rmsnorm", norm_fwd_kernel<TEAM, P, RES, FMT>, dim3(static_cast<unsigned>(blocks)),
+                dim3(kNormThreads), 0, s, a);
 }
 
 template <int TEAM, int P>
@@ -401,11 +417,14 @@ int norm_team(int H) { return H <= 256 ? 16 : H <= 2048 ? 64 : 256; }
 int norm_bwd_blocks(int64_t T, int H) {
   const int teams = kBwdThreads / norm_team(H);
   const int64_t need = (T + teams - 1) / teams;
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(need, 512)));
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(need, 256)));
 }
 
-bool launch_add_rmsnorm(const NormFwdArgs& a, bool res_f32, int format, hipStream_t s) {
-  const int H = a.H;
+bool launch_add_rmsnorm(const NormFwdArgs& args, bool res_f32, int format, hipStream_t s) {
+  NormFwdArgs a = args;
+  const int H = a.H, res = res_f32 ? 4 : 2;
+  a.stream = streams(static_cast<double>(a.T) * H *
+                     (2 + (a.residual ? res : 0) + (a.sum ? res : 0) + (a.y ? 2 : 0) + (a.codes ? 1 : 0)));
   if (H <= 128) launch_fwd_shape<16, 1>(a, res_f32, format, s);
   else if (H <= 256) launch_fwd_shape<16, 2>(a, res_f32, format, s);
   else if (H <= 512) launch_fwd_shape<64, 1>(a, res_f32, format, s);
@@ -417,8 +436,10 @@ bool launch_add_rmsnorm(const NormFwdArgs& a, bool res_f32, int format, hipStrea
   return launch_ok("add_rmsnorm");
 }
 
-bool launch_add_rmsnorm_bwd(const NormBwdArgs& a, bool res_f32, float* dgamma, hipStream_t s) {
-  const int H = a.H;
+bool launch_add_rmsnorm_bwd(const NormBwdArgs& args, bool res_f32, float* dgamma, hipStream_t s) {
+  NormBwdArgs a = args;
+  const int H = a.H, res = res_f32 ? 4 : 2;
+  a.stream = streams(static_cast<double>(a.T) * H * (2 + 2 * res + (a.dsum ? res : 0) + (a.dx ? 2 : 0)));
   if (a.T == 0) {
     if (dgamma == nullptr) return true;
     launch_kernel("add_rmsnorm_dgamma", zero_f32_kernel, dim3((H + kNormThreads - 1) / kNormThreads),
@@ -448,13 +469,16 @@ bool launch_mx_quantize_rows(const uint16_t* x, int64_t x_stride, int64_t T, int
   const int64_t need = (total + kNormThreads - 1) / kNormThreads;
   const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>(need, static_cast<int64_t>(device_cu_count()) * 16));
   const int64_t step = blocks * kNormThreads;
-  const dim3 grid(static_cast<unsigned>(blocks));
+  auto launch = [&](auto kernel) {
+    launch_kernel("mx_quantize_rows", kernel, dim3(static_cast<unsigned>(blocks)), dim3(kNormThreads), 0, s, x,
+                  x_stride, total, chunks, step / chunks, static_cast<int>(step % chunks), codes, scales, offsets, T);
+  };
   if (format == kMxFp8)
-    launch_kernel("mx_quantize_rows", quantize_rows_kernel<kMxFp8>, grid, dim3(kNormThreads), 0, s, x, x_stride,
-                  total, chunks, step / chunks, static_cast<int>(step % chunks), codes, scales, offsets, T);
+    streams(T * (K * (3 + 1 / 32.0))) ? launch(&quantize_rows_kernel<kMxFp8, true>)
+                                            : launch(&quantize_rows_kernel<kMxFp8, false>);
   else
-    launch_kernel("mx_quantize_rows", quantize_rows_kernel<kMxFp4>, grid, dim3(kNormThreads), 0, s, x, x_stride,
-                  total, chunks, step / chunks, static_cast<int>(step % chunks), codes, scales, offsets, T);
+    streams(T * (K * (2.5 + 1 / 32.0))) ? launch(&quantize_rows_kernel<kMxFp4, true>)
+                                              : launch(&quantize_rows_kernel<kMxFp4, false>);
   return launch_ok("mx_quantize_rows");
 }
 
