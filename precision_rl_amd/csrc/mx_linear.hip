@@ -41,9 +41,11 @@ struct LinCfg {
   // 1 KB pieces (one copy of a wave) per stage and per wave; where there are
   // fewer pieces than waves, some waves copy the same piece (the same bytes
   // to the same place), so that every wave has the same count outstanding.
-  // Scales: 64 rows x 4 bytes per copy and step.
-  static constexpr int kRowBlocks = (BM + BN + 63) / 64;
-  static constexpr int NX = BM * kXRow / 1024, NW = BN * kWRow / 1024, NS = kRowBlocks * kScaleSteps;
+  // Scales: 16 rows x four steps x 4 bytes per copy (four lanes a row), read
+  // one word per row and step; against one copy per step and a byte read per
+  // matrix instruction 2 to 15% of the time (T = 1024, N = 4096: 12.8 -> 11.1
+  // us as 64 x 64 with FP4; T = 16384: 130 -> 126 with FP8).
+  static constexpr int NX = BM * kXRow / 1024, NW = BN * kWRow / 1024, NS = (BM + BN) / 16;
   static constexpr int PX = (NX + kWaves - 1) / kWaves, PW = (NW + kWaves - 1) / kWaves,
                        PS = (NS + kWaves - 1) / kWaves;
   static constexpr int kCopies = PX + PW;
@@ -52,8 +54,8 @@ struct LinCfg {
   // group are copied when the stage S before its first has been read, by
   // when the last stage of the group kScaleGroups before it has been, too.
   static constexpr int GS = kScaleSteps / SK, kScaleGroups = (S + 2 * GS - 2) / GS;
-  static constexpr int kScales = S * kStage, kScaleStep = kRowBlocks * 256;
-  static constexpr int kLds = kScales + kScaleGroups * kScaleSteps * kScaleStep;
+  static constexpr int kScales = S * kStage, kScaleRow = kScaleSteps * 4, kScaleGroup = (BM + BN) * kScaleRow;
+  static constexpr int kLds = kScales + kScaleGroups * kScaleGroup;
   static_assert(FT >= 1 && FN >= 1 && FT * 32 * WM == BM && FN * 32 * WN == BN, "whole blocks");
   static_assert(kLds <= 160 * 1024, "LDS of a compute unit");
   static_assert((S - 2) * kCopies + ((S - 2) / GS + 1) * PS + (AHEAD ? kCopies + PS : 0) <= 63, "the vector-memory counter has six bits");
@@ -152,7 +154,7 @@ mx_linear_kernel(LinArgs a) {
   const uint32_t lds0 = lds_addr(lds);
   uint32_t x_off[C::PX], w_off[C::PW], x_dst[C::PX], w_dst[C::PW], s_dst[C::PS];
   const uint8_t* s_src[C::PS];
-  int s_step[C::PS];
+  int s_flip[C::PS];
   uint32_t x_upper = 0, w_upper = 0;   // bit j: the lane's chunk of copy j lies in the stage's second step
 #pragma unroll
   for (int j = 0; j < C::PX; ++j) {
@@ -172,13 +174,11 @@ mx_linear_kernel(LinArgs a) {
   }
 #pragma unroll
   for (int j = 0; j < C::PS; ++j) {
-    // the copies of a row's four steps run one after the other (in one wave or
-    // in neighbouring ones), on one cache line
-    const int piece = (wave + j * C::kWaves) % C::NS, block = piece / kScaleSteps, q = block * 64 + lane;
+    const int piece = (wave + j * C::kWaves) % C::NS, q = piece * 16 + lane / 4;
     s_src[j] = q < C::BM ? a.xs + (m0 + min(q, rows - 1)) * s_pitch
                          : a.ws + (n0 + min(q - C::BM, cols - 1)) * s_pitch;
-    s_step[j] = piece % kScaleSteps;
-    s_dst[j] = lds0 + C::kScales + s_step[j] * C::kScaleStep + block * 256;
+    s_dst[j] = lds0 + C::kScales + piece * 256;
+    s_flip[j] = 2 * (piece & 1);   // the upper 16 of 32 rows: steps 2 3 0 1, so that 32 rows' reads miss each other's banks
   }
   // Issues the copies of the next stage (stages are issued in order).
   int next = 0;
@@ -187,9 +187,9 @@ mx_linear_kernel(LinArgs a) {
     if (next % C::GS == 0) {
 #pragma unroll
       for (int j = 0; j < C::PS; ++j)
-        dma4(s_src[j] + min(next * C::SK + s_step[j], steps - 1) * 4, s_dst[j] + next_group);
-      next_group += kScaleSteps * C::kScaleStep;
-      if (next_group == C::kScaleGroups * kScaleSteps * C::kScaleStep) next_group = 0;
+        dma4(s_src[j] + min(next * C::SK + ((lane & 3) ^ s_flip[j]), steps - 1) * 4, s_dst[j] + next_group);
+      next_group += C::kScaleGroup;
+      if (next_group == C::kScaleGroups * C::kScaleGroup) next_group = 0;
     }
     const uint8_t* xb = x_base + static_cast<int64_t>(next) * C::kXRow;
     const uint8_t* wb = w_base + static_cast<int64_t>(next) * C::kWRow;
@@ -237,41 +237,57 @@ mx_linear_kernel(LinArgs a) {
   // apart, where the slots repeat.
   const int xr = wm * C::TM + r32, wr = wn * C::TN + col_of(r32);
   const uint32_t x_row = xr * C::kXRow, w_row = C::kW + wr * C::kWRow;
-  const uint32_t xs_lane = C::kScales + xr * 4 + h, ws_lane = C::kScales + (C::BM + wr) * 4 + h;
+  const uint32_t xs_row = lds0 + C::kScales + xr * C::kScaleRow, ws_row = lds0 + C::kScales + (C::BM + wr) * C::kScaleRow;
+  const uint32_t xs_flip = (xr & 16) / 2, ws_flip = (wr & 16) / 2;
 
+  using u32_steps = uint32_t __attribute__((ext_vector_type(C::SK)));
   struct Frags {   // one matrix instruction's worth of K
     u32x4_t x[C::FT][C::X8 ? 2 : 1], w[C::FN];
-    int sx[C::FT], sw[C::FN];
+  };
+  struct Scales {   // a stage's: per step the 4 bytes of the rows' 128 elements
+    u32_steps x[C::FT], w[C::FN];
   };
   uint32_t slot = 0, sc = 0;   // LDS offsets of the stage being read and of its first step's scales
   auto advance = [&]() {
     slot += C::kStage;
     if (slot == C::S * C::kStage) slot = 0;
-    sc += C::SK * C::kScaleStep;
-    if (sc == C::kScaleGroups * kScaleSteps * C::kScaleStep) sc = 0;
+    sc += C::SK * 4;
+    if (sc % C::kScaleRow == 0) sc += C::kScaleGroup - C::kScaleRow;   // the next group's first step
+    if (sc == C::kScaleGroups * C::kScaleGroup) sc = 0;
   };
   auto read = [&](auto part, Frags& f) {   // part of the stage: step part / 2, instruction part % 2
     constexpr int kSub = decltype(part)::value / 2, kHalf = decltype(part)::value % 2;
     const uint32_t st = lds0 + slot;
-    const uint32_t xs = opaque_vgpr(lds0 + sc + xs_lane), ws = opaque_vgpr(lds0 + sc + ws_lane);
     const uint32_t wa = opaque_vgpr(st + w_row + slot_of<C::kWRow>(wr, 4 * kSub + 2 * kHalf + h) * 16);
     const uint32_t xa = opaque_vgpr(
         st + x_row + slot_of<C::kXRow>(xr, C::X8 ? 8 * kSub + 4 * kHalf + h : 4 * kSub + 2 * kHalf + h) * 16);
     const uint32_t xb =
         C::X8 ? opaque_vgpr(st + x_row + slot_of<C::kXRow>(xr, 8 * kSub + 4 * kHalf + 2 + h) * 16) : 0u;
 #pragma unroll
-    for (int n = 0; n < C::FN; ++n) {
-      f.sw[n] = *lds_ptr<uint8_t>(ws + kSub * C::kScaleStep + n * 32 * 4 + 2 * kHalf);
-      f.w[n] = *lds_ptr<u32x4_t>(wa + n * 32 * C::kWRow);
-    }
+    for (int n = 0; n < C::FN; ++n) f.w[n] = *lds_ptr<u32x4_t>(wa + n * 32 * C::kWRow);
 #pragma unroll
     for (int t = 0; t < C::FT; ++t) {
-      f.sx[t] = *lds_ptr<uint8_t>(xs + kSub * C::kScaleStep + t * 32 * 4 + 2 * kHalf);
       f.x[t][0] = *lds_ptr<u32x4_t>(xa + t * 32 * C::kXRow);
       if constexpr (C::X8) f.x[t][1] = *lds_ptr<u32x4_t>(xb + t * 32 * C::kXRow);
     }
   };
-  auto multiply = [&](const Frags& f) {
+  auto read_scales = [&](Scales& g) {
+    const uint32_t xs = opaque_vgpr((xs_row + sc) ^ xs_flip), ws = opaque_vgpr((ws_row + sc) ^ ws_flip);
+#pragma unroll
+    for (int n = 0; n < C::FN; ++n) g.w[n] = *lds_ptr<u32_steps>(ws + n * 32 * C::kScaleRow);
+#pragma unroll
+    for (int t = 0; t < C::FT; ++t) g.x[t] = *lds_ptr<u32_steps>(xs + t * 32 * C::kScaleRow);
+  };
+  // The lane's byte of a matrix instruction becomes byte 0 or 2, which the
+  // instruction selects.
+  auto shift_scales = [&](const Scales& g, Scales& o) {
+#pragma unroll
+    for (int n = 0; n < C::FN; ++n) o.w[n] = g.w[n] >> (8u * h);
+#pragma unroll
+    for (int t = 0; t < C::FT; ++t) o.x[t] = g.x[t] >> (8u * h);
+  };
+  auto multiply = [&](auto part, const Frags& f, const Scales& g) {
+    constexpr int kSub = decltype(part)::value / 2, kHalf = decltype(part)::value % 2;
 #pragma unroll
     for (int t = 0; t < C::FT; ++t) {
       i32x8_t xv;
@@ -284,9 +300,10 @@ mx_linear_kernel(LinArgs a) {
       for (int n = 0; n < C::FN; ++n) {
         const i32x8_t wv = {static_cast<int>(f.w[n][0]), static_cast<int>(f.w[n][1]), static_cast<int>(f.w[n][2]),
                             static_cast<int>(f.w[n][3]), 0, 0, 0, 0};
-        // formats: 4 = FP4 E2M1, 0 = FP8 E4M3; scale bytes in bits 7:0
-        acc[n][t] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wv, xv, acc[n][t], 4, C::X8 ? 0 : 4, 0, f.sw[n], 0,
-                                                                    f.sx[t]);
+        // formats: 4 = FP4 E2M1, 0 = FP8 E4M3; scale byte 0 or 2 of the register
+        acc[n][t] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+            wv, xv, acc[n][t], 4, C::X8 ? 0 : 4, 2 * kHalf, static_cast<int>(g.w[n][kSub]), 2 * kHalf,
+            static_cast<int>(g.x[t][kSub]));
       }
     }
   };
@@ -300,19 +317,28 @@ mx_linear_kernel(LinArgs a) {
     // A stage's slot is free once every wave has its last part in registers:
     // at the barrier in front of that part's matrix instructions.
     Frags even, odd;
+    Scales scales, loaded;
+    constexpr std::integral_constant<int, 2 * C::SK - 1> last{};
     for (int s = 0; s < C::S && s < stages; ++s) issue();
     wait_stage(0, std::integral_constant<int, C::S - 1>{});
     barrier();
+    read_scales(loaded);
     read(p0, even);
     for (int st = 0; st < stages; ++st) {
       read(p1, odd);
-      multiply(even);
+      shift_scales(loaded, scales);
+      multiply(p0, even, scales);
       if constexpr (C::SK == 2) {
         if (!odd_steps || st + 1 < stages) {
           read(p2, even);
-          multiply(odd);
+          multiply(p1, odd, scales);
           read(p3, odd);
-          multiply(even);
+          multiply(p2, even, scales);
+        } else {   // the last part's scales are those of the only step
+#pragma unroll
+          for (int n = 0; n < C::FN; ++n) scales.w[n][1] = scales.w[n][0];
+#pragma unroll
+          for (int t = 0; t < C::FT; ++t) scales.x[t][1] = scales.x[t][0];
         }
       }
       wait_lds();
@@ -321,9 +347,10 @@ mx_linear_kernel(LinArgs a) {
         barrier();
         if (next < stages) issue();
         advance();
+        read_scales(loaded);
         read(p0, even);
       }
-      multiply(odd);
+      multiply(last, odd, scales);
     }
   } else {
     for (int s = 0; s < C::S - 1 && s < stages; ++s) issue();
@@ -333,16 +360,19 @@ mx_linear_kernel(LinArgs a) {
       barrier();
       if (next < stages) issue();
       Frags f;
+      Scales scales;
+      read_scales(scales);
       read(p0, f);
-      multiply(f);
+      shift_scales(scales, scales);
+      multiply(p0, f, scales);
       read(p1, f);
-      multiply(f);
+      multiply(p1, f, scales);
       if constexpr (C::SK == 2) {
         if (!odd_steps || st + 1 < stages) {
           read(p2, f);
-          multiply(f);
+          multiply(p2, f, scales);
           read(p3, f);
-          multiply(f);
+          multiply(p3, f, scales);
         }
       }
       advance();
@@ -401,22 +431,22 @@ int64_t tiles_of(const LinArgs& a, int bm, int bn) {
 
 // The tile: the larger, the fewer bytes a product copies, but every CU wants
 // one.
-//   32 x 32 up to 640 tiles (2.5 a CU), then 64 x 64 up to 640 of those: T =
-//     100, N = 4096, K = 2048: 5.6 us against 5.8 with 64 x 64; T = 200: 7.1
-//     against 6.1; T = 500: 7.4 (64 x 64) against 9.3 (128 x 128); T = 1024:
-//     12.5 against 10.6 (FP4; FP8 alike).
+//   32 x 32 up to 256 tiles, then 64 x 64 up to 640 (2.5 a CU): N = 4096, K =
+//     2048, T = 1: 5.8 us against 6.0 with 64 x 64 (FP8; 5.2 either way with
+//     FP4); T = 100: 6.4 against 6.2; T = 200: 7.4 against 6.6; T = 500: 8.8 (64
+//     x 64) against 10.9 (128 x 128); T = 1024: 16.6 against 13.7.
 //   64 x 128 for at most 64 tokens beyond that, half of whose rows a tile of
-//     128 would leave empty: T = 48, N = 65536: 13.4 us as 64 x 64 with FP4,
-//     14.4 against 16.9 with FP8.
+//     128 would leave empty: T = 48, N = 65536: 13.3 us, as 64 x 64, with FP4,
+//     14.0 against 16.4 with FP8.
 //   128 x 128 or 256 x 256 by rounds over the chip: two of the former run on a
 //     CU at once, and a round of 512 takes 1 / 1.6 of a round of 256 of the
 //     latter, its last one 0.65 of that where it has at most one tile a CU.  T
-//     = 5001, K = 4096, N = 2048 (1.25 against 0.6 rounds): 36 against 30 us;
-//     T = 10000, K = 2048 (2.5 against 1.25): 32 against 38; T = 1500, N =
-//     4096: 14 against 17; T = 16384: 100 against 92 (FP4).
+//     = 5001, K = 4096, N = 2048 (1.25 against 0.6 rounds): 35 against 32 us;
+//     T = 10000, K = 2048 (2.5 against 1.25): 32 against 37; T = 1500, N =
+//     4096: 13 against 17; T = 16384: 101 against 93 (FP4).
 template <bool X8>
 bool launch_format(const LinArgs& a, hipStream_t s) {
-  if (tiles_of(a, 32, 32) <= 640) return launch_cfg<LinCfg<X8, 32, 32, 1, 1, 2, 2>>(a, s);
+  if (tiles_of(a, 32, 32) <= 256) return launch_cfg<LinCfg<X8, 32, 32, 1, 1, 2, 2>>(a, s);
   if (tiles_of(a, 64, 64) <= 640) return launch_cfg<LinCfg<X8, 64, 64, 2, 2, 2, 2>>(a, s);
   if (a.T <= 64) return launch_cfg<LinCfg<X8, 64, 128, 2, 2, 2, 2>>(a, s);
   const int64_t n128 = tiles_of(a, 128, 128), n256 = tiles_of(a, 256, 256);
@@ -424,8 +454,8 @@ bool launch_format(const LinArgs& a, hipStream_t s) {
   if (rounds128 <= 1.6 * static_cast<double>((n256 + 255) / 256)) {
     if constexpr (X8) {
       // stages of one step, so that two workgroups fit on a CU; of two steps
-      // (whole cache lines of w) where there is one at most: 256 tiles 12.7
-      // us against 14.9, 384 tiles 21.5 against 19.6
+      // (whole cache lines of w) where there is one at most: 256 tiles 13.7
+      // us against 15.2, 384 tiles 22.2 against 18.3
       if (n128 <= 256) return launch_cfg<LinCfg<true, 128, 128, 4, 2, 2, 2>>(a, s);
       return launch_cfg<LinCfg<true, 128, 128, 2, 2, 2, 2, 1>>(a, s);
     } else {
