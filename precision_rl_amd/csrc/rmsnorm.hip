@@ -12,10 +12,10 @@
 // straight-through backward sees the operand that was quantised.
 //
 // The forward sums the squares in FP64 and multiplies by rstd as the sum of
-// two floats, so that y differs from the rounded exact value only where an FP32
-// rounding next to a midpoint tips it; neither costs time beside HBM, and no
-// row's squares overflow or underflow.  Everything else is FP32.  All calls
-// are bound by HBM: every tensor is read or written once.
+// two floats, and y is rounded once: it is the bf16 nearest to the exact value.
+// That costs no time beside HBM, and no row's squares overflow or underflow.
+// Everything else is FP32.  All calls are bound by HBM: every tensor is read
+// or written once.
 
 #include <algorithm>
 
@@ -109,6 +109,9 @@ __device__ __forceinline__ T team_sum(T v, T* slots) {
   return v;
 }
 
+// Whether v lies halfway between two bf16 values.
+__device__ __forceinline__ bool halfway(float v) { return (__float_as_uint(v) & 0xFFFFu) == 0x8000u; }
+
 template <int P>
 __device__ __forceinline__ void load_gamma(float (&g)[P][8], const void* gamma, bool gamma_f32, int lane, int team,
                                            int chunks) {
@@ -192,12 +195,27 @@ norm_fwd_kernel(NormFwdArgs a) {
   for (int p = 0; p < P; ++p) {
     const int c = lane + p * TEAM;
     if (c >= chunks) continue;
-    float v[8];
+    // s (rstd + rlow) = n + low, and its product with gamma rounded once to
+    // FP32.  Where that lands halfway between two bf16 values (1 of 2^16), it
+    // moves one unit to the side on which the product lies, so that y is not
+    // rounded twice.
+    float v[8], n[8], low[8];
+    bool tie = false;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      // s (rstd + rlow) = n + low, and its product with gamma rounded once
-      const float x = s[p].get(i), n = x * rstd, low = fmaf(x, rlow, fmaf(x, rstd, -n));
-      v[i] = fmaf(n, g[p][i], low * g[p][i]);
+      const float x = s[p].get(i);
+      n[i] = x * rstd;
+      low[i] = fmaf(x, rlow, fmaf(x, rstd, -n[i]));
+      v[i] = fmaf(n[i], g[p][i], low[i] * g[p][i]);
+      tie = tie || halfway(v[i]);
+    }
+    if (tie) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float rest = fmaf(n[i], g[p][i], -v[i]) + low[i] * g[p][i];
+        if (halfway(v[i]) && rest != 0.0f)
+          v[i] = __uint_as_float(__float_as_uint(v[i]) + ((rest < 0.0f) == (v[i] < 0.0f) ? 1 : -1));
+      }
     }
     Vec8<uint16_t> y;
     y.put(v);

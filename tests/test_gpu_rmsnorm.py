@@ -7,7 +7,8 @@ with u = 2^-24 and bf16 results off by at most half a step (2^-8):
   rstd    a lane adds at most 32 squares, a tree of at most 6 + 4 steps joins
           the lanes; then division, addition, square root, reciprocal:
           (42 + 4) u / 2 through the square root, below 32 u.
-  y       rstd's bound and two products: 34 u, and the rounding.
+  y       rstd's bound and two products: 34 u, and the rounding (and one test
+          for the single rounding of the exact value).
   dres    every product and sum a rounding; the inner mean's error is bounded
           by its terms' magnitudes (at most 32 + 10 additions, 3 roundings a term).
   dgamma  as many additions as rows a lane takes plus the joins; 2 roundings a term.
@@ -92,6 +93,22 @@ def test_norm_without_codes_takes_rows_of_eight(b, H):
     print_case("norm_rows_of_eight", H=H)
     out = b.w4a4_add_rmsnorm_fwd(x, g, 1e-5, residual=r, save=True)
     _check_norm(b, x, r, g, 1e-5, out, None)
+
+
+@pytest.mark.parametrize("res,gdt", [("bf16", "bf16"), ("f32", "f32")])
+def test_norm_rounds_once(b, res, gdt):
+    """y is the bf16 nearest to the exact value: of 4e6 values some 30 would be
+    off were the product rounded to FP32 in between (1 of 2^17).  The 64-bit
+    value's own error, below 2^-50 of it, decides a rounding with chance 2^-41."""
+    T, H, eps = 2000, 2048, 2.0 ** -20
+    x, r, g = _inputs(T, H, getattr(torch, {"bf16": "bfloat16", "f32": "float32"}[res]),
+                      getattr(torch, {"bf16": "bfloat16", "f32": "float32"}[gdt]), 41)
+    print_case("norm_rounds_once", res=res)
+    out = b.w4a4_add_rmsnorm_fwd(x, g, eps, residual=r, save=True)
+    y, _ = rmsnorm.forward(_f64(out["sum"]), _f64(g), eps)
+    _, e = np.frexp(y)
+    step = np.ldexp(1.0, np.maximum(e - 1, -126) - 7)
+    assert np.array_equal(_f64(out["y"]), np.rint(y / step) * step)
 
 
 def test_norm_in_place_slices_and_rows_behind(b):
