@@ -510,7 +510,7 @@ w4a4_status w4a4_add_rmsnorm_fwd(
  *   dgamma     [H] float out or NULL; zeros for T = 0.  Its sums run in an
  *              order that depends on T and H alone.
  *   workspace  w4a4_workspace_size(W4A4_WS_RMSNORM_BACKWARD, T, H, ...) bytes
- *              where dgamma is given, else NULL.
+ *              where dgamma is given (0 for few rows), else NULL.
  */
 w4a4_status w4a4_add_rmsnorm_bwd(
     int64_t T, int H, const void* dy, const void* sum, int residual_dtype,

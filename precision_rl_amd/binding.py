@@ -546,14 +546,15 @@ def w4a4_add_rmsnorm_bwd(dy, sum, gamma, rstd, dsum=None, dgamma=True, out=None,
         if res.get("dgamma") is None:
             res["dgamma"] = torch.empty(H, dtype=torch.float32, device=dev)
         nbytes = workspace_size(WS_RMSNORM_BACKWARD, T, H, 0, 1, 1)
-        workspace = _workspace(nbytes, dev, workspace)
+        if nbytes:
+            workspace = _workspace(nbytes, dev, workspace)
     _call(load().w4a4_add_rmsnorm_bwd, dev, T, H, _ptr(dy, "dy", dy.shape, torch.bfloat16, dev),
           _ptr(sum, "sum", dy.shape, sum.dtype, dev), rt, _ptr(gamma, "gamma", (H,), gamma.dtype, dev),
           _dtype(gamma, "gamma"), _ptr(rstd, "rstd", (T,), torch.float32, dev),
           _ptr(dsum, "dsum", dy.shape, sum.dtype, dev), _ptr(res["dres"], "dres", dy.shape, sum.dtype, dev),
           _ptr(res.get("dx"), "dx", dy.shape, torch.bfloat16, dev),
           _ptr(res["dgamma"], "dgamma", (H,), torch.float32, dev) if dgamma else None,
-          workspace.data_ptr() if dgamma else None, workspace.numel() if dgamma else 0)
+          workspace.data_ptr() if nbytes else None, workspace.numel() if nbytes else 0)
     return res
 
 

@@ -251,7 +251,7 @@ size_t w4a4_workspace_size(int kind, int64_t T, int H, int I, int E, int k, int 
   }
   if (kind == W4A4_WS_RMSNORM_BACKWARD) {
     if (T < 0 || H <= 0 || H > kMaxRowLen) return 0;
-    return round_up(static_cast<size_t>(norm_bwd_blocks(T, H)) * H * 4);
+    return round_up(norm_bwd_part_bytes(T, H));
   }
   const int64_t cap = w4a4_rows_capacity(T, k, E, row_align);
   if (cap < 0 || H <= 0) return 0;
@@ -854,15 +854,27 @@ w4a4_status w4a4_add_rmsnorm_bwd(int64_t T, int H, const void* dy, const void* s
   OPTIONAL_PTR(dsum);
   OPTIONAL_PTR(dx);
   if ((st = check_element_ptr("dgamma", dgamma, 4, false)) != W4A4_OK) return st;
-  if (dgamma != nullptr && T > 0) {
-    const size_t need = w4a4_workspace_size(W4A4_WS_RMSNORM_BACKWARD, T, H, 0, 1, 1, 1);
+  const size_t need = dgamma != nullptr && T > 0 ? norm_bwd_part_bytes(T, H) : 0;
+  if (need > 0) {
     if (workspace == nullptr || workspace_bytes < need)
       return fail(W4A4_ERR_WORKSPACE, "workspace needs %zu bytes", need);
     REQUIRE_PTR(workspace);
   }
-  const NormBwdArgs a{T, H, static_cast<const uint16_t*>(dy), sum, gamma, gamma_dtype == W4A4_F32, rstd, dsum, dres,
-                      static_cast<uint16_t*>(dx), dgamma != nullptr ? static_cast<float*>(workspace) : nullptr, false};
-  if (!launch_add_rmsnorm_bwd(a, residual_dtype == W4A4_F32, dgamma, static_cast<hipStream_t>(stream)))
+  NormBwdArgs a{};
+  a.T = T;
+  a.H = H;
+  a.dy = static_cast<const uint16_t*>(dy);
+  a.sum = sum;
+  a.gamma = gamma;
+  a.gamma_f32 = gamma_dtype == W4A4_F32;
+  a.rstd = rstd;
+  a.dsum = dsum;
+  a.dres = dres;
+  a.dx = static_cast<uint16_t*>(dx);
+  a.dgamma = dgamma;
+  a.part = need > 0 ? static_cast<float*>(workspace) : nullptr;
+  a.in_place = dres == dy || dres == sum || (dx != nullptr && (dx == dy || dx == sum));
+  if (!launch_add_rmsnorm_bwd(a, residual_dtype == W4A4_F32, static_cast<hipStream_t>(stream)))
     return W4A4_ERR_LAUNCH;
   return W4A4_OK;
 }

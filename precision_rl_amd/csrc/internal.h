@@ -203,8 +203,8 @@ struct NormFwdArgs {
 };
 bool launch_add_rmsnorm(const NormFwdArgs& a, bool res_f32, int format, hipStream_t s);
 
-// Its backward.  part: norm_bwd_blocks(T, H) rows of H floats of scratch, or
-// null where dgamma is.
+// Its backward.  part: norm_bwd_part_bytes(T, H) of scratch, null where that
+// is 0 or dgamma is null.  in_place: dres or dx overlaps dy or sum.
 struct NormBwdArgs {
   int64_t T;
   int H;
@@ -216,11 +216,13 @@ struct NormBwdArgs {
   const void* dsum;
   void* dres;
   uint16_t* dx;
+  float* dgamma;
   float* part;
+  bool in_place;
   bool stream;   // set by the launch: non-temporal loads
 };
-int norm_bwd_blocks(int64_t T, int H);
-bool launch_add_rmsnorm_bwd(const NormBwdArgs& a, bool res_f32, float* dgamma, hipStream_t s);
+size_t norm_bwd_part_bytes(int64_t T, int H);
+bool launch_add_rmsnorm_bwd(const NormBwdArgs& a, bool res_f32, hipStream_t s);
 
 // MXFP4 / MXFP8 of T bf16 rows of K elements (K % 32 == 0), x_stride elements apart.
 bool launch_mx_quantize_rows(const uint16_t* x, int64_t x_stride, int64_t T, int K, int format, uint8_t* codes,

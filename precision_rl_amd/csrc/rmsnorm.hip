@@ -29,6 +29,7 @@ typedef float floatx4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kNormThreads = 256;
 constexpr int kBwdThreads = 512;
+constexpr int kFewRows = 512;
 
 // Whether a call's loads are non-temporal: where it moves more than three
 // quarters of the 256 MiB memory-side cache, its inputs cannot all still lie
@@ -232,14 +233,20 @@ norm_fwd_kernel(NormFwdArgs a) {
 // As the forward, 512 threads; DG: each lane sums dy n of its columns over
 // its rows in FP32, the workgroup's teams add theirs in LDS in team order and
 // write one row of `part`, which dgamma_kernel adds in workgroup order.
+//
+// Up to kFewRows rows dgamma comes from the rows themselves instead, which lie
+// in the L2 then: column_sums' workgroups follow the rows' in one launch and
+// read them a second time.  Against partial rows and their sum, H = 2048, bf16:
+// T = 61 4.0 us against 7.2, T = 512 4.7 against 8.5, T = 1024 8.1 against 9.3, T
+// = 2048 16.6 against 11.9; H = 8192 in FP32: T = 512 17.3 against 17.6, T =
+// 1024 31.0 against 27.7; H = 512: T = 512 4.1 against 5.9, T = 2048 11.7 against 6.0.
 template <int TEAM, int P, typename RES, bool DG>
-__global__ void __launch_bounds__(kBwdThreads)
-norm_bwd_kernel(NormBwdArgs a) {
+__device__ __forceinline__ void norm_bwd_rows(const NormBwdArgs& a, int block, int blocks) {
   extern __shared__ __attribute__((aligned(16))) float dg_lds[];   // DG: [teams][H]
   __shared__ float slots[2][kBwdThreads / kWave];
   const int lane = threadIdx.x % TEAM, team = threadIdx.x / TEAM, chunks = a.H / 8;
   constexpr int kTeams = kBwdThreads / TEAM;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kTeams;
+  const int64_t step = static_cast<int64_t>(blocks) * kTeams;
   const RES* s_in = static_cast<const RES*>(a.sum);
   const RES* dsum = static_cast<const RES*>(a.dsum);
   RES* dres = static_cast<RES*>(a.dres);
@@ -253,7 +260,7 @@ norm_bwd_kernel(NormBwdArgs a) {
   // TEAM > 64 has a barrier in its sum: every team of the workgroup runs the
   // same iterations, those past the last row without loads or stores
   int turn = 0;
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kTeams + team; t - team < a.T; t += step) {
+  for (int64_t t = static_cast<int64_t>(block) * kTeams + team; t - team < a.T; t += step) {
     const bool live = t < a.T;
     const float rstd = live ? a.rstd[t] : 0.0f;
     Vec8<RES> s[P], ds[P];
@@ -316,13 +323,70 @@ norm_bwd_kernel(NormBwdArgs a) {
       d[1] = floatx4_t{dg[p][4], dg[p][5], dg[p][6], dg[p][7]};
     }
     __syncthreads();
-    float* out = a.part + static_cast<int64_t>(blockIdx.x) * a.H;
+    float* out = a.part + static_cast<int64_t>(block) * a.H;
     for (int h = threadIdx.x; h < a.H; h += kBwdThreads) {
       float v = dg_lds[h];
 #pragma unroll
       for (int w = 1; w < kTeams; ++w) v += dg_lds[w * a.H + h];
       out[h] = v;
     }
+  }
+}
+
+template <int TEAM, int P, typename RES, bool DG>
+__global__ void __launch_bounds__(kBwdThreads)
+norm_bwd_kernel(NormBwdArgs a) {
+  norm_bwd_rows<TEAM, P, RES, DG>(a, blockIdx.x, gridDim.x);
+}
+
+// dgamma of 64 columns: lane l of eight takes the columns 8 l .. +7 of rows r,
+// r + 64, ..., whose sums are added over a wave's eight r, then in wave order.
+template <typename RES>
+__device__ __forceinline__ void column_sums(const NormBwdArgs& a, int block) {
+  __shared__ float sums[kBwdThreads / kWave][kWave];
+  const int lane = threadIdx.x % 8, first = threadIdx.x / 8, wave = threadIdx.x / kWave;
+  const int64_t c = static_cast<int64_t>(block) * kWave + lane * 8;
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+  if (c < a.H) {
+#pragma unroll 4
+    for (int64_t t = first; t < a.T; t += kBwdThreads / 8) {
+      Vec8<uint16_t> dy;
+      Vec8<RES> s;
+      dy.load(a.dy + t * a.H + c);
+      s.load(static_cast<const RES*>(a.sum) + t * a.H + c);
+      const float rstd = a.rstd[t];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = fmaf(dy.get(i), s.get(i) * rstd, v[i]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+#pragma unroll
+    for (int off = 8; off < kWave; off <<= 1) v[i] += __shfl_xor(v[i], off, kWave);
+    if (threadIdx.x % kWave < 8) sums[wave][lane * 8 + i] = v[i];
+  }
+  __syncthreads();
+  const int64_t h = static_cast<int64_t>(block) * kWave + threadIdx.x;
+  if (threadIdx.x < kWave && h < a.H) {
+    float d = sums[0][threadIdx.x];
+#pragma unroll
+    for (int w = 1; w < kBwdThreads / kWave; ++w) d += sums[w][threadIdx.x];
+    a.dgamma[h] = d;
+  }
+}
+
+// Workgroups first, first + 1, ... of `rows` workgroups over rows and the
+// column sums' behind them.
+template <int TEAM, int P, typename RES>
+__global__ void __launch_bounds__(kBwdThreads)
+norm_bwd_few_kernel(NormBwdArgs a, int first, int rows) {
+  const int block = blockIdx.x + first;
+  if (block < rows) {
+    norm_bwd_rows<TEAM, P, RES, false>(a, block, rows);
+  } else {
+    column_sums<RES>(a, block - rows);
   }
 }
 
@@ -417,8 +481,29 @@ bool launch_bwd_variant(const NormBwdArgs& a, int blocks, hipStream_t s) {
   return true;
 }
 
+// The column sums read dy and sum, which the rows may be written over: then
+// they go first.
+template <int TEAM, int P, typename RES>
+bool launch_bwd_few(const NormBwdArgs& a, hipStream_t s) {
+  constexpr int kTeams = kBwdThreads / TEAM;
+  const int rows = static_cast<int>((a.T + kTeams - 1) / kTeams), columns = (a.H + kWave - 1) / kWave;
+  auto launch = [&](int first, int blocks) {
+    launch_kernel("add_rmsnorm_bwd", norm_bwd_few_kernel<TEAM, P, RES>, dim3(blocks), dim3(kBwdThreads), 0, s, a, first,
+                  rows);
+  };
+  if (a.in_place) {
+    launch(rows, columns);
+    launch(0, rows);
+  } else {
+    launch(0, rows + columns);
+  }
+  return true;
+}
+
 template <int TEAM, int P>
 bool launch_bwd_shape(const NormBwdArgs& a, bool res_f32, int blocks, hipStream_t s) {
+  if (a.dgamma != nullptr && a.T <= kFewRows)
+    return res_f32 ? launch_bwd_few<TEAM, P, float>(a, s) : launch_bwd_few<TEAM, P, uint16_t>(a, s);
   if (res_f32)
     return a.part ? launch_bwd_variant<TEAM, P, float, true>(a, blocks, s)
                   : launch_bwd_variant<TEAM, P, float, false>(a, blocks, s);
@@ -430,12 +515,17 @@ bool launch_bwd_shape(const NormBwdArgs& a, bool res_f32, int blocks, hipStream_
 // rows share a wave.
 int norm_team(int H) { return H <= 256 ? 16 : H <= 2048 ? 64 : 256; }
 
-}  // namespace
-
-int norm_bwd_blocks(int64_t T, int H) {
+// Workgroups over rows, and rows of scratch that they take with dgamma.
+int bwd_blocks(int64_t T, int H) {
   const int teams = kBwdThreads / norm_team(H);
   const int64_t need = (T + teams - 1) / teams;
   return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(need, 256)));
+}
+
+}  // namespace
+
+size_t norm_bwd_part_bytes(int64_t T, int H) {
+  return T <= kFewRows ? 0 : static_cast<size_t>(bwd_blocks(T, H)) * H * 4;
 }
 
 bool launch_add_rmsnorm(const NormFwdArgs& args, bool res_f32, int format, hipStream_t s) {
@@ -454,17 +544,17 @@ bool launch_add_rmsnorm(const NormFwdArgs& args, bool res_f32, int format, hipSt
   return launch_ok("add_rmsnorm");
 }
 
-bool launch_add_rmsnorm_bwd(const NormBwdArgs& args, bool res_f32, float* dgamma, hipStream_t s) {
+bool launch_add_rmsnorm_bwd(const NormBwdArgs& args, bool res_f32, hipStream_t s) {
   NormBwdArgs a = args;
   const int H = a.H, res = res_f32 ? 4 : 2;
   a.stream = streams(static_cast<double>(a.T) * H * (2 + 2 * res + (a.dsum ? res : 0) + (a.dx ? 2 : 0)));
   if (a.T == 0) {
-    if (dgamma == nullptr) return true;
+    if (a.dgamma == nullptr) return true;
     launch_kernel("add_rmsnorm_dgamma", zero_f32_kernel, dim3((H + kNormThreads - 1) / kNormThreads),
-                  dim3(kNormThreads), 0, s, dgamma, H);
+                  dim3(kNormThreads), 0, s, a.dgamma, H);
     return launch_ok("add_rmsnorm_dgamma");
   }
-  const int blocks = norm_bwd_blocks(a.T, H);
+  const int blocks = bwd_blocks(a.T, H);
   bool ok = false;
   if (H <= 128) ok = launch_bwd_shape<16, 1>(a, res_f32, blocks, s);
   else if (H <= 256) ok = launch_bwd_shape<16, 2>(a, res_f32, blocks, s);
@@ -474,9 +564,9 @@ bool launch_add_rmsnorm_bwd(const NormBwdArgs& args, bool res_f32, float* dgamma
   else if (H <= 4096) ok = launch_bwd_shape<256, 2>(a, res_f32, blocks, s);
   else if (H <= 8192) ok = launch_bwd_shape<256, 4>(a, res_f32, blocks, s);
   if (!ok || !launch_ok("add_rmsnorm_bwd")) return false;
-  if (dgamma == nullptr) return true;
+  if (a.part == nullptr) return true;
   launch_kernel("add_rmsnorm_dgamma", dgamma_kernel, dim3((H + kWave - 1) / kWave), dim3(kDgThreads), 0, s,
-                static_cast<const float*>(a.part), blocks, H, dgamma);
+                static_cast<const float*>(a.part), blocks, H, a.dgamma);
   return launch_ok("add_rmsnorm_dgamma");
 }
 

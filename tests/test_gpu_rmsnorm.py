@@ -162,7 +162,8 @@ def test_norm_extreme_rows(b):
 
 
 @pytest.mark.parametrize("T,H", [(1, 32), (5, 96), (3, 128), (131, 256), (2, 288), (9, 512), (4, 1000), (1, 2048),
-                                 (61, 2048), (5, 2080), (3, 4096), (2, 8192), (5000, 64), (9000, 160)])
+                                 (61, 2048), (5, 2080), (3, 4096), (2, 8192), (5000, 64), (9000, 160),
+                                 (300, 392), (640, 392), (700, 1024), (513, 2048), (770, 2080), (600, 8192)])
 @pytest.mark.parametrize("res", ["bf16", "f32"])
 def test_norm_backward(b, T, H, res):
     rt = torch.bfloat16 if res == "bf16" else torch.float32
@@ -205,8 +206,8 @@ def test_norm_backward_in_place_without_dgamma_and_empty(b):
     got = b.w4a4_add_rmsnorm_bwd(dy, s, g, r, dsum=over, dgamma=False, out=dict(dres=over))
     assert "dgamma" not in got and torch.equal(over, ref["dres"])
     over = dy.clone()
-    b.w4a4_add_rmsnorm_bwd(over, s, g, r, dsum=ds, out=dict(dres=over))
-    assert torch.equal(over, ref["dres"])
+    got = b.w4a4_add_rmsnorm_bwd(over, s, g, r, dsum=ds, out=dict(dres=over))
+    assert torch.equal(over, ref["dres"]) and torch.equal(got["dgamma"], ref["dgamma"])
     none = b.w4a4_add_rmsnorm_bwd(dy[:0], s[:0], g, r[:0], out=dict(dgamma=torch.full((H,), 7.0, device="cuda")))
     assert none["dres"].shape == (0, H) and not none["dgamma"].any()
 

@@ -82,14 +82,14 @@ def test_norm_refusals(lib, p):
     assert b(rdt=5) == INVALID and b(gdt=5) == INVALID
     assert b(rdt=F32) == INVALID                   # dres over a bf16 dy
     assert b(dsum=_off(p)) == INVALID and b(dx=_off(p)) == INVALID and b(dgamma=_off(p)) == INVALID
-    assert b(ws=None) == WORKSPACE and b(wsb=16) == WORKSPACE
+    assert b(T=600, ws=None) == WORKSPACE and b(T=600, wsb=16) == WORKSPACE
     assert b(T=0, dy=None, total=None, gamma=None, rstd=None, dres=None, dgamma=None, ws=None, wsb=0) == 0
 
 
 def test_norm_workspace_size(lib):
     size = lambda T, H: lib.w4a4_workspace_size(6, T, H, 0, 1, 1, 1)  # noqa: E731
-    assert size(1, 64) >= 64 * 4
-    assert size(16384, 2048) > size(16, 2048)
+    assert size(1, 64) == 0 and size(600, 64) >= 64 * 4      # none for few rows
+    assert size(16384, 2048) > size(600, 2048)
     assert size(-1, 64) == 0 and size(4, 0) == 0 and size(4, 16384) == 0
 
 
