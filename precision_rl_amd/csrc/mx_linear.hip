@@ -44,7 +44,7 @@ struct LinCfg {
   // Scales: 16 rows x four steps x 4 bytes per copy (four lanes a row), read
   // one word per row and step; against one copy per step and a byte read per
   // matrix instruction 2 to 15% of the time (T = 1024, N = 4096: 12.8 -> 11.1
-  // us as 64 x 64 with FP4; T = 16384: 130 -> 126 with FP8).
+  // us as 64 x 64 with FP4; T = 16384: 130 -> 126 as 256 x 256 with FP8).
   static constexpr int NX = BM * kXRow / 1024, NW = BN * kWRow / 1024, NS = (BM + BN) / 16;
   static constexpr int PX = (NX + kWaves - 1) / kWaves, PW = (NW + kWaves - 1) / kWaves,
                        PS = (NS + kWaves - 1) / kWaves;
@@ -438,29 +438,32 @@ int64_t tiles_of(const LinArgs& a, int bm, int bn) {
 //   64 x 128 for at most 64 tokens beyond that, half of whose rows a tile of
 //     128 would leave empty: T = 48, N = 65536: 13.3 us, as 64 x 64, with FP4,
 //     14.0 against 16.4 with FP8.
-//   128 x 128 or 256 x 256 by rounds over the chip: two of the former run on a
-//     CU at once, and a round of 512 takes 1 / 1.6 of a round of 256 of the
+//   FP4: 128 x 128 or 256 x 256 by rounds over the chip: two of the former run
+//     on a CU at once, and a round of 512 takes 1 / 1.6 of a round of 256 of the
 //     latter, its last one 0.65 of that where it has at most one tile a CU.  T
 //     = 5001, K = 4096, N = 2048 (1.25 against 0.6 rounds): 35 against 32 us;
 //     T = 10000, K = 2048 (2.5 against 1.25): 32 against 37; T = 1500, N =
-//     4096: 13 against 17; T = 16384: 101 against 93 (FP4).
+//     4096: 13 against 17; T = 16384: 101 against 93.
+//   FP8, whose instructions take twice as long per byte of w: 128 x 128 with
+//     stages of two steps for at most one tile a CU; 128 x 256, two of which run
+//     on a CU at once, beyond: 256 tiles of 128 x 128 12.8 us against 16.9, 320
+//     21.1 against 16.7; and 256 x 256 where one round of it does and at least
+//     three in five CUs have a tile: T = 6000, K = 4096, N = 2048 (192 tiles) 48
+//     against 51, T = 2048, K = 2048, N = 4096 (128) 25 against 20, T = 10000
+//     (640) 85 against 74.
 template <bool X8>
 bool launch_format(const LinArgs& a, hipStream_t s) {
   if (tiles_of(a, 32, 32) <= 256) return launch_cfg<LinCfg<X8, 32, 32, 1, 1, 2, 2>>(a, s);
   if (tiles_of(a, 64, 64) <= 640) return launch_cfg<LinCfg<X8, 64, 64, 2, 2, 2, 2>>(a, s);
   if (a.T <= 64) return launch_cfg<LinCfg<X8, 64, 128, 2, 2, 2, 2>>(a, s);
   const int64_t n128 = tiles_of(a, 128, 128), n256 = tiles_of(a, 256, 256);
-  const double rounds128 = static_cast<double>(n128 / 512) + (n128 % 512 > 256 ? 1.0 : n128 % 512 > 0 ? 0.65 : 0.0);
-  if (rounds128 <= 1.6 * static_cast<double>((n256 + 255) / 256)) {
-    if constexpr (X8) {
-      // stages of one step, so that two workgroups fit on a CU; of two steps
-      // (whole cache lines of w) where there is one at most: 256 tiles 13.7
-      // us against 15.2, 384 tiles 22.2 against 18.3
-      if (n128 <= 256) return launch_cfg<LinCfg<true, 128, 128, 4, 2, 2, 2>>(a, s);
-      return launch_cfg<LinCfg<true, 128, 128, 2, 2, 2, 2, 1>>(a, s);
-    } else {
+  if constexpr (X8) {
+    if (n128 <= 256) return launch_cfg<LinCfg<true, 128, 128, 4, 2, 2, 2>>(a, s);
+    if (n256 <= 150 || n256 > 256) return launch_cfg<LinCfg<true, 128, 256, 2, 4, 2, 2, 1, false>>(a, s);
+  } else {
+    const double rounds128 = static_cast<double>(n128 / 512) + (n128 % 512 > 256 ? 1.0 : n128 % 512 > 0 ? 0.65 : 0.0);
+    if (rounds128 <= 1.6 * static_cast<double>((n256 + 255) / 256))
       return launch_cfg<LinCfg<false, 128, 128, 2, 2, 2, 2>>(a, s);
-    }
   }
   // 16 waves of 64 x 64, whose registers a second set of operands would not
   // fit in; with FP8 stages of one step, for the ring to fit in LDS
