@@ -65,6 +65,10 @@ KERNEL_SOURCES = {
 }
 for _n in ("dual_dO", "cols_a", "cols_w2", "cols_w1", "cols_xp"):
     KERNEL_SOURCES["mx8_quant_" + _n] = "mx8.hip"
+KERNEL_SOURCES.update({"add_rmsnorm": "rmsnorm.hip", "add_rmsnorm_bwd": "rmsnorm.hip",
+                       "add_rmsnorm_dgamma": "rmsnorm.hip", "mx_linear": "mx_linear.hip"})
+# the dense MX product by the format of its activations (FP8 x FP4 runs at the FP8 rate)
+LINEAR_PEAK = {"mxfp4": PEAK_MFMA_FP4_TFLOPS, "mxfp8": PEAK_MFMA_FP8_TFLOPS}
 
 
 def algorithmic_work(T, H, E, k, I):
@@ -145,6 +149,20 @@ def linear_work(T, K, N):
     # the K split of the weight gradient (2 pieces at this shape on 256 CUs):
     # read the FP32 sums of the pieces, write bf16 dW
     by["splitk_reduce"] = N * K * (2 * 4 + 2)
+    return fl, by
+
+
+def linear_mx_work(T, K, N, recipe):
+    """Per-launch algorithmic flops / bytes of the pre-norm + dense MX linear step."""
+    fl = {n: 2.0 * T * K * N for n in ("mx_linear", "gemm_linear_dgrad", "gemm_linear_wgrad")}
+    codes = (K if recipe == "mxfp8" else K // 2) + K // 32
+    by = {
+        # read x, the residual and gamma; write the sum, y, codes, scales and rstd
+        "add_rmsnorm": T * (K * 2 * 4 + codes + 4) + K * 2,
+        # read dy, the sum, the residual stream's gradient, rstd and gamma; write the gradient
+        "add_rmsnorm_bwd": T * (K * 2 * 4 + 4) + K * 2,
+        "splitk_reduce": N * K * (2 * 4 + 2),
+    }
     return fl, by
 
 
@@ -247,6 +265,107 @@ def main_linear(args):
     if not args.no_cpu_baseline:
         print("[bench] timing the FP64 oracle on the host", file=sys.stderr, flush=True)
         out["cpu_baseline"] = cpu_baseline_linear(xb, wb, dyb, tokens=T)
+    print(json.dumps(out), flush=True)
+
+
+LINEAR_MX_METRIC = "Pre-norm + MX dense linear fwd+bwd tokens/s, Qwen3-30B-A3B q projection"
+
+
+def cpu_baseline_linear_mx(x, res, w, dy, dout, recipe, tokens):
+    """The FP64 oracle's pre-norm and MX linear, forward and backward, on the first `tokens` tokens."""
+    from oracle import mxfp4, nvfp4 as q, rmsnorm
+    try:
+        from threadpoolctl import threadpool_info
+        threads = max([p.get("num_threads", 1) for p in threadpool_info()] + [1])
+    except Exception:  # pragma: no cover
+        threads = 1
+    xf, rf, dyf, df = (q.bf16_bits_to_f64(v[:tokens]) for v in (x, res, dy, dout))
+    wf = q.bf16_bits_to_f64(w)
+    t0 = time.perf_counter()
+    s = q.round_bf16(xf + rf)
+    gamma = np.ones(w.shape[1])
+    yn, rstd = rmsnorm.forward(s, gamma, 1e-6)
+    yn = q.round_bf16(yn)
+    a = mxfp4.mx8_along_rows(yn) if recipe == "mxfp8" else mxfp4.block_values_mx(*mxfp4.quantize_rows_mx(yn))
+    q.round_bf16(a @ mxfp4.block_values_mx(*mxfp4.quantize_rows_mx(wf)).T)
+    dyn = q.round_bf16(dyf @ wf)
+    q.round_bf16(dyf.T @ yn)
+    rmsnorm.backward(dyn, s, gamma, rstd, df)
+    dt = time.perf_counter() - t0
+    return {"value": tokens / dt, "unit": "tokens/s", "cores": int(threads), "kind": "oracle",
+            "sample": f"{tokens} tokens of the pre-norm + {recipe.upper()} linear workload (K={w.shape[1]}, "
+                      f"N={w.shape[0]}), FP64 numpy, norm + quantize (x and W) + forward + backward, {dt:.1f} s",
+            "seconds": dt, **host_info()}
+
+
+def main_linear_mx(args):
+    """One pre-normed projection of the layer in an MX recipe: residual addition, RMS norm and
+    encoding, the product, its straight-through backward and the norm's."""
+    import torch
+    from precision_rl_amd import binding as b, synth
+
+    T, K, N = LINEAR["T"], LINEAR["K"], LINEAR["N"]
+    rng = np.random.Generator(np.random.PCG64(np.random.SeedSequence(1006)))
+    xb, rb, db = (synth.normal_bf16(rng, (T, K)) for _ in range(3))
+    wb = synth.normal_bf16(rng, (N, K), synth.W_STD)
+    dyb = synth.normal_bf16(rng, (T, N))
+    dev = torch.device("cuda:0")
+
+    def bf(bits):
+        return torch.from_numpy(bits.view(np.int16)).view(torch.bfloat16).to(dev)
+
+    def empty(dtype, *shape):
+        return torch.empty(*shape, dtype=dtype, device=dev)
+
+    x, res, W, dy, dout = bf(xb), bf(rb), bf(wb), bf(dyb), bf(db)
+    gamma = torch.ones(K, dtype=torch.bfloat16, device=dev)
+    fmt = b.MX_FP8 if args.recipe == "mxfp8" else b.MX_FP4
+    wq = b.w4a4_mx_quantize_rows(W, b.MX_FP4)     # offline, untimed
+    norm = dict(sum=empty(torch.bfloat16, T, K), y=empty(torch.bfloat16, T, K), rstd=empty(torch.float32, T),
+                codes=empty(torch.uint8, T, K if fmt == b.MX_FP8 else K // 2),
+                scales=empty(torch.uint8, T, K // 32), offsets=empty(torch.int32, 2))
+    y = empty(torch.bfloat16, T, N)
+    grads = dict(dx=empty(torch.bfloat16, T, K), dw=empty(torch.bfloat16, N, K))
+    back = dict(dres=empty(torch.bfloat16, T, K), dgamma=empty(torch.float32, K))
+    ws_b = empty(torch.uint8, b.workspace_size(b.WS_LINEAR_BACKWARD, 0, K, N, 1, 1, 1))
+    ws_n = empty(torch.uint8, max(1, b.workspace_size(b.WS_RMSNORM_BACKWARD, T, K, 0, 1, 1, 1)))
+    calibration_copy(torch, dev)
+
+    def step():
+        xq = b.w4a4_add_rmsnorm_fwd(x, gamma, 1e-6, residual=res, fmt=fmt, save=True, out=norm)
+        b.w4a4_mx_linear_fwd(xq, wq, T, K, N, y=y)
+        b.w4a4_linear_bwd(dy, xq["y"], W, xq, T, K, N, out=grads, workspace=ws_b)
+        b.w4a4_add_rmsnorm_bwd(grads["dx"], xq["sum"], gamma, xq["rstd"], dsum=dout, out=back, workspace=ws_n)
+
+    flush = Flusher(torch, dev)
+    st, kern = time_steps(b, torch, step, args, flush, "pre-norm + linear step")
+    ms = st["median"]
+    fl, by = linear_mx_work(T, K, N, args.recipe)
+    KERNEL_PEAK["mx_linear"] = LINEAR_PEAK[args.recipe]
+    per_kernel, roof = summarize(kern, ms, args.steps, fl, by, concurrent={})
+    out = {
+        "metric": LINEAR_MX_METRIC,
+        "value": round(T / (ms * 1e-3), 1),
+        "unit": "tokens/s",
+        "n_gpus": 1,
+        "steps": args.steps,
+        "warmup": args.warmup,
+        "ms_per_step": round(ms, 4),
+        "timing": time_fields(st, args.steps),
+        "higher_is_better": True,
+        "scaling": "weak",
+        "vs_baseline": None,
+        "dtype": f"{args.recipe} x mxfp4 scaled MFMA fwd, bf16 MFMA bwd, fp32 accumulate",
+        "data": "synthetic (seeded; random-init weight of the layer's shape)",
+        "config": {"workload": f"linear: add + RMS norm + {args.recipe.upper()} encode, MX linear fwd, BF16 STE bwd, "
+                               "norm bwd", "T": T, "K": K, "N": N},
+        "roofline": roof,
+        "step_mfma_tflops": round(sum(fl.values()) / (ms * 1e-3) / 1e12, 1),
+        "kernels": per_kernel,
+    }
+    if not args.no_cpu_baseline:
+        print("[bench] timing the FP64 oracle on the host", file=sys.stderr, flush=True)
+        out["cpu_baseline"] = cpu_baseline_linear_mx(xb, rb, wb, dyb, db, args.recipe, tokens=args.cpu_tokens)
     print(json.dumps(out), flush=True)
 
 
@@ -660,11 +779,14 @@ def main():
                     help="learner: the straight-through backward's GEMM operands -- bf16 (the "
                          "default) or mxfp8 (E4M3 + E8M0 per 32 along each GEMM's reduction axis, "
                          "scaled FP8 MFMA; routes with row_align 128)")
-    ap.add_argument("--recipe", choices=["nvfp4", "mxfp4"], default="nvfp4",
-                    help="learner and qp: the forward's format -- nvfp4 (E4M3 per 16 + FP32 outer "
+    ap.add_argument("--recipe", choices=["nvfp4", "mxfp4", "mxfp8"], default="nvfp4",
+                    help="the forward's format -- nvfp4 (E4M3 per 16 + FP32 outer "
                          "scales, exact f16 decode, the default) or mxfp4 (E8M0 per 32, scaled "
-                         "FP4 MFMA)")
+                         "FP4 MFMA); linear: with mxfp4 or mxfp8 (the activations') the projection "
+                         "with its pre-norm")
     args = ap.parse_args()
+    if args.recipe == "mxfp8" and args.workload != "linear":
+        ap.error("--recipe mxfp8 is a recipe of --workload linear")
     if args.gpus != 1:
         print(f"bench.py: the benchmark runs on one GPU only (asked for --gpus {args.gpus}); "
               "the library's expert path is single-GPU (sharding is described in the design notes).",
@@ -672,7 +794,7 @@ def main():
         sys.exit(2)
 
     if args.workload == "linear":
-        return main_linear(args)
+        return main_linear(args) if args.recipe == "nvfp4" else main_linear_mx(args)
     if args.workload == "qp":
         return main_qp(args)
 
