@@ -119,7 +119,7 @@ struct LinArgs {
 template <class C>
 __global__ void __launch_bounds__(C::kThreads, C::OCC)
 mx_linear_kernel(LinArgs a) {
-  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  extern __shared__ __attribute__((aligned(256))) uint8_t lds[];   // rows of at most 256 bytes
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave % C::WM, wn = wave / C::WM;
@@ -152,8 +152,8 @@ mx_linear_kernel(LinArgs a) {
   // Copy sources and destinations; rows past the operand are clamped to its
   // last (they feed only outputs that are not stored).
   const uint32_t lds0 = lds_addr(lds);
-  uint32_t x_off[C::PX], w_off[C::PW], x_dst[C::PX], w_dst[C::PW], s_dst[C::PS];
-  const uint8_t* s_src[C::PS];
+  uint32_t x_off[C::PX], w_off[C::PW], s_off[C::PS], x_dst[C::PX], w_dst[C::PW], s_dst[C::PS];
+  const uint8_t* s_base[C::PS];
   int s_flip[C::PS];
   uint32_t x_upper = 0, w_upper = 0;   // bit j: the lane's chunk of copy j lies in the stage's second step
 #pragma unroll
@@ -174,9 +174,10 @@ mx_linear_kernel(LinArgs a) {
   }
 #pragma unroll
   for (int j = 0; j < C::PS; ++j) {
-    const int piece = (wave + j * C::kWaves) % C::NS, q = piece * 16 + lane / 4;
-    s_src[j] = q < C::BM ? a.xs + (m0 + min(q, rows - 1)) * s_pitch
-                         : a.ws + (n0 + min(q - C::BM, cols - 1)) * s_pitch;
+    const int piece = (wave + j * C::kWaves) % C::NS;
+    const bool of_x = piece < C::BM / 16;
+    s_base[j] = of_x ? a.xs + m0 * s_pitch : a.ws + n0 * s_pitch;
+    s_off[j] = min((of_x ? piece : piece - C::BM / 16) * 16 + lane / 4, (of_x ? rows : cols) - 1) * s_pitch;
     s_dst[j] = lds0 + C::kScales + piece * 256;
     s_flip[j] = 2 * (piece & 1);   // the upper 16 of 32 rows: steps 2 3 0 1, so that 32 rows' reads miss each other's banks
   }
@@ -187,7 +188,8 @@ mx_linear_kernel(LinArgs a) {
     if (next % C::GS == 0) {
 #pragma unroll
       for (int j = 0; j < C::PS; ++j)
-        dma4(s_src[j] + min(next * C::SK + ((lane & 3) ^ s_flip[j]), steps - 1) * 4, s_dst[j] + next_group);
+        dma4_off(s_base[j], s_off[j] + min(next * C::SK + ((lane & 3) ^ s_flip[j]), steps - 1) * 4,
+                 s_dst[j] + next_group);
       next_group += C::kScaleGroup;
       if (next_group == C::kScaleGroups * C::kScaleGroup) next_group = 0;
     }
@@ -236,10 +238,10 @@ mx_linear_kernel(LinArgs a) {
   // instruction (and for FP8 per half of its 32 bytes).  Blocks lie 32 rows
   // apart, where the slots repeat.
   const int xr = wm * C::TM + r32, wr = wn * C::TN + col_of(r32);
-  const uint32_t x_row = xr * C::kXRow, w_row = C::kW + wr * C::kWRow;
-  const uint32_t xs_row = lds0 + C::kScales + xr * C::kScaleRow, ws_row = lds0 + C::kScales + (C::BM + wr) * C::kScaleRow;
-  const uint32_t xs_flip = (xr & 16) / 2, ws_flip = (wr & 16) / 2;
-
+  const uint32_t x_lane = lds0 + xr * C::kXRow + slot_of<C::kXRow>(xr, h) * 16;
+  const uint32_t w_lane = lds0 + C::kW + wr * C::kWRow + slot_of<C::kWRow>(wr, h) * 16;
+  const uint32_t xs_lane = lds0 + C::kScales + xr * C::kScaleRow + (xr & 16) / 2;
+  const uint32_t ws_lane = lds0 + C::kScales + (C::BM + wr) * C::kScaleRow + (wr & 16) / 2;
   using u32_steps = uint32_t __attribute__((ext_vector_type(C::SK)));
   struct Frags {   // one matrix instruction's worth of K
     u32x4_t x[C::FT][C::X8 ? 2 : 1], w[C::FN];
@@ -257,12 +259,10 @@ mx_linear_kernel(LinArgs a) {
   };
   auto read = [&](auto part, Frags& f) {   // part of the stage: step part / 2, instruction part % 2
     constexpr int kSub = decltype(part)::value / 2, kHalf = decltype(part)::value % 2;
-    const uint32_t st = lds0 + slot;
-    const uint32_t wa = opaque_vgpr(st + w_row + slot_of<C::kWRow>(wr, 4 * kSub + 2 * kHalf + h) * 16);
-    const uint32_t xa = opaque_vgpr(
-        st + x_row + slot_of<C::kXRow>(xr, C::X8 ? 8 * kSub + 4 * kHalf + h : 4 * kSub + 2 * kHalf + h) * 16);
-    const uint32_t xb =
-        C::X8 ? opaque_vgpr(st + x_row + slot_of<C::kXRow>(xr, 8 * kSub + 4 * kHalf + 2 + h) * 16) : 0u;
+    // chunk c ^ (h ^ row) of the row's slots: h is bit 0 of the chunk, the part its upper bits
+    const uint32_t wa = opaque_vgpr((w_lane + slot) ^ (4 * kSub + 2 * kHalf) * 16);
+    const uint32_t xa = opaque_vgpr((x_lane + slot) ^ (C::X8 ? 8 * kSub + 4 * kHalf : 4 * kSub + 2 * kHalf) * 16);
+    const uint32_t xb = C::X8 ? opaque_vgpr((x_lane + slot) ^ (8 * kSub + 4 * kHalf + 2) * 16) : 0u;
 #pragma unroll
     for (int n = 0; n < C::FN; ++n) f.w[n] = *lds_ptr<u32x4_t>(wa + n * 32 * C::kWRow);
 #pragma unroll
@@ -272,7 +272,8 @@ mx_linear_kernel(LinArgs a) {
     }
   };
   auto read_scales = [&](Scales& g) {
-    const uint32_t xs = opaque_vgpr((xs_row + sc) ^ xs_flip), ws = opaque_vgpr((ws_row + sc) ^ ws_flip);
+    const uint32_t at = sc % C::kScaleRow, group = sc - at;   // exchanged halves: see the copies
+    const uint32_t xs = opaque_vgpr((xs_lane ^ at) + group), ws = opaque_vgpr((ws_lane ^ at) + group);
 #pragma unroll
     for (int n = 0; n < C::FN; ++n) g.w[n] = *lds_ptr<u32_steps>(ws + n * 32 * C::kScaleRow);
 #pragma unroll
