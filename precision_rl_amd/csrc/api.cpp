@@ -826,7 +826,7 @@ w4a4_status w4a4_add_rmsnorm_fwd(int64_t T, int H, float eps, const void* x, int
   if ((st = check_element_ptr("offsets", offsets, 4, false)) != W4A4_OK) return st;
   if (T == 0 && offsets == nullptr) return W4A4_OK;
   const NormFwdArgs a{T, H, eps, static_cast<const uint16_t*>(x), x_stride, residual, T > 0 ? gamma : nullptr,
-                      gamma_dtype == W4A4_F32, sum, static_cast<uint16_t*>(y), codes, scales, rstd, offsets, false};
+                      gamma_dtype == W4A4_F32, sum, static_cast<uint16_t*>(y), codes, scales, rstd, offsets, false, 0};
   if (!launch_add_rmsnorm(a, residual_dtype == W4A4_F32, format, static_cast<hipStream_t>(stream)))
     return W4A4_ERR_LAUNCH;
   return W4A4_OK;
@@ -890,7 +890,7 @@ w4a4_status w4a4_mx_linear_fwd(int64_t T, int K, int N, int format, const uint8_
     return fail(W4A4_ERR_INVALID_ARG, "format %d is neither W4A4_MX_FP4 nor W4A4_MX_FP8", format);
   if (K % 128 || N % 8)
     return fail(W4A4_ERR_UNSUPPORTED, "kernels need K %% 128 == 0 and N %% 8 == 0 (K=%d N=%d)", K, N);
-  if (K > 65536) return fail(W4A4_ERR_UNSUPPORTED, "K=%d > 65536", K);
+  if (K > 65536 || N > (1 << 30)) return fail(W4A4_ERR_UNSUPPORTED, "K=%d > 65536 or N=%d > 2^30", K, N);
   if ((st = check_stride("y_stride", y_stride, N)) != W4A4_OK) return st;
   if (T > 0) {
     REQUIRE_PTR(x_codes);

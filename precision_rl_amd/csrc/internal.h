@@ -199,7 +199,8 @@ struct NormFwdArgs {
   uint8_t* scales;
   float* rstd;
   int32_t* offsets;
-  bool stream;   // set by the launch: non-temporal loads
+  bool stream;     // set by the launch: non-temporal loads
+  int64_t first;   // likewise: its first row
 };
 bool launch_add_rmsnorm(const NormFwdArgs& a, bool res_f32, int format, hipStream_t s);
 

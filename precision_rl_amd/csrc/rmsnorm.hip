@@ -148,9 +148,9 @@ norm_fwd_kernel(NormFwdArgs a) {
   constexpr int kTeams = kNormThreads / TEAM;
   const RES* residual = static_cast<const RES*>(a.residual);
   RES* sum = static_cast<RES*>(a.sum);
-  if (a.offsets != nullptr && blockIdx.x == 0 && threadIdx.x < 2)
+  if (a.offsets != nullptr && a.first == 0 && blockIdx.x == 0 && threadIdx.x < 2)
     a.offsets[threadIdx.x] = threadIdx.x == 0 ? 0 : static_cast<int32_t>(a.T);
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * kTeams + threadIdx.x / TEAM;
+  const int64_t t = a.first + static_cast<int64_t>(blockIdx.x) * kTeams + threadIdx.x / TEAM;
   if (t >= a.T) return;   // TEAM > 64: the whole workgroup
 
   // every load of the row in flight before the first is used
@@ -450,9 +450,15 @@ quantize_rows_kernel(const uint16_t* __restrict__ x, int64_t x_stride, int64_t t
 template <int TEAM, int P, typename RES, int FMT>
 void launch_fwd_variant(const NormFwdArgs& a, hipStream_t s) {
   constexpr int kTeams = kNormThreads / TEAM;
-  const int64_t blocks = std::max<int64_t>(1, (a.T + kTeams - 1) / kTeams);
-  launch_kernel("add_rmsnorm", norm_fwd_kernel<TEAM, P, RES, FMT>, dim3(static_cast<unsigned>(blocks)),
-                dim3(kNormThreads), 0, s, a);
+  // a launch holds fewer than 2^32 threads: more rows take further launches
+  constexpr int64_t kMost = int64_t{1} << 23;
+  NormFwdArgs part = a;
+  do {
+    const int64_t blocks = std::min(kMost, std::max<int64_t>(1, (a.T - part.first + kTeams - 1) / kTeams));
+    launch_kernel("add_rmsnorm", norm_fwd_kernel<TEAM, P, RES, FMT>, dim3(static_cast<unsigned>(blocks)),
+                  dim3(kNormThreads), 0, s, part);
+    part.first += blocks * kTeams;
+  } while (part.first < a.T);
 }
 
 template <int TEAM, int P>

@@ -247,6 +247,19 @@ def test_layer_chain(b, T, K, N):
     assert rel_l2(bufs["back"]["dgamma"].double().cpu().numpy(), dg) <= (T + 64) * U * np.sqrt(T) + 64 * U
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_linear_output_behind_four_gigabytes(b, fmt):
+    """Rows at both ends of an output of 4.9 GB: the bits of the rows alone."""
+    T, K, N = 600005, 128, 4096
+    f = _fmt(b, fmt)
+    xq, wq = _operands(b, T, K, N, f, 5)
+    print_case("mx_linear_far", T=T, K=K, N=N, fmt=fmt)
+    y = b.w4a4_mx_linear_fwd(xq, wq, T, K, N)
+    for t0, n in ((0, 70), (524200, 200), (T - 300, 300)):
+        part = {name: v[t0:t0 + n].contiguous() for name, v in xq.items()}
+        assert torch.equal(y[t0:t0 + n], b.w4a4_mx_linear_fwd(part, wq, n, K, N)), t0
+
+
 def test_layer_chain_on_a_stream_and_in_graphs(b):
     """The chain on a side stream and in two captured graphs, each with its own
     workspace, replayed in turn with eager work between: always the eager bits."""

@@ -111,6 +111,29 @@ def test_norm_rounds_once(b, res, gdt):
     assert np.array_equal(_f64(out["y"]), np.rint(y / step) * step)
 
 
+def test_norm_of_more_rows_than_a_launch_holds(b):
+    """2^28 + 37 rows of 8 are more than 2^24 workgroups of 256: three launches.
+    Rows at the ends of each against the same rows alone, offsets the whole
+    batch's."""
+    T, H = (1 << 28) + 37, 8
+    print_case("norm_many_rows", T=T, H=H)
+    x = torch.empty(T, H, dtype=torch.bfloat16, device="cuda")
+    x.view(torch.int16).fill_(0x3F80)
+    edges = [0, (1 << 27) - 16, (1 << 27), (1 << 28) - 16, (1 << 28), T - 16]
+    some = {t: _dev(np.random.default_rng(t % 1009).standard_normal((16, H)), torch.bfloat16) for t in edges}
+    for t, v in some.items():
+        x[t:t + 16] = v
+    g = _dev(np.linspace(0.5, 2.0, H), torch.bfloat16)
+    out = b.w4a4_add_rmsnorm_fwd(x, g, 1e-6, save=True,
+                                 out=dict(offsets=torch.empty(2, dtype=torch.int32, device="cuda")))
+    assert out["offsets"].tolist() == [0, T]
+    for t in edges:
+        alone = b.w4a4_add_rmsnorm_fwd(x[t:t + 16].clone(), g, 1e-6, save=True)
+        assert torch.equal(out["y"][t:t + 16], alone["y"]) and torch.equal(out["rstd"][t:t + 16], alone["rstd"]), t
+    one = b.w4a4_add_rmsnorm_fwd(torch.ones(1, H, dtype=torch.bfloat16, device="cuda"), g, 1e-6)["y"]
+    assert torch.equal(out["y"][(1 << 27) + 100], one[0]) and torch.equal(out["y"][T - 17], one[0])
+
+
 def test_norm_in_place_slices_and_rows_behind(b):
     """The sum over the residual, x a column slice, and nothing written past the
     last row."""
@@ -278,6 +301,18 @@ def test_quantize_rows(b, T, K, pad, fmt):
     _check_codes(b, x.contiguous(), out["codes"], out["scales"], f)
     assert off.tolist() == [0, T]
     assert bool((codes[T:] == 9).all()) and bool((scales[T:] == 9).all())
+
+
+def test_quantize_rows_behind_four_gigabytes(b):
+    T, K = 300000, 8192
+    print_case("quantize_rows_far", T=T, K=K)
+    x = torch.empty(T, K, dtype=torch.bfloat16, device="cuda")
+    x.view(torch.int16).fill_(0x3F80)
+    last = _dev(np.random.default_rng(6).standard_normal((3, K)), torch.bfloat16)
+    x[T - 3:] = last
+    got, alone = b.w4a4_mx_quantize_rows(x, b.MX_FP8), b.w4a4_mx_quantize_rows(last, b.MX_FP8)
+    for n in ("codes", "scales"):
+        assert torch.equal(got[n][T - 3:], alone[n]) and torch.equal(got[n][T - 4], got[n][0])
 
 
 def test_quantize_rows_matches_the_other_mx_quantisers(b):

@@ -103,6 +103,7 @@ def test_linear_refusals(lib, p):
     assert f(N=20) == UNSUPPORTED
     assert "128" in lib.w4a4_last_error().decode()
     assert f(K=65536 + 128) == UNSUPPORTED
+    assert f(N=(1 << 30) + 8, stride=(1 << 30) + 8) == UNSUPPORTED
     assert f(fmt=NONE) == INVALID
     assert f(stride=56) == INVALID and f(stride=68) == INVALID
     assert f(x=None) == INVALID and f(xs=None) == INVALID and f(w=None) == INVALID and f(ws=None) == INVALID
