@@ -510,7 +510,7 @@ w4a4_status w4a4_add_rmsnorm_fwd(
  *   dx         [T, H] bf16 out or NULL: the same gradient rounded to bf16
  *              (for x beside a float residual stream).
  *   dgamma     [H] float out or NULL; zeros for T = 0.  Its sums run in an
- *              order that depends on T and H alone.
+ *              order that depends on T, H and residual_dtype alone.
  *   workspace  w4a4_workspace_size(W4A4_WS_RMSNORM_BACKWARD, T, H, ...) bytes
  *              where dgamma is given (0 for few rows), else NULL.
  */

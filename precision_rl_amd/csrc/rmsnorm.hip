@@ -521,17 +521,25 @@ bool launch_bwd_shape(const NormBwdArgs& a, bool res_f32, int blocks, hipStream_
 // rows share a wave.
 int norm_team(int H) { return H <= 256 ? 16 : H <= 2048 ? 64 : 256; }
 
-// Workgroups over rows, and rows of scratch that they take with dgamma.
-int bwd_blocks(int64_t T, int H) {
+// Workgroups over rows, and rows of scratch that they take with dgamma: one a
+// CU, two where the lanes of one hold too few bytes of their rows to cover the
+// latency (one 16-byte chunk of each tensor, or two in the teams that wait at
+// barriers) and there are two rounds of rows for two: 131072 rows of 512 in
+// bf16 92 us against 113, of 2560 (16384 rows) 61 against 82, of 4096 88 against 101.  With
+// wider rows two are slower (H = 2048 51 against 48, 5120 in FP32 126 against
+// 123), and with few rows the second's partial sums cost more than it saves
+// (1000 rows of 2560: 13.0 against 10.3).
+int bwd_blocks(int64_t T, int H, bool res_f32) {
   const int teams = kBwdThreads / norm_team(H);
   const int64_t need = (T + teams - 1) / teams;
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(need, 256)));
+  const bool narrow = !res_f32 && (H <= 128 || (H > 256 && H <= 512) || (H > 2048 && H <= 4096));
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(need, narrow && need >= 1024 ? 512 : 256)));
 }
 
 }  // namespace
 
 size_t norm_bwd_part_bytes(int64_t T, int H) {
-  return T <= kFewRows ? 0 : static_cast<size_t>(bwd_blocks(T, H)) * H * 4;
+  return T <= kFewRows ? 0 : static_cast<size_t>(bwd_blocks(T, H, false)) * H * 4;   // bf16 takes no fewer
 }
 
 bool launch_add_rmsnorm(const NormFwdArgs& args, bool res_f32, int format, hipStream_t s) {
@@ -560,7 +568,7 @@ bool launch_add_rmsnorm_bwd(const NormBwdArgs& args, bool res_f32, hipStream_t s
                   dim3(kNormThreads), 0, s, a.dgamma, H);
     return launch_ok("add_rmsnorm_dgamma");
   }
-  const int blocks = bwd_blocks(a.T, H);
+  const int blocks = bwd_blocks(a.T, H, res_f32);
   bool ok = false;
   if (H <= 128) ok = launch_bwd_shape<16, 1>(a, res_f32, blocks, s);
   else if (H <= 256) ok = launch_bwd_shape<16, 2>(a, res_f32, blocks, s);
