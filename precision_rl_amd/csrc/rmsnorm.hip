@@ -15,7 +15,11 @@
 // two floats, and y is rounded once: it is the bf16 nearest to the exact value.
 // That costs no time beside HBM, and no row's squares overflow or underflow.
 // Everything else is FP32.  All calls are bound by HBM: every tensor is read
-// or written once.
+// or written once.  16384 rows of 2048 in bf16 with FP8 codes take 43 us (5.4
+// TB/s), with y and rstd 54 (5.6), the backward 48 (5.6); 4097 of 4096 with an
+// FP32 residual 37 (5.0), 8191 of 5120 the backward 115 (5.1); the quantiser of
+// 16384 rows of 4096 35 with FP8 (5.8), 32 with FP4 (5.2).  One row takes 4.5 us
+// forward and 3.2 backward, one quantised row 2.7.
 
 #include <algorithm>
 
@@ -230,7 +234,7 @@ norm_fwd_kernel(NormFwdArgs a) {
 }
 
 // ----------------------------------------------------------------- backward
-// As the forward, 512 threads; DG: each lane sums dy n of its columns over
+// As the forward, 512 threads or 256; DG: each lane sums dy n of its columns over
 // its rows in FP32, the workgroup's teams add theirs in LDS in team order and
 // write one row of `part`, which dgamma_kernel adds in workgroup order.
 //
@@ -240,12 +244,12 @@ norm_fwd_kernel(NormFwdArgs a) {
 // T = 61 4.0 us against 7.2, T = 512 4.7 against 8.5, T = 1024 8.1 against 9.3, T
 // = 2048 16.6 against 11.9; H = 8192 in FP32: T = 512 17.3 against 17.6, T =
 // 1024 31.0 against 27.7; H = 512: T = 512 4.1 against 5.9, T = 2048 11.7 against 6.0.
-template <int TEAM, int P, typename RES, bool DG>
+template <int THREADS, int TEAM, int P, typename RES, bool DG>
 __device__ __forceinline__ void norm_bwd_rows(const NormBwdArgs& a, int block, int blocks) {
   extern __shared__ __attribute__((aligned(16))) float dg_lds[];   // DG: [teams][H]
-  __shared__ float slots[2][kBwdThreads / kWave];
+  __shared__ float slots[2][THREADS / kWave];
   const int lane = threadIdx.x % TEAM, team = threadIdx.x / TEAM, chunks = a.H / 8;
-  constexpr int kTeams = kBwdThreads / TEAM;
+  constexpr int kTeams = THREADS / TEAM;
   const int64_t step = static_cast<int64_t>(blocks) * kTeams;
   const RES* s_in = static_cast<const RES*>(a.sum);
   const RES* dsum = static_cast<const RES*>(a.dsum);
@@ -324,7 +328,7 @@ __device__ __forceinline__ void norm_bwd_rows(const NormBwdArgs& a, int block, i
     }
     __syncthreads();
     float* out = a.part + static_cast<int64_t>(block) * a.H;
-    for (int h = threadIdx.x; h < a.H; h += kBwdThreads) {
+    for (int h = threadIdx.x; h < a.H; h += THREADS) {
       float v = dg_lds[h];
 #pragma unroll
       for (int w = 1; w < kTeams; ++w) v += dg_lds[w * a.H + h];
@@ -333,10 +337,10 @@ __device__ __forceinline__ void norm_bwd_rows(const NormBwdArgs& a, int block, i
   }
 }
 
-template <int TEAM, int P, typename RES, bool DG>
-__global__ void __launch_bounds__(kBwdThreads)
+template <int THREADS, int TEAM, int P, typename RES, bool DG>
+__global__ void __launch_bounds__(THREADS)
 norm_bwd_kernel(NormBwdArgs a) {
-  norm_bwd_rows<TEAM, P, RES, DG>(a, blockIdx.x, gridDim.x);
+  norm_bwd_rows<THREADS, TEAM, P, RES, DG>(a, blockIdx.x, gridDim.x);
 }
 
 // dgamma of 64 columns: lane l of eight takes the columns 8 l .. +7 of rows r,
@@ -384,7 +388,7 @@ __global__ void __launch_bounds__(kBwdThreads)
 norm_bwd_few_kernel(NormBwdArgs a, int first, int rows) {
   const int block = blockIdx.x + first;
   if (block < rows) {
-    norm_bwd_rows<TEAM, P, RES, false>(a, block, rows);
+    norm_bwd_rows<kBwdThreads, TEAM, P, RES, false>(a, block, rows);
   } else {
     column_sums<RES>(a, block - rows);
   }
@@ -473,18 +477,37 @@ void launch_fwd_shape(const NormFwdArgs& a, bool res_f32, int format, hipStream_
   else fmt(uint16_t{});
 }
 
-template <int TEAM, int P, typename RES, bool DG>
+// Lanes per row: a row's chunks fit its team's registers (P <= 4), and short
+// rows share a wave.
+int norm_team(int H) { return H <= 256 ? 16 : H <= 2048 ? 64 : 256; }
+
+// Threads of the backward's workgroups: for wide rows one row each, two
+// workgroups a CU, so that one loads beside the other's stores: 8191 rows of
+// 5120 in FP32 115 us against 123, 16384 of 8192 in bf16 178 against 187; few
+// of them are faster with half the partial sums (1000 of 8192 in bf16 18.9
+// against 20.7, 2000 33.6 against 32.6).
+int bwd_threads(int64_t T, int H) { return H > 4096 && T >= 2048 ? 256 : kBwdThreads; }
+
+template <int THREADS, int TEAM, int P, typename RES, bool DG>
 bool launch_bwd_variant(const NormBwdArgs& a, int blocks, hipStream_t s) {
-  const uint32_t lds = DG ? static_cast<uint32_t>(kBwdThreads / TEAM) * a.H * 4u : 0u;
+  const uint32_t lds = DG ? static_cast<uint32_t>(THREADS / TEAM) * a.H * 4u : 0u;
+  const auto kernel = norm_bwd_kernel<THREADS, TEAM, P, RES, DG>;
   if constexpr (DG) {
-    static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&norm_bwd_kernel<TEAM, P, RES, DG>),
-                                                       hipFuncAttributeMaxDynamicSharedMemorySize,
-                                                       kBwdThreads * P * 32);
+    static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                                       hipFuncAttributeMaxDynamicSharedMemorySize, THREADS * P * 32);
     if (attr != hipSuccess) return launch_ok("add_rmsnorm_bwd") && false;
   }
-  launch_kernel("add_rmsnorm_bwd", norm_bwd_kernel<TEAM, P, RES, DG>, dim3(static_cast<unsigned>(blocks)),
-                dim3(kBwdThreads), lds, s, a);
+  launch_kernel("add_rmsnorm_bwd", kernel, dim3(static_cast<unsigned>(blocks)), dim3(THREADS), lds, s, a);
   return true;
+}
+
+template <int THREADS, int TEAM, int P>
+bool launch_bwd_threads(const NormBwdArgs& a, bool res_f32, int blocks, hipStream_t s) {
+  if (res_f32)
+    return a.part ? launch_bwd_variant<THREADS, TEAM, P, float, true>(a, blocks, s)
+                  : launch_bwd_variant<THREADS, TEAM, P, float, false>(a, blocks, s);
+  return a.part ? launch_bwd_variant<THREADS, TEAM, P, uint16_t, true>(a, blocks, s)
+                : launch_bwd_variant<THREADS, TEAM, P, uint16_t, false>(a, blocks, s);
 }
 
 // The column sums read dy and sum, which the rows may be written over: then
@@ -510,16 +533,10 @@ template <int TEAM, int P>
 bool launch_bwd_shape(const NormBwdArgs& a, bool res_f32, int blocks, hipStream_t s) {
   if (a.dgamma != nullptr && a.T <= kFewRows)
     return res_f32 ? launch_bwd_few<TEAM, P, float>(a, s) : launch_bwd_few<TEAM, P, uint16_t>(a, s);
-  if (res_f32)
-    return a.part ? launch_bwd_variant<TEAM, P, float, true>(a, blocks, s)
-                  : launch_bwd_variant<TEAM, P, float, false>(a, blocks, s);
-  return a.part ? launch_bwd_variant<TEAM, P, uint16_t, true>(a, blocks, s)
-                : launch_bwd_variant<TEAM, P, uint16_t, false>(a, blocks, s);
+  if constexpr (TEAM == 256 && P == 4)
+    if (bwd_threads(a.T, a.H) == TEAM) return launch_bwd_threads<TEAM, TEAM, P>(a, res_f32, blocks, s);
+  return launch_bwd_threads<kBwdThreads, TEAM, P>(a, res_f32, blocks, s);
 }
-
-// Lanes per row: a row's chunks fit its team's registers (P <= 4), and short
-// rows share a wave.
-int norm_team(int H) { return H <= 256 ? 16 : H <= 2048 ? 64 : 256; }
 
 // Workgroups over rows, and rows of scratch that they take with dgamma: one a
 // CU, two where the lanes of one hold too few bytes of their rows to cover the
@@ -530,10 +547,10 @@ int norm_team(int H) { return H <= 256 ? 16 : H <= 2048 ? 64 : 256; }
 // 123), and with few rows the second's partial sums cost more than it saves
 // (1000 rows of 2560: 13.0 against 10.3).
 int bwd_blocks(int64_t T, int H, bool res_f32) {
-  const int teams = kBwdThreads / norm_team(H);
+  const int threads = bwd_threads(T, H), teams = threads / norm_team(H);
   const int64_t need = (T + teams - 1) / teams;
   const bool narrow = !res_f32 && (H <= 128 || (H > 256 && H <= 512) || (H > 2048 && H <= 4096));
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(need, narrow && need >= 1024 ? 512 : 256)));
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(need, threads == 256 || (narrow && need >= 1024) ? 512 : 256)));
 }
 
 }  // namespace

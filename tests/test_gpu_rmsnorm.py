@@ -186,7 +186,7 @@ def test_norm_extreme_rows(b):
 
 @pytest.mark.parametrize("T,H", [(1, 32), (5, 96), (3, 128), (131, 256), (2, 288), (9, 512), (4, 1000), (1, 2048),
                                  (61, 2048), (5, 2080), (3, 4096), (2, 8192), (5000, 64), (9000, 160),
-                                 (300, 392), (640, 392), (9000, 392), (2101, 4096), (700, 1024), (513, 2048), (770, 2080), (600, 8192)])
+                                 (300, 392), (640, 392), (9000, 392), (2101, 4096), (700, 1024), (513, 2048), (770, 2080), (600, 8192), (2060, 4104), (2300, 8192)])
 @pytest.mark.parametrize("res", ["bf16", "f32"])
 def test_norm_backward(b, T, H, res):
     rt = torch.bfloat16 if res == "bf16" else torch.float32
