@@ -425,7 +425,7 @@ def _ptr(t, name, shape, dtype, device, rows=False):
     further apart."""
     if t is None:
         return None
-    if t.dtype != dtype or t.shape != shape or t.device != device:
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device.index:
         raise W4A4Error(f"{name}: {dtype} {tuple(shape)} on {device} expected, "
                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
     if not t.is_contiguous() and not (rows and (t.stride(1) == 1 or t.shape[0] == 0)):
@@ -458,10 +458,14 @@ if _raw_stream is None:
     def _raw_stream(index):
         return torch.cuda.current_stream(index).cuda_stream
 
+# The current device, without torch.cuda.current_device's look whether the GPU is initialised:
+# a tensor lies on it here.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
 
 def _call(fn, device, *args):
     stream = _raw_stream(device.index)
-    if device.index == torch.cuda.current_device():
+    if device.index == _current_device():
         _check(fn(*args, stream))
     else:
         with torch.cuda.device(device):
