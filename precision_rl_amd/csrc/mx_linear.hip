@@ -455,12 +455,13 @@ int64_t tiles_of(const LinArgs& a, int bm, int bn) {
 //     T = 10000, K = 2048 (2.5 against 1.25): 32 against 37; T = 1500, N =
 //     4096: 13 against 17; T = 16384: 98 against 88.
 //   FP8, whose instructions take twice as long per byte of w: 128 x 128 with
-//     stages of two steps for at most one tile a CU; 128 x 256, two of which run
-//     on a CU at once, beyond: 256 tiles of 128 x 128 12.8 us against 16.9, 320
-//     21.1 against 16.7; and 256 x 256 where one round of it does and at least
-//     three in five CUs have a tile: T = 6000, K = 4096, N = 2048 (192 tiles) 48
-//     against 51, T = 2048, K = 2048, N = 4096 (128) 25 against 20, T = 10000
-//     (640) 85 against 74.
+//     stages of two steps for at most one tile a CU (256 tiles 12.8 us against
+//     16.9 with 128 x 256), beyond that the smallest of 128 x 256, 192 x 256 and
+//     256 x 256 of which one round over the chip does: N = 4096, K = 2048, T =
+//     2048 18.6, 22.2, 24.0 us, T = 2560 24.5, 22.4, 25.2; N = 2048, K = 4096, T
+//     = 5001 46.1, 39.4, 42.5, T = 8192 55.9, 77.4, 53.6.  Beyond one round 128 x
+//     256, two of which run on a CU at once: T = 10000, N = 4096, K = 2048 69,
+//     87, 81; T = 16384 113, 133, 121.
 template <bool X8>
 bool launch_format(const LinArgs& a, hipStream_t s) {
   if (tiles_of(a, 32, 32) <= 256) return launch_cfg<LinCfg<X8, 32, 32, 1, 1, 2, 2>>(a, s);
@@ -469,7 +470,11 @@ bool launch_format(const LinArgs& a, hipStream_t s) {
   const int64_t n128 = tiles_of(a, 128, 128), n256 = tiles_of(a, 256, 256);
   if constexpr (X8) {
     if (n128 <= 256) return launch_cfg<LinCfg<true, 128, 128, 4, 2, 2, 2>>(a, s);
-    if (n256 <= 150 || n256 > 256) return launch_cfg<LinCfg<true, 128, 256, 2, 4, 2, 2, 1, false>>(a, s);
+    if (tiles_of(a, 128, 256) > 256 && n256 <= 256) {
+      if (tiles_of(a, 192, 256) <= 256) return launch_cfg<LinCfg<true, 192, 256, 3, 4, 2, 1, 1, false>>(a, s);
+    } else {
+      return launch_cfg<LinCfg<true, 128, 256, 2, 4, 2, 2, 1, false>>(a, s);
+    }
   } else {
     const double rounds128 = static_cast<double>(n128 / 512) + (n128 % 512 > 256 ? 1.0 : n128 % 512 > 0 ? 0.65 : 0.0);
     if (rounds128 <= 1.6 * static_cast<double>((n256 + 255) / 256))

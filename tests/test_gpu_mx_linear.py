@@ -73,13 +73,13 @@ def _fmt(b, name):
 
 
 # one row, ragged rows and columns, one step, odd numbers of steps, fewer and
-# more stages than a ring; the last seven reach the tiles that larger products
-# take (64 x 128, 128 x 128, 128 x 256 and 256 x 256)
+# more stages than a ring; the last eight reach the tiles that larger products
+# take (64 x 128, 128 x 128, 128, 192 and 256 x 256)
 @pytest.mark.parametrize("T,K,N", [(1, 128, 8), (1, 2048, 256), (3, 384, 40), (16, 640, 1000), (17, 1024, 136),
                                    (32, 4096, 72), (33, 256, 264), (48, 2048, 512), (64, 1152, 2048), (65, 128, 128),
                                    (127, 896, 520), (300, 1024, 776), (513, 2048, 256), (1000, 256, 1032),
                                    (40, 128, 41000), (64, 384, 41224), (1200, 384, 2312), (2100, 640, 2568),
-                                   (4999, 384, 2056), (5121, 128, 2048), (8300, 128, 2056)])
+                                   (4999, 384, 2056), (5121, 128, 2048), (6300, 128, 2056), (8300, 128, 2056)])
 @pytest.mark.parametrize("fmt", FORMATS)
 def test_linear(b, T, K, N, fmt):
     f = _fmt(b, fmt)
