@@ -20,8 +20,9 @@
 // (4.3 PFLOP/s), the matrix instructions alone take 43, the copies alone 41
 // (one stage of 64 KB in flight a CU) and the operand reads alone 37; the
 // stores, which a round's tiles make together at the memory's rate, take 20 us
-// of the 88.  At T = 1 (N = 4096) a call takes 5.2 us (5.8 with FP8): the latency of
-// 8 stages in a row, no CU having more than one tile.
+// of the 88.  At T = 1 (N = 4096) a call takes 4.8 us (5.3 with FP8): 8 stages in a
+// row of one wave, each a chain of four instructions on one accumulator, the
+// operands' LDS latency and the next copies' issue.
 
 #include <algorithm>
 
@@ -65,6 +66,7 @@ struct LinCfg {
   static constexpr int GS = kScaleSteps / SK, kScaleGroups = (S + 2 * GS - 2) / GS;
   static constexpr int kScales = S * kStage, kScaleRow = kScaleSteps * 4, kScaleGroup = (BM + BN) * kScaleRow;
   static constexpr int kLds = kScales + kScaleGroups * kScaleGroup;
+  static_assert(NX % PX == 0 && NW % PW == 0, "a wave's pieces follow each other");
   static_assert(FT >= 1 && FN >= 1 && FT * 32 * WM == BM && FN * 32 * WN == BN, "whole blocks");
   static_assert(kLds <= 160 * 1024, "LDS of a compute unit");
   static_assert((S - 2) * kCopies + ((S - 2) / GS + 1) * PS + (AHEAD ? kCopies + PS : 0) <= 63, "the vector-memory counter has six bits");
@@ -116,6 +118,35 @@ __device__ __forceinline__ void wait_stages(int later, bool extra) {
   }
 }
 
+// N copies of 1 KB to consecutive places in LDS, lane offsets off[0 .. N).  The
+// instruction's offset moves both of its addresses, so four copies share one
+// LDS base; off[j] leaves out what the instruction adds: the caller puts `base`
+// 3 KB before the tile and 3 KB less j % 4 KB into off[j].  Against an address
+// per copy a stage of one wave takes 131 instructions instead of 147 (T = 1, N =
+// 4096, K = 2048: 5.7 -> 5.3 us with FP8), 128 x 128 with FP4 at T = 16384 98 -> 92.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"   // M0 is reserved; nothing else here uses it
+template <int N>
+__device__ __forceinline__ void copy_pieces(const uint8_t* base, const uint32_t* off, uint32_t to) {
+  const void* b = uniform_ptr(base);
+  const uint32_t m = __builtin_amdgcn_readfirstlane(to);
+  if constexpr (N == 1) {
+    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off[0]), "s"(b), "s"(m) : "memory", "m0");
+  } else if constexpr (N == 2) {
+    asm volatile("s_mov_b32 m0, %3\n\tglobal_load_lds_dwordx4 %0, %2\n\tglobal_load_lds_dwordx4 %1, %2 offset:1024"
+                 ::"v"(off[0]), "v"(off[1]), "s"(b), "s"(m) : "memory", "m0");
+  } else if constexpr (N == 4) {
+    asm volatile("s_mov_b32 m0, %5\n\tglobal_load_lds_dwordx4 %0, %4\n\tglobal_load_lds_dwordx4 %1, %4 offset:1024\n\t"
+                 "global_load_lds_dwordx4 %2, %4 offset:2048\n\tglobal_load_lds_dwordx4 %3, %4 offset:3072"
+                 ::"v"(off[0]), "v"(off[1]), "v"(off[2]), "v"(off[3]), "s"(b), "s"(m) : "memory", "m0");
+  } else {
+    static_assert(N % 4 == 0, "1, 2 or a multiple of 4");
+#pragma unroll
+    for (int j = 0; j < N; j += 4) copy_pieces<4>(base, off + j, to + j * 1024);
+  }
+}
+#pragma clang diagnostic pop
+
 struct LinArgs {
   int64_t T;
   int K, N;
@@ -156,29 +187,29 @@ mx_linear_kernel(LinArgs a) {
 
   const int x_pitch = C::X8 ? a.K : a.K / 2, w_pitch = a.K / 2, s_pitch = a.K / 32;
   const int steps = a.K / kStep, stages = (steps + C::SK - 1) / C::SK;
-  const uint8_t* x_base = a.x + m0 * x_pitch;
-  const uint8_t* w_base = a.w + n0 * w_pitch;
+  const uint8_t* x_base = a.x + m0 * x_pitch - 3 * 1024;
+  const uint8_t* w_base = a.w + n0 * w_pitch - 3 * 1024;
   // Copy sources and destinations; rows past the operand are clamped to its
   // last (they feed only outputs that are not stored).
   const uint32_t lds0 = lds_addr(lds);
-  uint32_t x_off[C::PX], w_off[C::PW], s_off[C::PS], x_dst[C::PX], w_dst[C::PW], s_dst[C::PS];
+  uint32_t x_off[C::PX], w_off[C::PW], s_off[C::PS], s_dst[C::PS];
+  const int x_piece = wave * C::PX % C::NX, w_piece = wave * C::PW % C::NW;   // the wave's first
+  const uint32_t x_dst = lds0 + x_piece * 1024, w_dst = lds0 + C::kW + w_piece * 1024;
   const uint8_t* s_base[C::PS];
   int s_flip[C::PS];
   uint32_t x_upper = 0, w_upper = 0;   // bit j: the lane's chunk of copy j lies in the stage's second step
 #pragma unroll
   for (int j = 0; j < C::PX; ++j) {
-    const int piece = (wave + j * C::kWaves) % C::NX, row = piece * (kWave / C::kXLanes) + lane / C::kXLanes;
+    const int row = (x_piece + j) * (kWave / C::kXLanes) + lane / C::kXLanes;
     const int chunk = slot_of<C::kXRow>(row, lane % C::kXLanes);
-    x_off[j] = static_cast<uint32_t>(min(row, rows - 1)) * static_cast<uint32_t>(x_pitch) + chunk * 16;
-    x_dst[j] = lds0 + piece * 1024;
+    x_off[j] = static_cast<uint32_t>(min(row, rows - 1)) * static_cast<uint32_t>(x_pitch) + chunk * 16 + (3 - j % 4) * 1024;
     x_upper |= (chunk >= C::kXLanes / 2 ? 1u : 0u) << j;
   }
 #pragma unroll
   for (int j = 0; j < C::PW; ++j) {
-    const int piece = (wave + j * C::kWaves) % C::NW, row = piece * (kWave / C::kWLanes) + lane / C::kWLanes;
+    const int row = (w_piece + j) * (kWave / C::kWLanes) + lane / C::kWLanes;
     const int chunk = slot_of<C::kWRow>(row, lane % C::kWLanes);
-    w_off[j] = static_cast<uint32_t>(min(row, cols - 1)) * static_cast<uint32_t>(w_pitch) + chunk * 16;
-    w_dst[j] = lds0 + C::kW + piece * 1024;
+    w_off[j] = static_cast<uint32_t>(min(row, cols - 1)) * static_cast<uint32_t>(w_pitch) + chunk * 16 + (3 - j % 4) * 1024;
     w_upper |= (chunk >= C::kWLanes / 2 ? 1u : 0u) << j;
   }
 #pragma unroll
@@ -207,17 +238,16 @@ mx_linear_kernel(LinArgs a) {
     if (C::SK == 2 && next * 2 + 1 == steps) {
       // an odd number of steps: the last stage's second half lies behind the
       // row and is filled from the first (never multiplied)
+      uint32_t x_last[C::PX], w_last[C::PW];
 #pragma unroll
-      for (int j = 0; j < C::PX; ++j)
-        dma16_off(xb, (x_upper >> j) & 1u ? x_off[j] - C::kXRow / 2 : x_off[j], x_dst[j] + next_slot);
+      for (int j = 0; j < C::PX; ++j) x_last[j] = (x_upper >> j) & 1u ? x_off[j] - C::kXRow / 2 : x_off[j];
 #pragma unroll
-      for (int j = 0; j < C::PW; ++j)
-        dma16_off(wb, (w_upper >> j) & 1u ? w_off[j] - C::kWRow / 2 : w_off[j], w_dst[j] + next_slot);
+      for (int j = 0; j < C::PW; ++j) w_last[j] = (w_upper >> j) & 1u ? w_off[j] - C::kWRow / 2 : w_off[j];
+      copy_pieces<C::PX>(xb, x_last, x_dst + next_slot);
+      copy_pieces<C::PW>(wb, w_last, w_dst + next_slot);
     } else {
-#pragma unroll
-      for (int j = 0; j < C::PX; ++j) dma16_off(xb, x_off[j], x_dst[j] + next_slot);
-#pragma unroll
-      for (int j = 0; j < C::PW; ++j) dma16_off(wb, w_off[j], w_dst[j] + next_slot);
+      copy_pieces<C::PX>(xb, x_off, x_dst + next_slot);
+      copy_pieces<C::PW>(wb, w_off, w_dst + next_slot);
     }
     ++next;
     next_slot += C::kStage;
@@ -441,10 +471,10 @@ int64_t tiles_of(const LinArgs& a, int bm, int bn) {
 
 // The tile: the larger, the fewer bytes a product copies, but every CU wants
 // one.
-//   32 x 32 up to 256 tiles, then 64 x 64 up to 640 (2.5 a CU): N = 4096, K =
-//     2048, T = 1: 5.8 us against 6.0 with 64 x 64 (FP8; 5.2 either way with
-//     FP4); T = 100: 6.4 against 6.2; T = 200: 7.4 against 6.6; T = 500: 8.8 (64
-//     x 64) against 10.9 (128 x 128); T = 1024: 16.6 against 13.7.
+//   32 x 32 up to 512 tiles (two a CU), then 64 x 64 up to 640: N = 4096, K =
+//     2048, T = 1: 5.3 us against 6.0 with 64 x 64 (FP8; 4.8 against 5.1 with
+//     FP4); T = 128: 5.8 against 6.2; T = 200: 6.6 against 6.4; T = 500: 8.8 (64 x
+//     64) against 10.9 (128 x 128); T = 1024: 16.1 against 13.2.
 //   64 x 128 for at most 64 tokens beyond that, half of whose rows a tile of
 //     128 would leave empty: T = 48, N = 65536: 13.3 us, as 64 x 64, with FP4,
 //     14.0 against 16.4 with FP8.
@@ -452,8 +482,8 @@ int64_t tiles_of(const LinArgs& a, int bm, int bn) {
 //     on a CU at once, and a round of 512 takes 1 / 1.6 of a round of 256 of the
 //     latter, its last one 0.65 of that where it has at most one tile a CU.  T
 //     = 5001, K = 4096, N = 2048 (1.25 against 0.6 rounds): 35 against 32 us;
-//     T = 10000, K = 2048 (2.5 against 1.25): 32 against 37; T = 1500, N =
-//     4096: 13 against 17; T = 16384: 98 against 88.
+//     T = 10000, K = 2048 (2.5 against 1.25): 29 against 35; T = 1500, N =
+//     4096: 13 against 17; T = 16384: 92 against 88.
 //   FP8, whose instructions take twice as long per byte of w: 128 x 128 with
 //     stages of two steps for at most one tile a CU (256 tiles 12.8 us against
 //     16.9 with 128 x 256), beyond that the smallest of 128 x 256, 192 x 256 and
@@ -464,7 +494,7 @@ int64_t tiles_of(const LinArgs& a, int bm, int bn) {
 //     87, 81; T = 16384 113, 133, 121.
 template <bool X8>
 bool launch_format(const LinArgs& a, hipStream_t s) {
-  if (tiles_of(a, 32, 32) <= 256) return launch_cfg<LinCfg<X8, 32, 32, 1, 1, 2, 2>>(a, s);
+  if (tiles_of(a, 32, 32) <= 512) return launch_cfg<LinCfg<X8, 32, 32, 1, 1, 2, 2>>(a, s);
   if (tiles_of(a, 64, 64) <= 640) return launch_cfg<LinCfg<X8, 64, 64, 2, 2, 2, 2>>(a, s);
   if (a.T <= 64) return launch_cfg<LinCfg<X8, 64, 128, 2, 2, 2, 2>>(a, s);
   const int64_t n128 = tiles_of(a, 128, 128), n256 = tiles_of(a, 256, 256);
