@@ -509,6 +509,7 @@ w4a4_status w4a4_add_rmsnorm_fwd(
  *              of x.  May be dsum itself, or dy where it is bf16.
  *   dx         [T, H] bf16 out or NULL: the same gradient rounded to bf16
  *              (for x beside a float residual stream).
+ *              A row's gradient does not depend on the other rows.
  *   dgamma     [H] float out or NULL; zeros for T = 0.  Its sums run in an
  *              order that depends on T, H and residual_dtype alone.
  *   workspace  w4a4_workspace_size(W4A4_WS_RMSNORM_BACKWARD, T, H, ...) bytes

@@ -18,8 +18,8 @@
 // or written once.  16384 rows of 2048 in bf16 with FP8 codes take 43 us (5.4
 // TB/s), with y and rstd 54 (5.6), the backward 48 (5.6); 4097 of 4096 with an
 // FP32 residual 37 (5.0), 8191 of 5120 the backward 115 (5.1); the quantiser of
-// 16384 rows of 4096 35 with FP8 (5.8), 32 with FP4 (5.2).  One row takes 4.5 us
-// forward and 3.2 backward, one quantised row 2.7.
+// 16384 rows of 4096 35 with FP8 (5.8), 32 with FP4 (5.2).  One row takes 2.6 us
+// forward and 2.7 backward, one quantised row 2.7.
 
 #include <algorithm>
 
@@ -34,6 +34,12 @@ typedef float floatx4_t __attribute__((ext_vector_type(4)));
 constexpr int kNormThreads = 256;
 constexpr int kBwdThreads = 512;
 constexpr int kFewRows = 512;
+// Up to how many rows of 1024 < H <= 2048 a whole workgroup (forward) or half of
+// one (backward) takes a row instead of one wave: H = 2048, FP8 codes: T = 1 2.6
+// us against 4.5, T = 512 4.0 against 5.8, T = 2048 8.1 against 9.2, T = 3000 the
+// same; backward: T = 1 2.7 against 3.3, T = 61 2.8 against 4.0, T = 256 3.5
+// against 4.1, T = 512 5.7 against 4.7.
+constexpr int kSpreadRows = 2048, kSpreadBwdRows = 256;
 
 // Whether a call's loads are non-temporal: where it moves more than three
 // quarters of the 256 MiB memory-side cache, its inputs cannot all still lie
@@ -92,19 +98,41 @@ struct Vec8<float> {
   }
 };
 
-// Sum over the TEAM lanes of a row, the same in each of them, in an order
-// that depends on TEAM alone.  TEAM > 64: the waves' sums meet in `slots` (LDS,
-// one per wave of the workgroup); a kernel that sums again takes two sets in
-// turn, so that one barrier per sum is enough (a wave can be at most one sum
-// ahead of a wave that still reads).
-template <int TEAM, typename T>
-__device__ __forceinline__ T team_sum(T v, T* slots) {
-  constexpr int kLanes = TEAM < kWave ? TEAM : kWave;
+// Sum over a row of the lanes' chunk sums q, the same in each lane, in an order
+// that depends on the row's length alone: a lane's chunks, then a wave's lanes
+// by halves, then the waves.  TEAM > 64 meets in `slots` (LDS); a kernel that
+// sums again takes two sets in turn, so that one barrier per sum is enough (a
+// wave can be at most one sum ahead of a wave that still reads).
+//
+// 256 lanes with one chunk each are the spread form of 64 lanes with four
+// chunks, for few rows: there each wave joins the four waves' chunks lane by
+// lane first, in the order in which the lane of the narrow form adds its own, so
+// that the two give the same bits.
+template <int TEAM, int P>
+constexpr bool kSpread = TEAM == 256 && P == 1;
+template <int THREADS, int TEAM, int P>
+constexpr int kSlots = kSpread<TEAM, P> ? THREADS : THREADS / kWave;
+
+template <int TEAM, int P, typename T>
+__device__ __forceinline__ T team_sum(const T (&q)[P], T* slots) {
+  constexpr int kLanes = TEAM < kWave ? TEAM : kWave, kWaves = TEAM / kWave;
+  const int wave = threadIdx.x / kWave;
+  T v = q[0];
+  if constexpr (kSpread<TEAM, P>) {
+    slots[threadIdx.x] = v;
+    __syncthreads();
+    const T* mine = slots + threadIdx.x / TEAM * TEAM + threadIdx.x % kWave;
+    v = mine[0];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) v += mine[w * kWave];
+  } else {
+#pragma unroll
+    for (int p = 1; p < P; ++p) v += q[p];
+  }
 #pragma unroll
   for (int off = kLanes / 2; off > 0; off >>= 1) v += __shfl_xor(v, off, kWave);
-  if constexpr (TEAM > kWave) {
-    constexpr int kWaves = TEAM / kWave;
-    const int wave = threadIdx.x / kWave, first = wave / kWaves * kWaves;
+  if constexpr (TEAM > kWave && !kSpread<TEAM, P>) {
+    const int first = wave / kWaves * kWaves;
     if (threadIdx.x % kWave == 0) slots[wave] = v;
     __syncthreads();
     v = slots[first];
@@ -147,7 +175,7 @@ __device__ __forceinline__ void load_gamma(float (&g)[P][8], const void* gamma, 
 template <int TEAM, int P, typename RES, int FMT>
 __global__ void __launch_bounds__(kNormThreads)
 norm_fwd_kernel(NormFwdArgs a) {
-  __shared__ double slots[kNormThreads / kWave];
+  __shared__ double slots[kSlots<kNormThreads, TEAM, P>];
   const int lane = threadIdx.x % TEAM, chunks = a.H / 8;
   constexpr int kTeams = kNormThreads / TEAM;
   const RES* residual = static_cast<const RES*>(a.residual);
@@ -177,7 +205,7 @@ norm_fwd_kernel(NormFwdArgs a) {
   else load(std::false_type{});
   float g[P][8];
   load_gamma<P>(g, a.gamma, a.gamma_f32, lane, TEAM, chunks);
-  double ss = 0.0;
+  double q[P];
 #pragma unroll
   for (int p = 0; p < P; ++p) {
     const int c = lane + p * TEAM;
@@ -189,10 +217,10 @@ norm_fwd_kernel(NormFwdArgs a) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const double w = s[p].get(i);
-      ss = fma(w, w, ss);
+      q[p] = i == 0 ? w * w : fma(w, w, q[p]);
     }
   }
-  ss = team_sum<TEAM>(ss, slots);
+  const double ss = team_sum<TEAM>(q, slots);
   const double r64 = 1.0 / sqrt(ss / a.H + static_cast<double>(a.eps));
   const float rstd = static_cast<float>(r64), rlow = static_cast<float>(r64 - static_cast<double>(rstd));
   if (a.rstd != nullptr && lane == 0) a.rstd[t] = rstd;
@@ -217,7 +245,7 @@ norm_fwd_kernel(NormFwdArgs a) {
     if (tie) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float rest = fmaf(n[i], g[p][i], -v[i]) + low[i] * g[p][i];
+        const float rest = fmaf(low[i], g[p][i], fmaf(n[i], g[p][i], -v[i]));
         if (halfway(v[i]) && rest != 0.0f)
           v[i] = __uint_as_float(__float_as_uint(v[i]) + ((rest < 0.0f) == (v[i] < 0.0f) ? 1 : -1));
       }
@@ -241,13 +269,13 @@ norm_fwd_kernel(NormFwdArgs a) {
 // Up to kFewRows rows dgamma comes from the rows themselves instead, which lie
 // in the L2 then: column_sums' workgroups follow the rows' in one launch and
 // read them a second time.  Against partial rows and their sum, H = 2048, bf16:
-// T = 61 4.0 us against 7.2, T = 512 4.7 against 8.5, T = 1024 8.1 against 9.3, T
+// T = 512 4.7 against 8.5, T = 1024 8.1 against 9.3, T
 // = 2048 16.6 against 11.9; H = 8192 in FP32: T = 512 17.3 against 17.6, T =
 // 1024 31.0 against 27.7; H = 512: T = 512 4.1 against 5.9, T = 2048 11.7 against 6.0.
 template <int THREADS, int TEAM, int P, typename RES, bool DG>
 __device__ __forceinline__ void norm_bwd_rows(const NormBwdArgs& a, int block, int blocks) {
   extern __shared__ __attribute__((aligned(16))) float dg_lds[];   // DG: [teams][H]
-  __shared__ float slots[2][THREADS / kWave];
+  __shared__ float slots[2][kSlots<THREADS, TEAM, P>];
   const int lane = threadIdx.x % TEAM, team = threadIdx.x / TEAM, chunks = a.H / 8;
   constexpr int kTeams = THREADS / TEAM;
   const int64_t step = static_cast<int64_t>(blocks) * kTeams;
@@ -286,16 +314,18 @@ __device__ __forceinline__ void norm_bwd_rows(const NormBwdArgs& a, int block, i
     };
     if (a.stream) load(std::true_type{});
     else load(std::false_type{});
-    float inner = 0.0f;
+    float q[P];
 #pragma unroll
-    for (int p = 0; p < P; ++p)
+    for (int p = 0; p < P; ++p) {
+      q[p] = 0.0f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float n = s[p].get(i) * rstd, d = dy[p].get(i);
-        inner = fmaf(d * g[p][i], n, inner);
+        q[p] = fmaf(d * g[p][i], n, q[p]);
         if constexpr (DG) dg[p][i] = fmaf(d, n, dg[p][i]);
       }
-    inner = team_sum<TEAM>(inner, slots[turn]) / static_cast<float>(a.H);
+    }
+    const float inner = team_sum<TEAM>(q, slots[turn]) / static_cast<float>(a.H);
     turn ^= 1;
 #pragma unroll
     for (int p = 0; p < P; ++p) {
@@ -305,7 +335,7 @@ __device__ __forceinline__ void norm_bwd_rows(const NormBwdArgs& a, int block, i
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float n = s[p].get(i) * rstd;
-        v[i] = fmaf(rstd, dy[p].get(i) * g[p][i] - n * inner, ds[p].get(i));
+        v[i] = fmaf(rstd, fmaf(dy[p].get(i), g[p][i], -(n * inner)), ds[p].get(i));
       }
       Vec8<RES> o;
       o.put(v);
@@ -531,8 +561,12 @@ bool launch_bwd_few(const NormBwdArgs& a, hipStream_t s) {
 
 template <int TEAM, int P>
 bool launch_bwd_shape(const NormBwdArgs& a, bool res_f32, int blocks, hipStream_t s) {
-  if (a.dgamma != nullptr && a.T <= kFewRows)
+  if (a.dgamma != nullptr && a.T <= kFewRows) {
+    if constexpr (TEAM == 64 && P == 4)
+      if (a.T <= kSpreadBwdRows)
+        return res_f32 ? launch_bwd_few<256, 1, float>(a, s) : launch_bwd_few<256, 1, uint16_t>(a, s);
     return res_f32 ? launch_bwd_few<TEAM, P, float>(a, s) : launch_bwd_few<TEAM, P, uint16_t>(a, s);
+  }
   if constexpr (TEAM == 256 && P == 4)
     if (bwd_threads(a.T, a.H) == TEAM) return launch_bwd_threads<TEAM, TEAM, P>(a, res_f32, blocks, s);
   return launch_bwd_threads<kBwdThreads, TEAM, P>(a, res_f32, blocks, s);
@@ -568,6 +602,7 @@ bool launch_add_rmsnorm(const NormFwdArgs& args, bool res_f32, int format, hipSt
   else if (H <= 256) launch_fwd_shape<16, 2>(a, res_f32, format, s);
   else if (H <= 512) launch_fwd_shape<64, 1>(a, res_f32, format, s);
   else if (H <= 1024) launch_fwd_shape<64, 2>(a, res_f32, format, s);
+  else if (H <= 2048 && a.T <= kSpreadRows) launch_fwd_shape<256, 1>(a, res_f32, format, s);
   else if (H <= 2048) launch_fwd_shape<64, 4>(a, res_f32, format, s);
   else if (H <= 4096) launch_fwd_shape<256, 2>(a, res_f32, format, s);
   else if (H <= 8192) launch_fwd_shape<256, 4>(a, res_f32, format, s);

@@ -76,7 +76,7 @@ def _check_norm(b, x, r, gamma, eps, out, fmt):
 # every team shape and its edges (rows of 16, 64 and 256 lanes, 1 to 4 chunks
 # a lane), one row, fewer rows than a workgroup, rows in several rounds
 @pytest.mark.parametrize("T,H", [(1, 32), (5, 96), (3, 128), (131, 160), (7, 256), (2, 288), (9, 512), (4, 1024),
-                                 (1, 2048), (33, 2048), (5, 2080), (3, 4096), (2, 4128), (3, 8192), (9000, 64)])
+                                 (1, 2048), (33, 2048), (2050, 2048), (5, 2080), (3, 4096), (2, 4128), (3, 8192), (9000, 64)])
 @pytest.mark.parametrize("res,fmt", [("bf16", "fp8"), ("f32", "fp4"), (None, "fp4"), ("f32", None)])
 def test_norm_forward(b, T, H, res, fmt):
     rt = {"bf16": torch.bfloat16, "f32": torch.float32, None: None}[res]
@@ -185,7 +185,7 @@ def test_norm_extreme_rows(b):
 
 
 @pytest.mark.parametrize("T,H", [(1, 32), (5, 96), (3, 128), (131, 256), (2, 288), (9, 512), (4, 1000), (1, 2048),
-                                 (61, 2048), (5, 2080), (3, 4096), (2, 8192), (5000, 64), (9000, 160),
+                                 (61, 2048), (300, 2048), (5, 2080), (3, 4096), (2, 8192), (5000, 64), (9000, 160),
                                  (300, 392), (640, 392), (9000, 392), (2101, 4096), (700, 1024), (513, 2048), (770, 2080), (600, 8192), (2060, 4104), (2300, 8192)])
 @pytest.mark.parametrize("res", ["bf16", "f32"])
 def test_norm_backward(b, T, H, res):
@@ -233,6 +233,26 @@ def test_norm_backward_in_place_without_dgamma_and_empty(b):
     assert torch.equal(over, ref["dres"]) and torch.equal(got["dgamma"], ref["dgamma"])
     none = b.w4a4_add_rmsnorm_bwd(dy[:0], s[:0], g, r[:0], out=dict(dgamma=torch.full((H,), 7.0, device="cuda")))
     assert none["dres"].shape == (0, H) and not none["dgamma"].any()
+
+
+@pytest.mark.parametrize("H", [1032, 1536, 2048])
+@pytest.mark.parametrize("res", ["bf16", "f32"])
+def test_rows_have_the_same_bits_in_small_and_large_batches(b, H, res):
+    """Across the row counts at which another number of lanes takes a row."""
+    T = 2500
+    rt = torch.bfloat16 if res == "bf16" else torch.float32
+    x, r, g = _inputs(T, H, rt, torch.bfloat16, H)
+    dy = _dev(np.random.default_rng(2).standard_normal((T, H)), torch.bfloat16)
+    print_case("rows_small_large", H=H, res=res)
+    full = b.w4a4_add_rmsnorm_fwd(x, g, 1e-6, residual=r, save=True)
+    back = b.w4a4_add_rmsnorm_bwd(dy, full["sum"], g, full["rstd"], dsum=r)
+    for n in (1, 7, 256, 257, 512, 2048, 2049):
+        some = b.w4a4_add_rmsnorm_fwd(x[:n], g, 1e-6, residual=r[:n], save=True)
+        for name in ("sum", "y", "rstd"):
+            assert torch.equal(some[name], full[name][:n]), (name, n)
+        for dgamma in (True, False):
+            part = b.w4a4_add_rmsnorm_bwd(dy[:n], some["sum"], g, some["rstd"], dsum=r[:n], dgamma=dgamma)
+            assert torch.equal(part["dres"], back["dres"][:n]), (n, dgamma)
 
 
 def test_rows_of_a_batch_apart(b):
