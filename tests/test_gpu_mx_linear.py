@@ -261,9 +261,9 @@ def test_linear_output_behind_four_gigabytes(b, fmt):
 
 
 def test_layer_chain_on_a_stream_and_in_graphs(b):
-    """The chain on a side stream and in two captured graphs, each with its own
+    """The chain on a side stream and in three captured graphs, each with its own
     workspace, replayed in turn with eager work between: always the eager bits."""
-    states = [_layer_state(b, 96, 512, 512, 1), _layer_state(b, 200, 256, 768, 2)]
+    states = [_layer_state(b, 96, 512, 512, 1), _layer_state(b, 600, 256, 768, 2), _layer_state(b, 700, 512, 256, 3)]
     print_case("layer_chain_graphs")
     want = []
     for a in states:
