@@ -471,7 +471,9 @@ int64_t tiles_of(const LinArgs& a, int bm, int bn) {
 
 // The tile: the larger, the fewer bytes a product copies, but every CU wants
 // one.
-//   32 x 32 up to 512 tiles (two a CU), then 64 x 64 up to 640: N = 4096, K =
+//   32 x 32 up to 512 tiles (two a CU; up to 1024 for at most 32 tokens, half of
+//     whose rows a tile of 64 would leave empty: T = 1, N = 32768, K = 4096 12.2
+//     us against 13.7 with FP8, 12.0 against 12.4), then 64 x 64 up to 640: N = 4096, K =
 //     2048, T = 1: 5.3 us against 6.0 with 64 x 64 (FP8; 4.8 against 5.1 with
 //     FP4); T = 128: 5.8 against 6.2; T = 200: 6.6 against 6.4; T = 500: 8.8 (64 x
 //     64) against 10.9 (128 x 128); T = 1024: 16.1 against 13.2.
@@ -494,7 +496,7 @@ int64_t tiles_of(const LinArgs& a, int bm, int bn) {
 //     87, 81; T = 16384 113, 133, 121.
 template <bool X8>
 bool launch_format(const LinArgs& a, hipStream_t s) {
-  if (tiles_of(a, 32, 32) <= 512) return launch_cfg<LinCfg<X8, 32, 32, 1, 1, 2, 2>>(a, s);
+  if (tiles_of(a, 32, 32) <= (a.T <= 32 ? 1024 : 512)) return launch_cfg<LinCfg<X8, 32, 32, 1, 1, 2, 2>>(a, s);
   if (tiles_of(a, 64, 64) <= 640) return launch_cfg<LinCfg<X8, 64, 64, 2, 2, 2, 2>>(a, s);
   if (a.T <= 64) return launch_cfg<LinCfg<X8, 64, 128, 2, 2, 2, 2>>(a, s);
   const int64_t n128 = tiles_of(a, 128, 128), n256 = tiles_of(a, 256, 256);
