@@ -137,8 +137,8 @@ __device__ __forceinline__ void copy_pieces(const uint8_t* base, const uint32_t*
                  ::"v"(off[0]), "v"(off[1]), "s"(b), "s"(m) : "memory", "m0");
   } else if constexpr (N == 4) {
     asm volatile("s_mov_b32 m0, %5\n\tglobal_load_lds_dwordx4 %0, %4\n\tglobal_load_lds_dwordx4 %1, %4 offset:1024\n\t"
-                 "global_load_lds_dwordx4 %2, %4 offset:2048\n\tglobal_load_lds_dwordx4 %3, %4 offset:3072"
-                 ::"v"(off[0]), "v"(off[1]), "v"(off[2]), "v"(off[3]), "s"(b), "s"(m) : "memory", "m0");
+                 "global_load_lds_dwordx4 %2, %4 offset:2048\n\tglobal_load_lds_dwordx4 %3, %4 offset:%6"
+                 ::"v"(off[0]), "v"(off[1]), "v"(off[2]), "v"(off[3]), "s"(b), "s"(m), "n"(3 * 1024) : "memory", "m0");
   } else {
     static_assert(N % 4 == 0, "1, 2 or a multiple of 4");
 #pragma unroll
