@@ -125,7 +125,9 @@ constexpr int waitcnt_vm(int vm) {
 // assembly so that the compiler's dependency tracking does not treat every
 // later LDS read as aliasing the in-flight copies (it would wait for all of
 // them); the kernels order LDS reads after copies explicitly.  M0 (the copy's
-// LDS base) is not used for anything else in these kernels.
+// LDS base) is not used for anything else in these kernels.  The s_nop is the
+// wait state that the hardware wants between a scalar write of M0 and a copy
+// that reads it, which the compiler keeps for its own builtin alone.
 __device__ __forceinline__ uint32_t lds_addr(const void* p) {
   return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p));   // low half of the flat address
 }
@@ -152,22 +154,22 @@ __device__ __forceinline__ const void* uniform_ptr(const void* p) {
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"   // M0 is reserved; nothing else here uses it
 __device__ __forceinline__ void dma16(const void* g, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off"
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
                ::"v"(g), "s"(__builtin_amdgcn_readfirstlane(lds)) : "memory", "m0");
 }
 __device__ __forceinline__ void dma4(const void* g, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off"
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off"
                ::"v"(g), "s"(__builtin_amdgcn_readfirstlane(lds)) : "memory", "m0");
 }
 // Same copies addressed as a wave-uniform base (SGPR pair) plus a 32-bit
 // per-lane byte offset, which saves the per-lane 64-bit address registers.
 __device__ __forceinline__ void dma16_off(const void* base, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1"
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
                ::"v"(off), "s"(uniform_ptr(base)), "s"(__builtin_amdgcn_readfirstlane(lds))
                : "memory", "m0");
 }
 __device__ __forceinline__ void dma4_off(const void* base, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dword %0, %1"
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1"
                ::"v"(off), "s"(uniform_ptr(base)), "s"(__builtin_amdgcn_readfirstlane(lds))
                : "memory", "m0");
 }

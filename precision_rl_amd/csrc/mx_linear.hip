@@ -121,9 +121,10 @@ __device__ __forceinline__ void wait_stages(int later, bool extra) {
 // N copies of 1 KB to consecutive places in LDS, lane offsets off[0 .. N).  The
 // instruction's offset moves both of its addresses, so four copies share one
 // LDS base; off[j] leaves out what the instruction adds: the caller puts `base`
-// 3 KB before the tile and 3 KB less j % 4 KB into off[j].  Against an address
-// per copy a stage of one wave takes 131 instructions instead of 147 (T = 1, N =
-// 4096, K = 2048: 5.7 -> 5.3 us with FP8), 128 x 128 with FP4 at T = 16384 98 -> 92.
+// 3 KB before the tile and 3 KB less j % 4 KB into off[j]; the s_nop as in
+// dma16.  Against an address per copy a stage of one wave takes 16 instructions
+// fewer (T = 1, N = 4096, K = 2048: 5.7 -> 5.3 us with FP8), 128 x 128 with FP4
+// at T = 16384 98 -> 92.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"   // M0 is reserved; nothing else here uses it
 template <int N>
@@ -131,12 +132,12 @@ __device__ __forceinline__ void copy_pieces(const uint8_t* base, const uint32_t*
   const void* b = uniform_ptr(base);
   const uint32_t m = __builtin_amdgcn_readfirstlane(to);
   if constexpr (N == 1) {
-    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off[0]), "s"(b), "s"(m) : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off[0]), "s"(b), "s"(m) : "memory", "m0");
   } else if constexpr (N == 2) {
-    asm volatile("s_mov_b32 m0, %3\n\tglobal_load_lds_dwordx4 %0, %2\n\tglobal_load_lds_dwordx4 %1, %2 offset:1024"
+    asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %2\n\tglobal_load_lds_dwordx4 %1, %2 offset:1024"
                  ::"v"(off[0]), "v"(off[1]), "s"(b), "s"(m) : "memory", "m0");
   } else if constexpr (N == 4) {
-    asm volatile("s_mov_b32 m0, %5\n\tglobal_load_lds_dwordx4 %0, %4\n\tglobal_load_lds_dwordx4 %1, %4 offset:1024\n\t"
+    asm volatile("s_mov_b32 m0, %5\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %4\n\tglobal_load_lds_dwordx4 %1, %4 offset:1024\n\t"
                  "global_load_lds_dwordx4 %2, %4 offset:2048\n\tglobal_load_lds_dwordx4 %3, %4 offset:%6"
                  ::"v"(off[0]), "v"(off[1]), "v"(off[2]), "v"(off[3]), "s"(b), "s"(m), "n"(3 * 1024) : "memory", "m0");
   } else {
