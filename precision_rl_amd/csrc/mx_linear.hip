@@ -103,7 +103,11 @@ __device__ __forceinline__ void wait_lds() {
   __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0) alone
   asm volatile("" ::: "memory");
 }
-__device__ __forceinline__ void barrier() { asm volatile("s_barrier" ::: "memory"); }
+// Behind a barrier the next copies, or the results, overwrite what was read
+// last: this wave's reads are done at it, wherever the compiler puts the matrix
+// instructions that wait for them.  No cost where they are done already (the
+// counter is at zero).
+__device__ __forceinline__ void barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
 // Waits until everything up to a stage has landed, `later` stages (at most
 // MAX) having been issued after it: COPIES copies each, and SCALES more for
@@ -396,7 +400,7 @@ mx_linear_kernel(LinArgs a) {
   } else {
     for (int s = 0; s < C::S - 1 && s < stages; ++s) issue();
     for (int st = 0; st < stages; ++st) {
-      // stage st has landed in every wave, and every wave is past stage st - 1
+      // stage st has landed in every wave, and every wave has stage st - 1 in registers
       wait_stage(st, std::integral_constant<int, C::S - 2>{});
       barrier();
       if (next < stages) issue();

@@ -96,3 +96,26 @@ def hazards(code):
             if waited < 5:
                 todo += [(q, waited) for q in pred[p]]
     return found
+
+
+def lds_outstanding_at_barriers(code):
+    """Barriers (addresses) in front of which, on some path, an LDS operation of the wave may still be
+    outstanding: behind the barrier another wave may overwrite what it reads."""
+    pred = _predecessors(code)
+    follow = [[] for _ in code]
+    for k, ps in enumerate(pred):
+        for p in ps:
+            follow[p].append(k)
+    most, todo = [0] * len(code), list(range(len(code)))
+    while todo:
+        k = todo.pop()
+        n = max((most[p] for p in pred[k]), default=0)
+        if code[k][1].startswith("ds_"):
+            n = min(n + 1, 16)   # the counter has four bits
+        wait = re.search(r"lgkmcnt\((\d+)\)", code[k][2]) if code[k][1] == "s_waitcnt" else None
+        if wait:
+            n = min(n, int(wait.group(1)))
+        if n != most[k]:
+            most[k] = n
+            todo += follow[k]
+    return [i[0] for i, n in zip(code, most) if i[1] == "s_barrier" and n]

@@ -43,3 +43,25 @@ def test_copies_to_lds_keep_their_wait_states(kernels):
     assert len(copying) > 20
     bad = {n: h for n, c in copying.items() if (h := isa.hazards(c))}
     assert not bad, "\n".join(f"{n}: {len(h)} places, first {h[0]}" for n, h in bad.items())
+
+
+def test_checker_sees_lds_reads_behind_a_barrier():
+    read, wait = "ds_read_b128 v[0:3], v4", "s_waitcnt lgkmcnt(0)"
+    assert isa.lds_outstanding_at_barriers(_listing(read, "s_barrier")) == [4]
+    assert isa.lds_outstanding_at_barriers(_listing(read, read, "s_waitcnt lgkmcnt(1)", "s_barrier")) == [12]
+    assert not isa.lds_outstanding_at_barriers(_listing(read, wait, "s_barrier"))
+    # a read at the end of a loop whose barrier stands at its start
+    assert isa.lds_outstanding_at_barriers(_listing("s_barrier", read, "s_cbranch_scc1 65533")) == [0]
+
+
+def test_lds_reads_are_done_at_barriers(kernels):
+    """Of every kernel that copies to LDS; in the dense MX product, whose next copies overwrite what
+    was read last, by a wait directly in front of each barrier, which no order that the compiler gives
+    the matrix instructions (and the waits for their operands) can open."""
+    bad = {n: a for n, c in kernels if any("_lds_" in i[1] for i in c) and (a := isa.lds_outstanding_at_barriers(c))}
+    assert not bad
+    products = [(n, c) for n, c in kernels if "mx_linear_kernel" in n]
+    assert len(products) >= 10
+    for n, c in products:
+        before = [c[k - 1] for k, i in enumerate(c) if i[1] == "s_barrier"]
+        assert before and all(i[1] == "s_waitcnt" and "lgkmcnt(0)" in i[2] for i in before), n
