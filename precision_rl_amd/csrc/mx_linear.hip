@@ -28,6 +28,7 @@
 
 #include "gemm_common.h"
 #include "internal.h"
+#include "launch_parts.h"
 
 namespace w4a4 {
 namespace {
@@ -159,6 +160,7 @@ struct LinArgs {
   uint16_t* y;
   int64_t y_stride;
   int m_tiles, n_tiles;
+  int64_t first, count;   // the launch's tiles
 };
 
 template <class C>
@@ -175,11 +177,11 @@ mx_linear_kernel(LinArgs a) {
   // tiles that run together share both operands in the XCD's L2.
   int64_t tile;
   {
-    const int64_t total = static_cast<int64_t>(a.m_tiles) * a.n_tiles;
-    const int64_t per_xcd = (total + kXcds - 1) / kXcds;
+    const int64_t per_xcd = (a.count + kXcds - 1) / kXcds;
     const int64_t b = blockIdx.x;
     tile = (b % kXcds) * per_xcd + b / kXcds;
-    if (b / kXcds >= per_xcd || tile >= total) return;
+    if (b / kXcds >= per_xcd || tile >= a.count) return;
+    tile += a.first;
   }
   constexpr int kGroup = 8;
   const int64_t group = tile / (static_cast<int64_t>(kGroup) * a.n_tiles);
@@ -464,8 +466,11 @@ bool launch_cfg(LinArgs a, hipStream_t s) {
   if (attr != hipSuccess) return launch_ok("mx_linear") && false;
   a.m_tiles = static_cast<int>((a.T + C::BM - 1) / C::BM);
   a.n_tiles = (a.N + C::BN - 1) / C::BN;
-  const int64_t tiles = static_cast<int64_t>(a.m_tiles) * a.n_tiles;
-  launch_kernel("mx_linear", mx_linear_kernel<C>, dim3(xcd_grid(tiles)), dim3(C::kThreads), C::kLds, s, a);
+  launch_parts(static_cast<int64_t>(a.m_tiles) * a.n_tiles, C::kThreads, [&](int64_t first, int64_t count) {
+    a.first = first;
+    a.count = count;
+    launch_kernel("mx_linear", mx_linear_kernel<C>, dim3(xcd_grid(count)), dim3(C::kThreads), C::kLds, s, a);
+  });
   return launch_ok("mx_linear");
 }
 
@@ -527,7 +532,7 @@ bool launch_format(const LinArgs& a, hipStream_t s) {
 bool launch_mx_linear(int64_t T, int K, int N, bool x_fp8, const uint8_t* x, const uint8_t* xs, const uint8_t* w,
                       const uint8_t* ws, uint16_t* y, int64_t y_stride, hipStream_t s) {
   if (T == 0) return true;
-  const LinArgs a{T, K, N, x, xs, w, ws, y, y_stride, 0, 0};
+  const LinArgs a{T, K, N, x, xs, w, ws, y, y_stride, 0, 0, 0, 0};
   return x_fp8 ? launch_format<true>(a, s) : launch_format<false>(a, s);
 }
 

@@ -260,6 +260,32 @@ def test_linear_output_behind_four_gigabytes(b, fmt):
         assert torch.equal(y[t0:t0 + n], b.w4a4_mx_linear_fwd(part, wq, n, K, N)), t0
 
 
+@pytest.mark.parametrize("fmt,T", [("fp8", (1 << 30) + 300), ("fp4", (1 << 31) - 1)])
+def test_linear_of_more_rows_than_a_launch_holds(b, fmt, T):
+    """2^23 tiles of 512 threads (FP8), 2^24 of 256 (FP4): two launches. Rows at
+    the ends of each have the bits of the rows alone, rows between them their own."""
+    K, N, f = 128, 8, _fmt(b, fmt)
+    one = 0x38 if fmt == "fp8" else 0x22
+    n = 70
+    edges = [0, ((1 << 30) - 1024) - 35 if fmt == "fp8" else (1 << 31) - 1024 - 35, T - n]   # the second launch's first row
+    some, wq = _operands(b, n, K, N, f, 8)
+    print_case("mx_linear_many_rows", T=T, K=K, N=N, fmt=fmt)
+    xq = dict(codes=torch.full((T, K if fmt == "fp8" else K // 2), one, dtype=torch.uint8, device="cuda"),
+              scales=torch.full((T, K // 32), 127, dtype=torch.uint8, device="cuda"))
+    for t in edges:
+        for name in xq:
+            xq[name][t:t + n] = some[name]
+    y = b.w4a4_mx_linear_fwd(xq, wq, T, K, N)
+    alone = b.w4a4_mx_linear_fwd(some, wq, n, K, N)
+    ones = b.w4a4_mx_linear_fwd({name: v[n:n + 1].contiguous() for name, v in xq.items()}, wq, 1, K, N)
+    for t in edges:
+        assert torch.equal(y[t:t + n], alone), t
+    for t in (n, T // 2, T - n - 1):
+        assert torch.equal(y[t:t + 1], ones), t
+    del xq, y
+    torch.cuda.empty_cache()
+
+
 def test_layer_chain_on_a_stream_and_in_graphs(b):
     """The chain on a side stream and in three captured graphs, each with its own
     workspace, replayed in turn with eager work between: always the eager bits."""
