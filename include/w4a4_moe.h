@@ -454,7 +454,9 @@ w4a4_status w4a4_mx8_quantize(
  * `offsets` (optional, [2] int32 out) receives {0, T}, as w4a4_linear_bwd
  * reads it.  Tensors are 16-byte aligned, as everywhere; scales, rstd, dgamma
  * and offsets only to their element (the product reads scales by 4 bytes), so
- * that any rows of a batch can be passed alone.
+ * that any rows of a batch can be passed alone.  Outputs overlap no other
+ * tensor of a call but where it is said below; one that shares another's
+ * address all the same is W4A4_ERR_INVALID_ARG.
  */
 
 /*
@@ -482,7 +484,8 @@ w4a4_status w4a4_mx_quantize_rows(
  *   gamma      [H] gamma_dtype.     eps > 0, finite.
  *   sum        [T, H] residual_dtype out or NULL: s.  May be `residual`
  *              itself, or x where it is dense and bf16.
- *   y          [T, H] bf16 out or NULL.
+ *   y          [T, H] bf16 out or NULL.  May be x where that is dense, or a
+ *              bf16 residual.
  *   format     W4A4_MX_NONE (codes and scales NULL), W4A4_MX_FP4 or
  *              W4A4_MX_FP8.  codes, scales as in w4a4_mx_quantize_rows.
  *   rstd       [T] float out or NULL (the backward reads it).
@@ -506,9 +509,10 @@ w4a4_status w4a4_add_rmsnorm_fwd(
  *   dsum       [T, H] residual_dtype or NULL: the gradient that reaches s
  *              along the residual stream.
  *   dres       [T, H] residual_dtype out: the gradient of the residual and
- *              of x.  May be dsum itself, or dy where it is bf16.
+ *              of x.  May be dsum or sum itself, or dy where it is bf16.
  *   dx         [T, H] bf16 out or NULL: the same gradient rounded to bf16
- *              (for x beside a float residual stream).
+ *              (for x beside a float residual stream).  May be dy, and beside
+ *              a bf16 stream sum, dsum or dres.
  *              A row's gradient does not depend on the other rows.
  *   dgamma     [H] float out or NULL; zeros for T = 0.  Its sums run in an
  *              order that depends on T, H and residual_dtype alone.

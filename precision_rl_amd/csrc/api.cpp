@@ -11,6 +11,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <map>
 #include <mutex>
 #include <string>
@@ -768,6 +769,28 @@ w4a4_status check_stride(const char* what, int64_t stride, int64_t width) {
                 static_cast<long long>(stride), static_cast<long long>(width));
   return W4A4_OK;
 }
+// An output shares its address with no other tensor, but for the inputs that
+// its `over` (bits by their place in the list) names: those whose rows, and
+// elements, lie where the output's do, each read by the lane that writes there.
+struct Named {
+  const char* name;
+  const void* p;
+  unsigned over = 0;
+};
+w4a4_status check_apart(std::initializer_list<Named> outputs, std::initializer_list<Named> inputs) {
+  for (const Named* o = outputs.begin(); o != outputs.end(); ++o) {
+    if (o->p == nullptr) continue;
+    for (const Named* b = outputs.begin(); b != o; ++b)
+      if (b->p == o->p) return fail(W4A4_ERR_INVALID_ARG, "%s and %s may not share an address", b->name, o->name);
+    unsigned bit = 1;
+    for (const Named& i : inputs) {
+      if (i.p == o->p && !(o->over & bit))
+        return fail(W4A4_ERR_INVALID_ARG, "%s may not share the address of %s", o->name, i.name);
+      bit <<= 1;
+    }
+  }
+  return W4A4_OK;
+}
 }  // namespace
 
 w4a4_status w4a4_mx_quantize_rows(int64_t T, int K, int format, const void* x, int64_t x_stride, uint8_t* codes,
@@ -785,6 +808,8 @@ w4a4_status w4a4_mx_quantize_rows(int64_t T, int K, int format, const void* x, i
   }
   if ((st = check_element_ptr("offsets", offsets, 4, false)) != W4A4_OK) return st;
   if (T == 0 && offsets == nullptr) return W4A4_OK;
+  if (T > 0 && (st = check_apart({{"codes", codes}, {"scales", scales}, {"offsets", offsets}}, {{"x", x}})) != W4A4_OK)
+    return st;
   if (!launch_mx_quantize_rows(static_cast<const uint16_t*>(x), x_stride, T, K, format, codes, scales, offsets,
                                static_cast<hipStream_t>(stream)))
     return W4A4_ERR_LAUNCH;
@@ -825,6 +850,14 @@ w4a4_status w4a4_add_rmsnorm_fwd(int64_t T, int H, float eps, const void* x, int
   if ((st = check_element_ptr("rstd", rstd, 4, false)) != W4A4_OK) return st;
   if ((st = check_element_ptr("offsets", offsets, 4, false)) != W4A4_OK) return st;
   if (T == 0 && offsets == nullptr) return W4A4_OK;
+  if (T > 0) {
+    constexpr unsigned kX = 1, kResidual = 2;
+    const unsigned y_over = (x_stride == H ? kX : 0) | (residual_dtype == W4A4_BF16 ? kResidual : 0);
+    st = check_apart({{"sum", sum, kX | kResidual}, {"y", y, y_over}, {"codes", codes}, {"scales", scales},
+                      {"rstd", rstd}, {"offsets", offsets}},
+                     {{"x", x}, {"residual", residual}, {"gamma", gamma}});
+    if (st != W4A4_OK) return st;
+  }
   const NormFwdArgs a{T, H, eps, static_cast<const uint16_t*>(x), x_stride, residual, T > 0 ? gamma : nullptr,
                       gamma_dtype == W4A4_F32, sum, static_cast<uint16_t*>(y), codes, scales, rstd, offsets, false, 0};
   if (!launch_add_rmsnorm(a, residual_dtype == W4A4_F32, format, static_cast<hipStream_t>(stream)))
@@ -859,6 +892,15 @@ w4a4_status w4a4_add_rmsnorm_bwd(int64_t T, int H, const void* dy, const void* s
     if (workspace == nullptr || workspace_bytes < need)
       return fail(W4A4_ERR_WORKSPACE, "workspace needs %zu bytes", need);
     REQUIRE_PTR(workspace);
+  }
+  if (T > 0) {
+    constexpr unsigned kDy = 1, kSum = 2, kDsum = 4;
+    const bool bf16 = residual_dtype == W4A4_BF16;
+    // over dres, in bf16, dx holds the same values
+    st = check_apart({{"dres", dres, kDy | kSum | kDsum},
+                      {"dx", bf16 && dx == dres ? nullptr : dx, bf16 ? kDy | kSum | kDsum : kDy}, {"dgamma", dgamma}},
+                     {{"dy", dy}, {"sum", sum}, {"dsum", dsum}, {"rstd", rstd}, {"gamma", gamma}});
+    if (st != W4A4_OK) return st;
   }
   NormBwdArgs a{};
   a.T = T;
@@ -898,6 +940,9 @@ w4a4_status w4a4_mx_linear_fwd(int64_t T, int K, int N, int format, const uint8_
     REQUIRE_PTR(y);
     if ((st = check_element_ptr("x_scales", x_scales, 4, true)) != W4A4_OK) return st;
     if ((st = check_element_ptr("w_scales", w_scales, 4, true)) != W4A4_OK) return st;
+    st = check_apart({{"y", y}}, {{"x_codes", x_codes}, {"x_scales", x_scales}, {"w_codes", w_codes},
+                                  {"w_scales", w_scales}});
+    if (st != W4A4_OK) return st;
   }
   if (!launch_mx_linear(T, K, N, format == W4A4_MX_FP8, x_codes, x_scales, w_codes, w_scales,
                         static_cast<uint16_t*>(y), y_stride, static_cast<hipStream_t>(stream)))
