@@ -489,6 +489,14 @@ def _mx_buffers(out, T, K, fmt, device):
     return (_ptr(codes, "codes", cs, torch.uint8, device), _ptr(scales, "scales", ss, torch.uint8, device))
 
 
+def _check_workspace(ws, nbytes, index):
+    """A caller's workspace: enough dense bytes on device `index`, or an error (one that is too small
+    is not replaced, which a program that captures a graph would not notice)."""
+    if ws.dtype is not torch.uint8 or ws.get_device() != index or not ws.is_contiguous() or ws.numel() < nbytes:
+        raise W4A4Error(f"workspace: {nbytes} contiguous bytes (torch.uint8) on device {index} expected, "
+                        f"got {ws.dtype} {tuple(ws.shape)} with strides {ws.stride()} on {ws.device}")
+
+
 def w4a4_mx_quantize_rows(x, fmt, out=None):
     """MXFP4 (fmt MX_FP4) or MXFP8 (MX_FP8) of the rows of x [T, K] bf16 (K % 32 == 0; a column slice
     of a wider matrix will do).  Returns a dict: codes [T, K/2] or [T, K] u8, scales [T, K/32] u8
@@ -539,7 +547,8 @@ def w4a4_add_rmsnorm_bwd(dy, sum, gamma, rstd, dsum=None, dgamma=True, out=None,
     sum: the forward's (its x where there was no residual), rstd: the forward's.  Returns a dict:
     dres [T, H] (the type of `sum`), the gradient of the residual and of x, and dgamma [H] float32
     unless `dgamma` is false.  Tensors of `out` are used where given; a `dx` there ([T, H] bf16)
-    receives dres rounded to bf16."""
+    receives dres rounded to bf16.  workspace: at least workspace_size(WS_RMSNORM_BACKWARD, T, H, 0, 1, 1)
+    bytes (uint8) where dgamma is wanted; allocated where it is not given."""
     (T, H), dev = _matrix(dy, "dy", torch.bfloat16)
     rt = _dtype(sum, "sum")
     res = {} if out is None else dict(out)
@@ -550,8 +559,10 @@ def w4a4_add_rmsnorm_bwd(dy, sum, gamma, rstd, dsum=None, dgamma=True, out=None,
         if res.get("dgamma") is None:
             res["dgamma"] = torch.empty(H, dtype=torch.float32, device=dev)
         nbytes = workspace_size(WS_RMSNORM_BACKWARD, T, H, 0, 1, 1)
-        if nbytes:
-            workspace = _workspace(nbytes, dev, workspace)
+        if workspace is not None:
+            _check_workspace(workspace, nbytes, dev.index)
+        elif nbytes:
+            workspace = _workspace(nbytes, dev)
     _call(load().w4a4_add_rmsnorm_bwd, dev, T, H, _ptr(dy, "dy", dy.shape, torch.bfloat16, dev),
           _ptr(sum, "sum", dy.shape, sum.dtype, dev), rt, _ptr(gamma, "gamma", (H,), gamma.dtype, dev),
           _dtype(gamma, "gamma"), _ptr(rstd, "rstd", (T,), torch.float32, dev),
