@@ -1082,16 +1082,10 @@ unsigned persistent_grid(int64_t tiles) {
   return xcd_grid(std::min<int64_t>(tiles, cap));
 }
 
-template <typename Kern>
-hipError_t set_lds(Kern k, int bytes) {
-  return hipFuncSetAttribute(reinterpret_cast<const void*>(k),
-                             hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-}
-
 template <dg::DgradMode MODE>
 bool launch_dgrad(const dg::DgradArgs& a, const char* name, hipStream_t s) {
-  static const hipError_t attr = set_lds(&dg::dgrad_kernel<MODE>, dg::kLdsBytes);
-  if (attr != hipSuccess) return launch_ok(name) && false;
+  static OncePerDevice lds;
+  if (!set_lds(lds, &dg::dgrad_kernel<MODE>, dg::kLdsBytes)) return launch_ok(name) && false;
   // The A operand arrives 64 k at a time: every caller's K (H, 2I, the dense
   // layer's N) is a multiple of 256, which the shape checks enforce.
   if (a.K % 64 != 0) return false;
@@ -1128,9 +1122,10 @@ int wgrad_split_max(int M, int N) {
 size_t wgrad_sched_ints(const WgradPlan& p) { return wg::kSchedTable + 4 * static_cast<size_t>(p.tiles); }
 
 bool launch_wgrad(const wg::WgradArgs& a, const char* name, hipStream_t s, int split = 1) {
-  static const hipError_t attr = set_lds(&wg::wgrad_kernel<false>, wg::kLdsBytes);
-  static const hipError_t attr_split = set_lds(&wg::wgrad_kernel<true>, wg::kLdsBytes);
-  if (attr != hipSuccess || attr_split != hipSuccess) return launch_ok(name) && false;
+  static OncePerDevice lds, lds_split;
+  if (!set_lds(lds, &wg::wgrad_kernel<false>, wg::kLdsBytes) ||
+      !set_lds(lds_split, &wg::wgrad_kernel<true>, wg::kLdsBytes))
+    return launch_ok(name) && false;
   const WgradPlan p = wgrad_plan(a.M, a.N, a.E, split);
   if (p.tiles == 0) return true;
   if (a.partial != nullptr)

@@ -654,9 +654,8 @@ fwd_mx_kernel(FwdArgs args) {
 
 template <FwdMode MODE>
 bool launch_fwd_mx(const FwdArgs& args, int n_tiles, const char* name, hipStream_t s) {
-  static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&fwd_mx_kernel<MODE>),
-                                                     hipFuncAttributeMaxDynamicSharedMemorySize, kMxLdsBytes);
-  if (attr != hipSuccess) return launch_ok(name) && false;
+  static OncePerDevice lds;
+  if (!set_lds(lds, &fwd_mx_kernel<MODE>, kMxLdsBytes)) return launch_ok(name) && false;
   const int64_t tiles = grouped_m_tiles_bound(args.rows_alloc, args.E, kBM) * n_tiles;
   if (tiles == 0) return true;
   launch_kernel(name, fwd_mx_kernel<MODE>, dim3(xcd_grid(tiles)), dim3(kThreads), kMxLdsBytes, s, args);
@@ -880,9 +879,8 @@ mx8_gemm_kernel(Mx8Args args) {
 
 template <bool WGRAD>
 bool launch_mx8(const Mx8Args& args, int64_t tiles, const char* name, hipStream_t s) {
-  static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&mx8_gemm_kernel<WGRAD>),
-                                                     hipFuncAttributeMaxDynamicSharedMemorySize, kM8LdsBytes);
-  if (attr != hipSuccess) return launch_ok(name) && false;
+  static OncePerDevice lds;
+  if (!set_lds(lds, &mx8_gemm_kernel<WGRAD>, kM8LdsBytes)) return launch_ok(name) && false;
   if (tiles == 0) return true;
   launch_kernel(name, mx8_gemm_kernel<WGRAD>, dim3(xcd_grid(tiles)), dim3(kThreads), kM8LdsBytes, s, args);
   return launch_ok(name);
@@ -890,10 +888,8 @@ bool launch_mx8(const Mx8Args& args, int64_t tiles, const char* name, hipStream_
 
 template <FwdMode MODE, bool GS>
 bool launch_fwd_variant(const FwdArgs& args, int64_t tiles, const char* name, hipStream_t s) {
-  static const hipError_t attr = hipFuncSetAttribute(
-      reinterpret_cast<const void*>(&fwd_gemm_kernel<MODE, GS>),
-      hipFuncAttributeMaxDynamicSharedMemorySize, FwdLds<GS>::kBytes);
-  if (attr != hipSuccess) return launch_ok(name) && false;
+  static OncePerDevice lds;
+  if (!set_lds(lds, &fwd_gemm_kernel<MODE, GS>, FwdLds<GS>::kBytes)) return launch_ok(name) && false;
   launch_kernel(name, fwd_gemm_kernel<MODE, GS>, dim3(xcd_grid(tiles)), dim3(kThreads), FwdLds<GS>::kBytes, s,
                 args);
   return launch_ok(name);

@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include "../../include/w4a4_moe.h"
+#include "once_per_device.h"
 
 namespace w4a4 {
 
@@ -31,6 +32,18 @@ inline void launch_kernel(const char* name, void (*kernel)(Params...), dim3 grid
 
 // Records the HIP error of the last launch; returns false on failure.
 bool launch_ok(const char* what);
+
+// Lets a kernel use `bytes` of dynamic LDS on the current device.  The limit is
+// one of the device's own copy of the kernel, so a process that launches on
+// several sets it on each: `done` is the kernel's.
+template <typename Kern>
+inline bool set_lds(OncePerDevice& done, Kern kernel, int bytes) {
+  int device = 0;
+  return hipGetDevice(&device) == hipSuccess && done(device, [&] {
+           return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                      hipFuncAttributeMaxDynamicSharedMemorySize, bytes) == hipSuccess;
+         });
+}
 
 // Compute units of the current device (queried once).
 int device_cu_count();

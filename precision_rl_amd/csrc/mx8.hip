@@ -261,10 +261,8 @@ bool launch_q8_dual(const uint16_t* x, const uint16_t* h, int64_t R, int C, int 
     launch_kernel(name, q8_dual_kernel<false>, grid, dim3(kQ8Threads), dual_lds_bytes<false>(), st, x, h, R, C, I,
                   offsets, E, pitch, q_r, s_r, q_c, s_c);
   } else {
-    static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&q8_dual_kernel<true>),
-                                                       hipFuncAttributeMaxDynamicSharedMemorySize,
-                                                       dual_lds_bytes<true>());
-    if (attr != hipSuccess) return launch_ok(name) && false;
+    static OncePerDevice lds;
+    if (!set_lds(lds, &q8_dual_kernel<true>, dual_lds_bytes<true>())) return launch_ok(name) && false;
     launch_kernel(name, q8_dual_kernel<true>, grid, dim3(kQ8Threads), dual_lds_bytes<true>(), st, x, h, R, C, I,
                   offsets, E, pitch, q_r, s_r, q_c, s_c);
   }

@@ -461,9 +461,8 @@ mx_linear_kernel(LinArgs a) {
 
 template <class C>
 bool launch_cfg(LinArgs a, hipStream_t s) {
-  static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(&mx_linear_kernel<C>),
-                                                     hipFuncAttributeMaxDynamicSharedMemorySize, C::kLds);
-  if (attr != hipSuccess) return launch_ok("mx_linear") && false;
+  static OncePerDevice lds;
+  if (!set_lds(lds, &mx_linear_kernel<C>, C::kLds)) return launch_ok("mx_linear") && false;
   a.m_tiles = static_cast<int>((a.T + C::BM - 1) / C::BM);
   a.n_tiles = (a.N + C::BN - 1) / C::BN;
   launch_parts(static_cast<int64_t>(a.m_tiles) * a.n_tiles, C::kThreads, [&](int64_t first, int64_t count) {

@@ -523,9 +523,8 @@ bool launch_bwd_variant(const NormBwdArgs& a, int blocks, hipStream_t s) {
   const uint32_t lds = DG ? static_cast<uint32_t>(THREADS / TEAM) * a.H * 4u : 0u;
   const auto kernel = norm_bwd_kernel<THREADS, TEAM, P, RES, DG>;
   if constexpr (DG) {
-    static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                                       hipFuncAttributeMaxDynamicSharedMemorySize, THREADS * P * 32);
-    if (attr != hipSuccess) return launch_ok("add_rmsnorm_bwd") && false;
+    static OncePerDevice limit;
+    if (!set_lds(limit, kernel, THREADS * P * 32)) return launch_ok("add_rmsnorm_bwd") && false;
   }
   launch_kernel("add_rmsnorm_bwd", kernel, dim3(static_cast<unsigned>(blocks)), dim3(THREADS), lds, s, a);
   return true;
