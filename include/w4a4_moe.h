@@ -440,7 +440,9 @@ w4a4_status w4a4_mx8_quantize(
  * addition, RMS norm, quantisation) and the projection itself on the formats
  * that gfx950's scaled matrix instructions take.  The projection's
  * straight-through backward is w4a4_linear_bwd on the bf16 y of the norm and
- * the bf16 weight (it does not see the forward's format), within its shapes.
+ * the bf16 weight (it does not see the forward's format).  That backward takes
+ * K and N that are multiples of 256 up to 8192: a product of another shape has
+ * no backward here.
  *
  * MX blocks as in the MXFP4 recipe and w4a4_mx8_expert_bwd above (32 elements
  * of a row, E8M0 byte X + 127, X = floor(log2 amax) - 2 for E2M1, - 8 for
@@ -537,8 +539,9 @@ w4a4_status w4a4_add_rmsnorm_bwd(
  *   y          [T, N] bf16 out, rows y_stride elements apart (>= N, a
  *              multiple of 8): columns [N, y_stride) are not touched.
  *   Requirements: K % 128 == 0 and N % 8 == 0 (else W4A4_ERR_UNSUPPORTED; K
- *   not a multiple of 32 is invalid), K <= 65536, N <= 2^30.  No workspace.  The bits of
- *   a row of y depend on that row and W alone: not on T, not on the other rows.
+ *   not a multiple of 32 is invalid), K <= 65536, N <= 2^30 (w4a4_linear_bwd:
+ *   both % 256 == 0 and <= 8192).  No workspace.  The bits of a row of y
+ *   depend on that row and W alone: not on T, not on the other rows.
  *   Accuracy: FP4 activations lose nothing but FP32 additions.  With FP8
  *   activations gfx950's matrix instruction adds groups of 8 adjacent products
  *   and cuts each below 2^-13 of the group's largest, so that an output is off

@@ -577,8 +577,9 @@ def w4a4_mx_linear_fwd(xq, wq, T, K, N, y=None):
     """y [T, N] = x W^T on MX operands, bf16 out, FP32 accumulation.
 
     xq: codes and scales of ``w4a4_add_rmsnorm_fwd`` or ``w4a4_mx_quantize_rows`` (MXFP8 or MXFP4, told
-    apart by the codes' width); wq: ``w4a4_mx_quantize_rows(w, MX_FP4)`` of the weight w [N, K].  K % 128 == 0, N % 8 == 0.  y: where to write (a column slice will do).
-    A row's bits do not depend on T or on the other rows."""
+    apart by the codes' width); wq: ``w4a4_mx_quantize_rows(w, MX_FP4)`` of the weight w [N, K].
+    K % 128 == 0, N % 8 == 0 (``w4a4_linear_bwd``, its backward: both % 256 == 0 and <= 8192).
+    y: where to write (a column slice will do).  A row's bits do not depend on T or on the other rows."""
     codes = xq["codes"]
     _, dev = _matrix(codes, "xq codes", torch.uint8)
     fmt = MX_FP8 if codes.shape[1] == K else MX_FP4

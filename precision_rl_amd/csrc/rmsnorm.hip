@@ -14,8 +14,9 @@
 // The forward sums the squares in FP64 and multiplies by rstd as the sum of
 // two floats, and y is rounded once: it is the bf16 nearest to the exact value.
 // That costs no time beside HBM, and no row's squares overflow or underflow.
-// Everything else is FP32.  All calls are bound by HBM: every tensor is read
-// or written once.  16384 rows of 2048 in bf16 with FP8 codes take 43 us (5.4
+// Everything else is FP32.  Calls of many rows are bound by HBM: every tensor is
+// read or written once.  The backward of few rows (kFewRows) reads dy and s a
+// second time, from the L2, for dgamma; short calls are bound by latency.  16384 rows of 2048 in bf16 with FP8 codes take 43 us (5.4
 // TB/s), with y and rstd 54 (5.6), the backward 48 (5.6); 4097 of 4096 with an
 // FP32 residual 37 (5.0), 8191 of 5120 the backward 115 (5.1); the quantiser of
 // 16384 rows of 4096 35 with FP8 (5.8), 32 with FP4 (5.2).  One row takes 2.6 us
@@ -38,7 +39,8 @@ constexpr int kFewRows = 512;
 // one (backward) takes a row instead of one wave: H = 2048, FP8 codes: T = 1 2.6
 // us against 4.5, T = 512 4.0 against 5.8, T = 2048 8.1 against 9.2, T = 3000 the
 // same; backward: T = 1 2.7 against 3.3, T = 61 2.8 against 4.0, T = 256 3.5
-// against 4.1, T = 512 5.7 against 4.7.
+// against 4.1, T = 512 5.7 against 4.7 (with dgamma; without it one wave takes a
+// row at every T).
 constexpr int kSpreadRows = 2048, kSpreadBwdRows = 256;
 
 // Whether a call's loads are non-temporal: where it moves more than three
