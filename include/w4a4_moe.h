@@ -486,8 +486,8 @@ w4a4_status w4a4_mx_quantize_rows(
  *   gamma      [H] gamma_dtype.     eps > 0, finite.
  *   sum        [T, H] residual_dtype out or NULL: s.  May be `residual`
  *              itself, or x where it is dense and bf16.
- *   y          [T, H] bf16 out or NULL.  May be x where that is dense, or a
- *              bf16 residual.
+ *   y          [T, H] bf16 out or NULL.  May be x where that is dense (or one
+ *              row), or a bf16 residual.
  *   format     W4A4_MX_NONE (codes and scales NULL), W4A4_MX_FP4 or
  *              W4A4_MX_FP8.  codes, scales as in w4a4_mx_quantize_rows.
  *   rstd       [T] float out or NULL (the backward reads it).

@@ -852,7 +852,7 @@ w4a4_status w4a4_add_rmsnorm_fwd(int64_t T, int H, float eps, const void* x, int
   if (T == 0 && offsets == nullptr) return W4A4_OK;
   if (T > 0) {
     constexpr unsigned kX = 1, kResidual = 2;
-    const unsigned y_over = (x_stride == H ? kX : 0) | (residual_dtype == W4A4_BF16 ? kResidual : 0);
+    const unsigned y_over = (x_stride == H || T == 1 ? kX : 0) | (residual_dtype == W4A4_BF16 ? kResidual : 0);
     st = check_apart({{"sum", sum, kX | kResidual}, {"y", y, y_over}, {"codes", codes}, {"scales", scales},
                       {"rstd", rstd}, {"offsets", offsets}},
                      {{"x", x}, {"residual", residual}, {"gamma", gamma}});

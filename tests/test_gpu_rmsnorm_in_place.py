@@ -37,6 +37,18 @@ def test_forward_over_its_inputs(b, T, H):
             assert torch.equal(got[n], ref[n]), (n, y_over, sum_over)
 
 
+def test_one_row_over_a_strided_x(b):
+    """Through the C call, whose one row has a pitch that nothing reads."""
+    H = 2048
+    x, g = _rows(np.random.default_rng(4), 1, H), torch.ones(H, device="cuda")
+    print_case("norm_one_strided_row")
+    want = b.w4a4_add_rmsnorm_fwd(x, g, 1e-6)["y"]
+    stream = torch.cuda.current_stream().cuda_stream
+    status = b.load().w4a4_add_rmsnorm_fwd(1, H, 1e-6, x.data_ptr(), 2 * H, None, 0, g.data_ptr(), 1, b.MX_NONE, None,
+                                           x.data_ptr(), None, None, None, None, stream)
+    assert status == 0 and torch.equal(x, want)
+
+
 @pytest.mark.parametrize("T,H", SHAPES)
 @pytest.mark.parametrize("res", ["bf16", "f32"])
 def test_backward_over_its_inputs(b, T, H, res):
