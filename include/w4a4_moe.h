@@ -85,7 +85,8 @@ typedef enum {
   W4A4_WS_LINEAR_BACKWARD = 3,  /* w4a4_linear_bwd: H = K, I = N; T, E, k, row_align unused */
   W4A4_WS_QUANTIZE_PERMUTE_DOMAIN = 4,  /* w4a4_quantize_permute_domain, any group_rows; H = K */
   W4A4_WS_MX8_BACKWARD = 5,             /* w4a4_mx8_expert_bwd */
-  W4A4_WS_RMSNORM_BACKWARD = 6          /* w4a4_add_rmsnorm_bwd with dgamma; I, E, k, row_align unused */
+  W4A4_WS_RMSNORM_BACKWARD = 6,         /* w4a4_add_rmsnorm_bwd with dgamma; I, E, k, row_align unused */
+  W4A4_WS_PERMUTE = 8                   /* w4a4_permute_fwd: T, E and k; the others unused (0 bytes for few tokens) */
 } w4a4_workspace_kind;
 
 /* Element formats of the MX calls with a format argument. */
@@ -95,7 +96,7 @@ typedef enum {
   W4A4_MX_FP8 = 1     /* MXFP8: E4M3FN codes, one per byte     */
 } w4a4_mx_format;
 
-/* Element types of the pre-norm's residual stream and gamma. */
+/* Element types of the pre-norm's residual stream and gamma, and of dispatched rows. */
 typedef enum { W4A4_BF16 = 0, W4A4_F32 = 1 } w4a4_dtype;
 
 /* Padded dispatched-row capacity: T*k + E*(row_align-1).  Returns -1 on bad
@@ -554,6 +555,123 @@ w4a4_status w4a4_mx_linear_fwd(
     const uint8_t* x_codes, const uint8_t* x_scales,
     const uint8_t* w_codes, const uint8_t* w_scales,
     void* y, int64_t y_stride, void* stream);
+
+/*
+ * Token dispatch around separate expert calls: the sort by expert, the way back
+ * with the router's weights applied, and both gradients, for experts that do
+ * not run inside w4a4_grouped_expert_fwd (other ranks' experts behind an
+ * all-to-all, experts in bf16) and for training the router.  Beside the
+ * library's own expert calls: rows [0, cap) of xp quantised with identity
+ * routing are the rows of w4a4_quantize_permute, and the expert calls run on
+ * them as cap tokens with k = 1 and row_map[r] = r.
+ *   Layout as in w4a4_quantize_permute (Expert-contiguous layout above), with
+ *   these additions.  An id outside [0, E) is a slot that is not dispatched
+ *   (another rank's expert, a dropped token): its row_map entry is -1, it takes
+ *   no row, and it adds nothing to its token.  A token may name an expert twice
+ *   (one row each, in slot order); E may be smaller than k.
+ *   `dtype` (w4a4_dtype) is the element type of rows and tokens alike.  H % 8 ==
+ *   0, H <= 65536, k <= 8, E <= 1024 (else W4A4_ERR_UNSUPPORTED); T >= 0 of any
+ *   size with at most 2^31 - 1 rows (tensors of T = 0 tokens may be NULL).
+ *   Token tensors (x, y, dx, dy) have rows *_stride elements apart (>= H, a
+ *   multiple of 8).  row_map, topk_w, dtopk_w, src_row and the offsets are
+ *   aligned to their element, everything else to 16 bytes.  No output may share
+ *   an address with another tensor of its call.
+ *   `rows`: rows that the expert-row buffer holds (cap, as a rule).  row_map
+ *   entries outside [0, rows) count as not dispatched.
+ *   A token's results do not depend on the other tokens.
+ */
+
+/*
+ * w4a4_permute_fwd -- xp[row_map[t, j]] = x[t], pad rows zero.
+ *   x          [T, H].   topk_idx [T, k] int32.   row_align 1, 16, 32, 64, 128.
+ *   xp         [cap, H] out, cap = w4a4_rows_capacity(T, k, E, row_align), or
+ *              NULL: the maps alone (x may be NULL then).  Rows at or past
+ *              expert_offsets[E] are not written, in src_row neither.
+ *   expert_offsets [E+1], row_map [T, k], src_row [cap] int32 out.
+ *   workspace  w4a4_workspace_size(W4A4_WS_PERMUTE, T, 0, 0, E, k, 1) bytes (may
+ *              be NULL where that is 0).
+ */
+w4a4_status w4a4_permute_fwd(
+    int64_t T, int H, int k, int E, int row_align, int dtype, const void* x, int64_t x_stride,
+    const int32_t* topk_idx, void* xp, int32_t* expert_offsets, int32_t* row_map, int32_t* src_row,
+    void* workspace, size_t workspace_bytes, void* stream);
+
+/* w4a4_permute_bwd -- dx[t] = rnd(sum_j dxp[row_map[t, j]]), FP32 in ascending
+ * j; zeros for a token without a dispatched slot.  dxp [rows, H], dx [T, H] out. */
+w4a4_status w4a4_permute_bwd(
+    int64_t T, int H, int k, int64_t rows, int dtype, const void* dxp, const int32_t* row_map,
+    void* dx, int64_t dx_stride, void* stream);
+
+/* w4a4_unpermute_fwd -- y[t] = rnd(sum_j topk_w[t, j] o[row_map[t, j]]), FP32 in
+ * ascending j, as the expert forward's own; zeros for a token without a
+ * dispatched slot (whose weights are not looked at).  o [rows, H], topk_w [T, k]
+ * float, y [T, H] out. */
+w4a4_status w4a4_unpermute_fwd(
+    int64_t T, int H, int k, int64_t rows, int dtype, const void* o, const int32_t* row_map,
+    const float* topk_w, void* y, int64_t y_stride, void* stream);
+
+/*
+ * w4a4_unpermute_bwd -- its gradients:
+ *   d_o[row_map[t, j]] = rnd(topk_w[t, j] dy[t])       pad rows zero
+ *   dtopk_w[t, j] = sum_h dy[t, h] o[row_map[t, j], h]  (FP32, in an order that
+ *              depends on H and dtype alone; 0 where not dispatched)
+ *   dy         [T, H].   o [rows, H]: the forward's (NULL without dtopk_w).
+ *   d_o        [rows, H] out or NULL; rows at or past expert_offsets[E] are not
+ *              written.   dtopk_w [T, k] float out or NULL.
+ *   expert_offsets [E+1], src_row: of the permute (read where d_o is wanted and
+ *              rows > T * k, to find the pad rows; else they may be NULL).
+ */
+w4a4_status w4a4_unpermute_bwd(
+    int64_t T, int H, int k, int E, int64_t rows, int dtype, const void* dy, int64_t dy_stride,
+    const void* o, const int32_t* row_map, const float* topk_w,
+    const int32_t* expert_offsets, const int32_t* src_row,
+    void* d_o, float* dtopk_w, void* stream);
+
+/*
+ * The SwiGLU between two products as a call of its own, with its input kept in
+ * 8 bits for the backward pass.  h = (gate, up) [T, 2I]: the first I columns of
+ * a row are the gate, the next I the up projection, as in the expert forward.
+ * The checkpoint is MXFP8 of h, the bytes of w4a4_mx_quantize_rows(h): h_codes
+ * [T, 2I], h_scales [T, 2I/32].  It takes 33/16 I bytes a row where bf16 h and a
+ * take 6 I, and the backward pass computes from its values throughout, as if
+ * they had been h (a block that held an infinity or a NaN is all NaN).
+ *   I % 8 == 0, I % 32 == 0 with codes or a checkpoint; I <= 65536 (else
+ *   W4A4_ERR_UNSUPPORTED).  `rows` (device, one int32, or NULL): rows at or past
+ *   min(T, *rows) are neither read nor written, so that T can be a capacity
+ *   (expert_offsets + E for an expert path's rows).  A row's results do not
+ *   depend on the other rows.  Alignment and overlaps as in the dense MX calls.
+ *   Arithmetic in FP32 from the bf16 or 8-bit values, each output rounded once;
+ *   the sigmoid by the hardware's exp2 and reciprocal, as in the expert path.
+ */
+
+/*
+ * w4a4_swiglu_fwd -- a = bf16(gate sigmoid(gate) up)
+ *   h          bf16, rows h_stride elements apart (>= 2I, a multiple of 8).
+ *   a          [T, I] bf16 out or NULL.
+ *   format     W4A4_MX_NONE (codes and scales NULL), W4A4_MX_FP4 or W4A4_MX_FP8:
+ *              codes, scales out = the MX encoding of the bf16 a, as
+ *              w4a4_mx_quantize_rows gives.
+ *   h_codes, h_scales  both or neither: the checkpoint, out.
+ *   At least one of a, codes and h_codes is wanted.
+ */
+w4a4_status w4a4_swiglu_fwd(
+    int64_t T, int I, const void* h, int64_t h_stride, const int32_t* rows, int format,
+    void* a, uint8_t* codes, uint8_t* scales, uint8_t* h_codes, uint8_t* h_scales, void* stream);
+
+/*
+ * w4a4_swiglu_bwd -- with s = sigmoid(gate):
+ *   dh = (bf16(da up s (1 + gate (1 - s))), bf16(da gate s))
+ *   a  = bf16(gate s up), for the weight gradient of the next product
+ *   da         [T, I] bf16: the gradient of a (NULL without dh).
+ *   h          bf16 as in the forward, or NULL with the checkpoint h_codes,
+ *              h_scales in its place.
+ *   dh         [T, 2I] bf16 out or NULL.  May be h where that is dense.
+ *   a          [T, I] bf16 out or NULL.  May be da.
+ */
+w4a4_status w4a4_swiglu_bwd(
+    int64_t T, int I, const void* da, const void* h, int64_t h_stride,
+    const uint8_t* h_codes, const uint8_t* h_scales, const int32_t* rows,
+    void* dh, void* a, void* stream);
 
 /* Static description of a status code. */
 const char* w4a4_status_string(int status);

@@ -25,6 +25,7 @@ Modules
 ``mxfp4``  the MXFP4 recipe's E8M0 codec and row quantiser (E2M1 elements,
            one power-of-two scale per 32).
 ``linear`` the dense per-token NVFP4 linear layer.
+``dispatch`` token dispatch by expert and SwiGLU, with their gradients.
 
 Parity status: every function here is pinned by tests under ``tests/``
 (``-m "not gpu"``) against closed forms, exact rational brute force, worked

@@ -52,6 +52,14 @@ _SIGS = {
     "w4a4_add_rmsnorm_bwd": (c_int, [c_i64, c_int, c_vp, c_vp, c_int, c_vp, c_int, c_vp, c_vp,
                                      c_vp, c_vp, c_vp, c_vp, c_sz, c_vp]),
     "w4a4_mx_linear_fwd": (c_int, [c_i64, c_int, c_int, c_int, c_vp, c_vp, c_vp, c_vp, c_vp, c_i64, c_vp]),
+    "w4a4_permute_fwd": (c_int, [c_i64, c_int, c_int, c_int, c_int, c_int, c_vp, c_i64, c_vp,
+                                 c_vp, c_vp, c_vp, c_vp, c_vp, c_sz, c_vp]),
+    "w4a4_permute_bwd": (c_int, [c_i64, c_int, c_int, c_i64, c_int, c_vp, c_vp, c_vp, c_i64, c_vp]),
+    "w4a4_unpermute_fwd": (c_int, [c_i64, c_int, c_int, c_i64, c_int, c_vp, c_vp, c_vp, c_vp, c_i64, c_vp]),
+    "w4a4_unpermute_bwd": (c_int, [c_i64, c_int, c_int, c_int, c_i64, c_int, c_vp, c_i64, c_vp, c_vp, c_vp,
+                                   c_vp, c_vp, c_vp, c_vp, c_vp]),
+    "w4a4_swiglu_fwd": (c_int, [c_i64, c_int, c_vp, c_i64, c_vp, c_int, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp]),
+    "w4a4_swiglu_bwd": (c_int, [c_i64, c_int, c_vp, c_vp, c_i64, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp]),
     "w4a4_check_routing": (c_int, [c_vp, c_i64, c_int, c_int, c_vp, c_vp]),
     "w4a4_quantize_permute_noalloc": (c_int, [c_vp, c_i64, c_int, c_vp, c_int, c_int, c_int,
                                               c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp]),
@@ -65,6 +73,7 @@ WS_QUANTIZE_PERMUTE, WS_FORWARD, WS_BACKWARD, WS_LINEAR_BACKWARD = 0, 1, 2, 3
 WS_QUANTIZE_PERMUTE_DOMAIN = 4
 WS_MX8_BACKWARD = 5
 WS_RMSNORM_BACKWARD = 6
+WS_PERMUTE = 8
 
 # Element formats of the MX calls (w4a4_mx_format) and types (w4a4_dtype)
 MX_NONE, MX_FP4, MX_FP8 = -1, 0, 1
@@ -592,6 +601,172 @@ def w4a4_mx_linear_fwd(xq, wq, T, K, N, y=None):
           _ptr(wq["scales"], "wq scales", (N, K // 32), torch.uint8, dev),
           _ptr(y, "y", (T, N), torch.bfloat16, dev, rows=True), _pitch(y))
     return y
+
+
+# ------------------------------------------------ token dispatch and SwiGLU
+# Checks and streams as the calls above.
+def _row(t):
+    """(T, k) of a routing tensor."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2 or not t.is_cuda:
+        raise W4A4Error("topk_idx, topk_w and row_map must be 2-d tensors on the GPU")
+    return t.shape
+
+
+def w4a4_permute_fwd(x, topk_idx, E, row_align=1, out=None, workspace=None):
+    """Rows of x [T, H] (bf16 or float32; a column slice will do) sorted by expert, one for each of a token's
+    k slots: xp[row_map[t, j]] = x[t], each expert's rows in ascending token order and padded with zeros to
+    a multiple of row_align.  topk_idx [T, k] int32; ids outside [0, E) are slots that are not dispatched
+    (row_map -1).  x None: the maps alone.
+
+    Returns a dict: xp [cap, H] (with x), offsets [E + 1], row_map [T, k], src_row [cap] int32, where cap =
+    rows_capacity(T, k, E, row_align); rows from offsets[E] on are not written.  Tensors of `out` are used where
+    given.  workspace: at least workspace_size(WS_PERMUTE, T, 0, 0, E, k) bytes (uint8), allocated where it is not
+    given."""
+    T, k = _row(topk_idx)
+    dev = topk_idx.device
+    res = {} if out is None else dict(out)
+    cap = max(0, T * k + E * (row_align - 1))
+    H, dtype, pitch, xptr, xp = 8, 0, 8, None, None
+    if x is not None:
+        (_, H), _ = _matrix(x, "x")
+        dtype, pitch = _dtype(x, "x"), _pitch(x)
+        xptr = _ptr(x, "x", (T, H), x.dtype, dev, rows=True)
+        xp = res.get("xp")
+        if xp is None:
+            xp = res["xp"] = torch.empty(cap, H, dtype=x.dtype, device=dev)
+        xp = _ptr(xp, "xp", (cap, H), x.dtype, dev)
+    for name, shape in (("offsets", (E + 1,)), ("row_map", (T, k)), ("src_row", (cap,))):
+        if res.get(name) is None:
+            res[name] = torch.empty(shape, dtype=torch.int32, device=dev)
+    nbytes = load().w4a4_workspace_size(WS_PERMUTE, T, 0, 0, E, k, 1)
+    if workspace is not None:
+        _check_workspace(workspace, nbytes, dev.index)
+    elif nbytes:
+        workspace = _workspace(nbytes, dev)
+    i32 = torch.int32
+    _call(_lib.w4a4_permute_fwd, dev, T, H, k, E, row_align, dtype, xptr, pitch,
+          _ptr(topk_idx, "topk_idx", (T, k), i32, dev), xp, _ptr(res["offsets"], "offsets", (E + 1,), i32, dev),
+          _ptr(res["row_map"], "row_map", (T, k), i32, dev), _ptr(res["src_row"], "src_row", (cap,), i32, dev),
+          workspace.data_ptr() if nbytes else None, workspace.numel() if nbytes else 0)
+    return res
+
+
+def w4a4_permute_bwd(dxp, perm, dx=None):
+    """Gradient of ``w4a4_permute_fwd``: dx[t] = sum_j dxp[row_map[t, j]] in FP32, rounded once.  dxp [rows, H] bf16
+    or float32; perm: the maps (row_map is read).  dx: where to write (a column slice will do)."""
+    (rows, H), dev = _matrix(dxp, "dxp")
+    row_map = perm["row_map"]
+    T, k = _row(row_map)
+    if dx is None:
+        dx = torch.empty(T, H, dtype=dxp.dtype, device=dev)
+    _call(load().w4a4_permute_bwd, dev, T, H, k, rows, _dtype(dxp, "dxp"), _ptr(dxp, "dxp", (rows, H), dxp.dtype, dev),
+          _ptr(row_map, "row_map", (T, k), torch.int32, dev), _ptr(dx, "dx", (T, H), dxp.dtype, dev, rows=True),
+          _pitch(dx))
+    return dx
+
+
+def w4a4_unpermute_fwd(o, perm, topk_w, y=None):
+    """y[t] = sum_j topk_w[t, j] o[row_map[t, j]] in FP32 over the dispatched slots, rounded once.  o [rows, H] bf16
+    or float32; perm: the maps (row_map is read); topk_w [T, k] float32.  y: where to write (a column slice will
+    do)."""
+    (rows, H), dev = _matrix(o, "o")
+    row_map = perm["row_map"]
+    T, k = _row(row_map)
+    if y is None:
+        y = torch.empty(T, H, dtype=o.dtype, device=dev)
+    _call(load().w4a4_unpermute_fwd, dev, T, H, k, rows, _dtype(o, "o"), _ptr(o, "o", (rows, H), o.dtype, dev),
+          _ptr(row_map, "row_map", (T, k), torch.int32, dev), _ptr(topk_w, "topk_w", (T, k), torch.float32, dev),
+          _ptr(y, "y", (T, H), o.dtype, dev, rows=True), _pitch(y))
+    return y
+
+
+def w4a4_unpermute_bwd(dy, o, perm, topk_w, do=True, dtopk_w=True, out=None):
+    """Gradients of ``w4a4_unpermute_fwd`` for dy [T, H], the gradient of y (a column slice will do): do [rows, H]
+    (the type of dy; do[row_map[t, j]] = topk_w[t, j] dy[t], pad rows zero, rows from offsets[E] on not written)
+    and dtopk_w [T, k] float32 (<dy[t], o[row_map[t, j]]>, 0 where not dispatched).  o: the forward's; None will do
+    without dtopk_w.  perm: the dict of ``w4a4_permute_fwd`` (or of a quantise-and-permute call).  Returns a dict of
+    what `do` and `dtopk_w` ask for; tensors of `out` are used where given."""
+    (T, H), dev = _matrix(dy, "dy")
+    row_map, offsets, src_row = perm["row_map"], perm["offsets"], perm["src_row"]
+    k = _row(row_map)[1]
+    res = {} if out is None else dict(out)
+    rows = (o if o is not None else src_row).shape[0]
+    d_o = dw = None
+    if do:
+        d_o = res.get("do")
+        if d_o is None:
+            d_o = res["do"] = torch.empty(rows, H, dtype=dy.dtype, device=dev)
+        d_o = _ptr(d_o, "do", (rows, H), dy.dtype, dev)
+    if dtopk_w:
+        dw = res.get("dtopk_w")
+        if dw is None:
+            dw = res["dtopk_w"] = torch.empty(T, k, dtype=torch.float32, device=dev)
+        dw = _ptr(dw, "dtopk_w", (T, k), torch.float32, dev)
+    i32 = torch.int32
+    _call(load().w4a4_unpermute_bwd, dev, T, H, k, offsets.shape[0] - 1, rows, _dtype(dy, "dy"),
+          _ptr(dy, "dy", (T, H), dy.dtype, dev, rows=True), _pitch(dy), _ptr(o, "o", (rows, H), dy.dtype, dev),
+          _ptr(row_map, "row_map", (T, k), i32, dev), _ptr(topk_w, "topk_w", (T, k), torch.float32, dev),
+          _ptr(offsets, "offsets", offsets.shape, i32, dev), _ptr(src_row, "src_row", (rows,), i32, dev), d_o, dw)
+    return res
+
+
+def _checkpoint(kept, T, width, dev):
+    """Addresses of an MXFP8 checkpoint's codes and scales [T, width]."""
+    return (_ptr(kept["h_codes"], "h_codes", (T, width), torch.uint8, dev),
+            _ptr(kept["h_scales"], "h_scales", (T, width // 32), torch.uint8, dev))
+
+
+def w4a4_swiglu_fwd(h, fmt=None, a=True, checkpoint=False, rows=None, out=None):
+    """a = gate sigmoid(gate) up of h = (gate, up) [T, 2I] bf16 (a column slice of a wider matrix will do), rounded
+    to bf16, with the MX encoding of a (fmt MX_FP4 or MX_FP8) and the MXFP8 checkpoint of h for
+    ``w4a4_swiglu_bwd``.
+
+    rows: int32 tensor of one element on the GPU, the number of rows in use (None: all T); rows behind them are
+    left as they are.  Returns a dict with what was asked for: a [T, I], codes and scales (with fmt), h_codes [T, 2I]
+    and h_scales [T, 2I/32] uint8 (with checkpoint).  Tensors of `out` are used where given."""
+    (T, W), dev = _matrix(h, "h", torch.bfloat16)
+    I = W // 2  # noqa: E741
+    if W % 2:
+        raise W4A4Error(f"h has an odd number of columns ({W})")
+    res = {} if out is None else dict(out)
+    if a and res.get("a") is None:
+        res["a"] = torch.empty(T, I, dtype=torch.bfloat16, device=dev)
+    codes, scales = (None, None) if fmt is None else _mx_buffers(res, T, I, fmt, dev)
+    hc = hs = None
+    if checkpoint:
+        if res.get("h_codes") is None:
+            res["h_codes"] = torch.empty(T, W, dtype=torch.uint8, device=dev)
+        if res.get("h_scales") is None:
+            res["h_scales"] = torch.empty(T, W // 32, dtype=torch.uint8, device=dev)
+        hc, hs = _checkpoint(res, T, W, dev)
+    _call(load().w4a4_swiglu_fwd, dev, T, I, _ptr(h, "h", (T, W), torch.bfloat16, dev, rows=True), _pitch(h),
+          _ptr(rows, "rows", (1,), torch.int32, dev), MX_NONE if fmt is None else fmt,
+          _ptr(res["a"], "a", (T, I), torch.bfloat16, dev) if a else None, codes, scales, hc, hs)
+    return res
+
+
+def w4a4_swiglu_bwd(da, kept, a=False, dh=True, rows=None, out=None):
+    """Gradient of ``w4a4_swiglu_fwd`` for da [T, I] bf16, the gradient of a.  kept: the bf16 h [T, 2I] (a column slice
+    will do) or a dict with its checkpoint (h_codes, h_scales), whose values then stand for h throughout.
+
+    Returns a dict: dh [T, 2I] bf16 unless `dh` is false (da may be None then), and with `a` the forward's output
+    once more [T, I] (for the next product's weight gradient).  rows as in the forward.  Tensors of `out` are
+    used where given: its dh may be a dense kept h, its a may be da."""
+    ckpt = isinstance(kept, dict)
+    (T, W), dev = _matrix(kept["h_codes"], "h_codes", torch.uint8) if ckpt else _matrix(kept, "h", torch.bfloat16)
+    I = W // 2  # noqa: E741
+    res = {} if out is None else dict(out)
+    if dh and res.get("dh") is None:
+        res["dh"] = torch.empty(T, W, dtype=torch.bfloat16, device=dev)
+    if a and res.get("a") is None:
+        res["a"] = torch.empty(T, I, dtype=torch.bfloat16, device=dev)
+    hc, hs = _checkpoint(kept, T, W, dev) if ckpt else (None, None)
+    _call(load().w4a4_swiglu_bwd, dev, T, I, _ptr(da, "da", (T, I), torch.bfloat16, dev),
+          None if ckpt else _ptr(kept, "h", (T, W), torch.bfloat16, dev, rows=True), W if ckpt else _pitch(kept),
+          hc, hs, _ptr(rows, "rows", (1,), torch.int32, dev),
+          _ptr(res["dh"], "dh", (T, W), torch.bfloat16, dev) if dh else None,
+          _ptr(res["a"], "a", (T, I), torch.bfloat16, dev) if a else None)
+    return res
 
 
 def w4a4_profiler_enable(on=True):

@@ -85,6 +85,8 @@ bool valid_align(int a) { return a == 1 || a == 16 || a == 32 || a == 64 || a ==
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopK = 8;
 constexpr int kMaxRowLen = 8192;
+constexpr int kMaxWideRowLen = 65536;   // rows that are walked, not held in registers
+constexpr int64_t kMaxRows = (int64_t{1} << 31) - 1;
 
 // ------------------------------------------------------------------ profiler
 struct ProfEntry {
@@ -253,6 +255,10 @@ size_t w4a4_workspace_size(int kind, int64_t T, int H, int I, int E, int k, int 
   if (kind == W4A4_WS_RMSNORM_BACKWARD) {
     if (T < 0 || H <= 0 || H > kMaxRowLen) return 0;
     return round_up(norm_bwd_part_bytes(T, H));
+  }
+  if (kind == W4A4_WS_PERMUTE) {
+    if (T < 0 || k <= 0 || k > kMaxTopK || E <= 0 || E > kMaxExperts || T > kMaxRows / k) return 0;
+    return round_up(permute_workspace_bytes(T, k, E));
   }
   const int64_t cap = w4a4_rows_capacity(T, k, E, row_align);
   if (cap < 0 || H <= 0) return 0;
@@ -743,8 +749,6 @@ w4a4_status w4a4_mx8_quantize(const void* x, int64_t R, int C, uint8_t* q_rows, 
 }
 
 namespace {
-constexpr int64_t kMaxRows = (int64_t{1} << 31) - 1;
-
 bool valid_dtype(int d) { return d == W4A4_BF16 || d == W4A4_F32; }
 
 // Size checks shared by the dense MX calls.
@@ -947,6 +951,210 @@ w4a4_status w4a4_mx_linear_fwd(int64_t T, int K, int N, int format, const uint8_
   if (!launch_mx_linear(T, K, N, format == W4A4_MX_FP8, x_codes, x_scales, w_codes, w_scales,
                         static_cast<uint16_t*>(y), y_stride, static_cast<hipStream_t>(stream)))
     return W4A4_ERR_LAUNCH;
+  return W4A4_OK;
+}
+
+namespace {
+// Sizes shared by the dispatch calls; E = 0 where a call has none.
+w4a4_status check_dispatch(int64_t T, int H, int k, int E, int row_align, int dtype) {
+  w4a4_status st = check_rows(T, H, 8);
+  if (st != W4A4_OK) return st;
+  if (k <= 0 || E < 0) return fail(W4A4_ERR_INVALID_ARG, "bad k=%d / E=%d", k, E);
+  if (!valid_align(row_align)) return fail(W4A4_ERR_INVALID_ARG, "row_align %d not in {1,16,32,64,128}", row_align);
+  if (!valid_dtype(dtype)) return fail(W4A4_ERR_INVALID_ARG, "unknown element type %d", dtype);
+  if (H > kMaxWideRowLen) return fail(W4A4_ERR_UNSUPPORTED, "H=%d > %d", H, kMaxWideRowLen);
+  if (k > kMaxTopK || E > kMaxExperts)
+    return fail(W4A4_ERR_UNSUPPORTED, "E <= %d and k <= %d supported", kMaxExperts, kMaxTopK);
+  if (T * k + static_cast<int64_t>(E) * (row_align - 1) > kMaxRows)
+    return fail(W4A4_ERR_UNSUPPORTED, "T*k + E*(row_align-1) rows exceed int32 row indices");
+  return W4A4_OK;
+}
+w4a4_status check_buffer_rows(int64_t rows) {
+  if (rows < 0 || rows > kMaxRows)
+    return fail(W4A4_ERR_INVALID_ARG, "rows=%lld outside [0, 2^31)", static_cast<long long>(rows));
+  return W4A4_OK;
+}
+int64_t bytes_of(int dtype) { return dtype == W4A4_F32 ? 4 : 2; }
+
+// permute's gradient (w = NULL) and the unpermute.
+w4a4_status gather_rows(int64_t T, int H, int k, int64_t rows, int dtype, const char* src_name, const void* src,
+                        const int32_t* row_map, bool weighted, const float* w, const char* out_name, void* out,
+                        int64_t out_stride, const char* kernel, void* stream) {
+  w4a4_status st = check_dispatch(T, H, k, 0, 1, dtype);
+  if (st != W4A4_OK || (st = check_buffer_rows(rows)) != W4A4_OK) return st;
+  if ((st = check_stride(weighted ? "y_stride" : "dx_stride", out_stride, H)) != W4A4_OK) return st;
+  if (T == 0) return W4A4_OK;
+  if (rows > 0 && src == nullptr) return fail(W4A4_ERR_INVALID_ARG, "%s is NULL", src_name);
+  if (out == nullptr) return fail(W4A4_ERR_INVALID_ARG, "%s is NULL", out_name);
+  if (!aligned16(src)) return fail(W4A4_ERR_INVALID_ARG, "%s is not 16-byte aligned", src_name);
+  if (!aligned16(out)) return fail(W4A4_ERR_INVALID_ARG, "%s is not 16-byte aligned", out_name);
+  if ((st = check_element_ptr("row_map", row_map, 4, true)) != W4A4_OK) return st;
+  if ((st = check_element_ptr("topk_w", w, 4, weighted)) != W4A4_OK) return st;
+  if ((st = check_apart({{out_name, out}}, {{src_name, src}, {"row_map", row_map}, {"topk_w", w}})) != W4A4_OK) return st;
+  if (!launch_gather_rows(T, H, k, rows, dtype == W4A4_F32, src, row_map, w, out, out_stride * bytes_of(dtype), kernel,
+                          static_cast<hipStream_t>(stream)))
+    return W4A4_ERR_LAUNCH;
+  return W4A4_OK;
+}
+}  // namespace
+
+w4a4_status w4a4_permute_fwd(int64_t T, int H, int k, int E, int row_align, int dtype, const void* x, int64_t x_stride,
+                             const int32_t* topk_idx, void* xp, int32_t* expert_offsets, int32_t* row_map,
+                             int32_t* src_row, void* workspace, size_t workspace_bytes, void* stream) {
+  g_last_error.clear();
+  w4a4_status st = check_dispatch(T, H, k, E, row_align, dtype);
+  if (st != W4A4_OK) return st;
+  if (E == 0) return fail(W4A4_ERR_INVALID_ARG, "bad k=%d / E=%d", k, E);
+  if ((st = check_stride("x_stride", x_stride, H)) != W4A4_OK) return st;
+  if ((st = check_element_ptr("expert_offsets", expert_offsets, 4, true)) != W4A4_OK) return st;
+  size_t need = 0;
+  if (T > 0) {
+    if (xp != nullptr) REQUIRE_PTR(x);
+    OPTIONAL_PTR(x);
+    OPTIONAL_PTR(xp);
+    if ((st = check_element_ptr("topk_idx", topk_idx, 4, true)) != W4A4_OK) return st;
+    if ((st = check_element_ptr("row_map", row_map, 4, true)) != W4A4_OK) return st;
+    if ((st = check_element_ptr("src_row", src_row, 4, true)) != W4A4_OK) return st;
+    need = permute_workspace_bytes(T, k, E);
+    if (need > 0) {
+      if (workspace == nullptr || workspace_bytes < need)
+        return fail(W4A4_ERR_WORKSPACE, "workspace needs %zu bytes", need);
+      REQUIRE_PTR(workspace);
+    }
+    st = check_apart({{"xp", xp}, {"expert_offsets", expert_offsets}, {"row_map", row_map}, {"src_row", src_row},
+                      {"workspace", need > 0 ? workspace : nullptr}},
+                     {{"x", x}, {"topk_idx", topk_idx}});
+    if (st != W4A4_OK) return st;
+  }
+  const int64_t size = bytes_of(dtype);
+  if (!launch_permute(T, static_cast<int>(H * size), k, E, row_align, x, x_stride * size, topk_idx, xp, expert_offsets,
+                      row_map, src_row, need > 0 ? workspace : nullptr, static_cast<hipStream_t>(stream)))
+    return W4A4_ERR_LAUNCH;
+  return W4A4_OK;
+}
+
+w4a4_status w4a4_permute_bwd(int64_t T, int H, int k, int64_t rows, int dtype, const void* dxp, const int32_t* row_map,
+                             void* dx, int64_t dx_stride, void* stream) {
+  g_last_error.clear();
+  return gather_rows(T, H, k, rows, dtype, "dxp", dxp, row_map, false, nullptr, "dx", dx, dx_stride, "permute_bwd",
+                     stream);
+}
+
+w4a4_status w4a4_unpermute_fwd(int64_t T, int H, int k, int64_t rows, int dtype, const void* o, const int32_t* row_map,
+                               const float* topk_w, void* y, int64_t y_stride, void* stream) {
+  g_last_error.clear();
+  return gather_rows(T, H, k, rows, dtype, "o", o, row_map, true, topk_w, "y", y, y_stride, "unpermute_fwd", stream);
+}
+
+w4a4_status w4a4_unpermute_bwd(int64_t T, int H, int k, int E, int64_t rows, int dtype, const void* dy,
+                               int64_t dy_stride, const void* o, const int32_t* row_map, const float* topk_w,
+                               const int32_t* expert_offsets, const int32_t* src_row, void* d_o, float* dtopk_w,
+                               void* stream) {
+  g_last_error.clear();
+  w4a4_status st = check_dispatch(T, H, k, E, 1, dtype);
+  if (st != W4A4_OK || (st = check_buffer_rows(rows)) != W4A4_OK) return st;
+  if ((st = check_stride("dy_stride", dy_stride, H)) != W4A4_OK) return st;
+  if (T == 0) return W4A4_OK;
+  if (d_o == nullptr && dtopk_w == nullptr) return fail(W4A4_ERR_INVALID_ARG, "neither d_o nor dtopk_w is wanted");
+  REQUIRE_PTR(dy);
+  OPTIONAL_PTR(d_o);
+  if (dtopk_w != nullptr && rows > 0) REQUIRE_PTR(o);
+  OPTIONAL_PTR(o);
+  if ((st = check_element_ptr("row_map", row_map, 4, true)) != W4A4_OK) return st;
+  if ((st = check_element_ptr("topk_w", topk_w, 4, true)) != W4A4_OK) return st;
+  if ((st = check_element_ptr("dtopk_w", dtopk_w, 4, false)) != W4A4_OK) return st;
+  const bool pads = d_o != nullptr && rows > T * k;
+  if (pads && E == 0) return fail(W4A4_ERR_INVALID_ARG, "bad k=%d / E=%d", k, E);
+  if ((st = check_element_ptr("expert_offsets", expert_offsets, 4, pads)) != W4A4_OK) return st;
+  if ((st = check_element_ptr("src_row", src_row, 4, pads)) != W4A4_OK) return st;
+  st = check_apart({{"d_o", d_o}, {"dtopk_w", dtopk_w}},
+                   {{"dy", dy}, {"o", o}, {"row_map", row_map}, {"topk_w", topk_w}, {"expert_offsets", expert_offsets},
+                    {"src_row", src_row}});
+  if (st != W4A4_OK) return st;
+  if (!launch_unpermute_bwd(T, H, k, E, rows, dtype == W4A4_F32, dy, dy_stride * bytes_of(dtype), o, row_map, topk_w,
+                            expert_offsets, src_row, d_o, dtopk_w, static_cast<hipStream_t>(stream)))
+    return W4A4_ERR_LAUNCH;
+  return W4A4_OK;
+}
+
+w4a4_status w4a4_swiglu_fwd(int64_t T, int I, const void* h, int64_t h_stride, const int32_t* rows, int format, void* a,
+                            uint8_t* codes, uint8_t* scales, uint8_t* h_codes, uint8_t* h_scales, void* stream) {
+  g_last_error.clear();
+  if (format != W4A4_MX_NONE && format != W4A4_MX_FP4 && format != W4A4_MX_FP8)
+    return fail(W4A4_ERR_INVALID_ARG, "unknown format %d", format);
+  w4a4_status st = check_rows(T, I, format != W4A4_MX_NONE || h_codes != nullptr ? 32 : 8);
+  if (st != W4A4_OK) return st;
+  if (I > kMaxWideRowLen) return fail(W4A4_ERR_UNSUPPORTED, "I=%d > %d", I, kMaxWideRowLen);
+  if ((st = check_stride("h_stride", h_stride, 2 * static_cast<int64_t>(I))) != W4A4_OK) return st;
+  if (format == W4A4_MX_NONE && (codes != nullptr || scales != nullptr))
+    return fail(W4A4_ERR_INVALID_ARG, "codes and scales need a format");
+  if (T == 0) return W4A4_OK;
+  if ((h_codes == nullptr) != (h_scales == nullptr))
+    return fail(W4A4_ERR_INVALID_ARG, "h_codes and h_scales: both or neither");
+  REQUIRE_PTR(h);
+  OPTIONAL_PTR(a);
+  OPTIONAL_PTR(h_codes);
+  if (format != W4A4_MX_NONE) {
+    REQUIRE_PTR(codes);
+    if ((st = check_element_ptr("scales", scales, 1, true)) != W4A4_OK) return st;
+  }
+  if (a == nullptr && codes == nullptr && h_codes == nullptr)
+    return fail(W4A4_ERR_INVALID_ARG, "none of a, codes and h_codes is wanted");
+  if ((st = check_element_ptr("rows", rows, 4, false)) != W4A4_OK) return st;
+  st = check_apart({{"a", a}, {"codes", codes}, {"scales", scales}, {"h_codes", h_codes}, {"h_scales", h_scales}},
+                   {{"h", h}, {"rows", rows}});
+  if (st != W4A4_OK) return st;
+  SwigluArgs args{};
+  args.T = T;
+  args.I = I;
+  args.rows = rows;
+  args.h = static_cast<const uint16_t*>(h);
+  args.h_stride = h_stride;
+  args.h_codes = h_codes;
+  args.h_scales = h_scales;
+  args.a = static_cast<uint16_t*>(a);
+  args.codes = codes;
+  args.scales = scales;
+  if (!launch_swiglu_fwd(args, format, static_cast<hipStream_t>(stream))) return W4A4_ERR_LAUNCH;
+  return W4A4_OK;
+}
+
+w4a4_status w4a4_swiglu_bwd(int64_t T, int I, const void* da, const void* h, int64_t h_stride, const uint8_t* h_codes,
+                            const uint8_t* h_scales, const int32_t* rows, void* dh, void* a, void* stream) {
+  g_last_error.clear();
+  w4a4_status st = check_rows(T, I, h_codes != nullptr ? 32 : 8);
+  if (st != W4A4_OK) return st;
+  if (I > kMaxWideRowLen) return fail(W4A4_ERR_UNSUPPORTED, "I=%d > %d", I, kMaxWideRowLen);
+  if (h != nullptr && (st = check_stride("h_stride", h_stride, 2 * static_cast<int64_t>(I))) != W4A4_OK) return st;
+  if (T == 0) return W4A4_OK;
+  if ((h_codes == nullptr) != (h_scales == nullptr))
+    return fail(W4A4_ERR_INVALID_ARG, "h_codes and h_scales: both or neither");
+  if ((h == nullptr) == (h_codes == nullptr))
+    return fail(W4A4_ERR_INVALID_ARG, "either h or its checkpoint (h_codes, h_scales)");
+  if (dh == nullptr && a == nullptr) return fail(W4A4_ERR_INVALID_ARG, "neither dh nor a is wanted");
+  OPTIONAL_PTR(h);
+  OPTIONAL_PTR(h_codes);
+  OPTIONAL_PTR(dh);
+  OPTIONAL_PTR(a);
+  if (dh != nullptr) REQUIRE_PTR(da);
+  OPTIONAL_PTR(da);
+  if ((st = check_element_ptr("rows", rows, 4, false)) != W4A4_OK) return st;
+  constexpr unsigned kDa = 1, kH = 2;
+  st = check_apart({{"dh", dh, h_stride == 2 * static_cast<int64_t>(I) || T == 1 ? kH : 0}, {"a", a, kDa}},
+                   {{"da", da}, {"h", h}, {"h_codes", h_codes}, {"h_scales", h_scales}, {"rows", rows}});
+  if (st != W4A4_OK) return st;
+  SwigluArgs args{};
+  args.T = T;
+  args.I = I;
+  args.rows = rows;
+  args.h = static_cast<const uint16_t*>(h);
+  args.h_stride = h_stride;
+  args.h_codes = const_cast<uint8_t*>(h_codes);
+  args.h_scales = const_cast<uint8_t*>(h_scales);
+  args.da = dh != nullptr ? static_cast<const uint16_t*>(da) : nullptr;
+  args.a = static_cast<uint16_t*>(a);
+  args.dh = static_cast<uint16_t*>(dh);
+  if (!launch_swiglu_bwd(args, static_cast<hipStream_t>(stream))) return W4A4_ERR_LAUNCH;
   return W4A4_OK;
 }
 

@@ -1,0 +1,543 @@
+// Token dispatch around separate expert calls on gfx950: tokens sorted by
+// expert and back with the router's weights applied, and both gradients.
+//
+//   permute         xp[row_map[t,j]] = x[t];  pad rows zero
+//   its gradient    dx[t] = rnd(sum_j dxp[row_map[t,j]])
+//   unpermute       y[t] = rnd(sum_j p[t,j] o[row_map[t,j]])
+//   its gradient    do[row_map[t,j]] = rnd(p[t,j] dy[t]);  pad rows zero
+//                   dp[t,j] = sum_h dy[t,h] o[row_map[t,j],h]
+//
+// Sums run in FP32, those over j in ascending j, and are rounded once.  A slot
+// whose expert id lies outside [0, E) is not dispatched: its row_map entry is
+// -1 and it adds nothing.  Every row index is checked against the buffer's rows
+// before it is used.
+//
+// All four move rows of at least some hundred bytes and compute next to
+// nothing: HBM binds them, every row is read or written once, and a token's row
+// is read once for its k destinations.
+
+#include <type_traits>
+
+#include "device_common.h"
+#include "internal.h"
+#include "launch_parts.h"
+
+namespace w4a4 {
+namespace {
+
+typedef float floatx4_t __attribute__((ext_vector_type(4)));
+
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / kWave;
+constexpr int kMaxK = 8;
+constexpr int kMaxE = 1024;
+// Entries (token, slot) that one workgroup of the counting kernel ranks.
+constexpr int kRankChunk = 1024;
+
+int64_t rank_chunks(int64_t T, int k) { return (T * k + kRankChunk - 1) / kRankChunk; }
+
+// Whether every workgroup finds its own ranks in the whole list of entries.
+bool one_launch(int64_t T, int k) { return T * k <= kRankChunk; }
+
+// A 16-byte chunk of a row.
+template <typename T>
+struct Chunk;
+template <>
+struct Chunk<uint16_t> {   // bf16
+  static constexpr int N = 8;
+  u32x4_t w;
+  __device__ __forceinline__ float get(int i) const {
+    return __uint_as_float((i & 1) ? (w[i >> 1] & 0xFFFF0000u) : (w[i >> 1] << 16));
+  }
+  __device__ __forceinline__ void put(const float (&v)[8]) {
+#pragma unroll
+    for (int d = 0; d < 4; ++d) w[d] = pack_bf16x2(v[2 * d], v[2 * d + 1]);
+  }
+};
+template <>
+struct Chunk<float> {
+  static constexpr int N = 4;
+  u32x4_t w;
+  __device__ __forceinline__ float get(int i) const { return __uint_as_float(w[i]); }
+  __device__ __forceinline__ void put(const float (&v)[4]) {
+#pragma unroll
+    for (int d = 0; d < 4; ++d) w[d] = __float_as_uint(v[d]);
+  }
+};
+
+// --------------------------------------------------------------- the maps
+// Per chunk of 1024 entries, one thread each: a bit per entry in the mask of
+// its expert and wave; an entry's rank within the chunk is the number of set
+// bits before its own (ascending t * k + j, also where a token names an expert
+// twice), parked in row_map, and the chunk's counts go to `counts`.
+__global__ void __launch_bounds__(kRankChunk)
+permute_count_kernel(int64_t n, int E, const int32_t* __restrict__ idx, int32_t* __restrict__ row_map,
+                     int32_t* __restrict__ counts) {
+  constexpr int W = kRankChunk / kWave;
+  extern __shared__ __attribute__((aligned(16))) uint32_t count_lds[];   // [W][E] 64-bit masks, then [W][E] prefixes
+  uint32_t* const mask = count_lds;
+  uint16_t* const prefix = reinterpret_cast<uint16_t*>(count_lds + 2 * W * E);
+  const int tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave;
+  for (int i = tid; i < 2 * W * E; i += kRankChunk) mask[i] = 0u;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kRankChunk + tid;
+  const int e = i < n ? idx[i] : -1;
+  const bool live = static_cast<uint32_t>(e) < static_cast<uint32_t>(E);
+  __syncthreads();
+  const int m = wave * E + e;
+  if (live) atomicOr(&mask[2 * m + lane / 32], 1u << (lane % 32));
+  __syncthreads();
+  if (tid < E) {
+    int run = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      prefix[w * E + tid] = static_cast<uint16_t>(run);
+      run += __popc(mask[2 * (w * E + tid)]) + __popc(mask[2 * (w * E + tid) + 1]);
+    }
+    counts[static_cast<int64_t>(blockIdx.x) * E + tid] = run;
+  }
+  __syncthreads();
+  if (live) {
+    const uint32_t lo = mask[2 * m], hi = mask[2 * m + 1], below = (1u << (lane % 32)) - 1u;
+    row_map[i] = prefix[m] + (lane < 32 ? __popc(lo & below) : __popc(lo) + __popc(hi & below));
+  }
+}
+inline int count_lds_bytes(int E) { return kRankChunk / kWave * E * 10; }
+
+struct PermuteArgs {
+  int64_t T;
+  int chunks, k, E, align;             // chunks: 16-byte chunks of a row
+  const uint8_t* x;
+  int64_t x_pitch;                     // bytes
+  const int32_t* idx;
+  uint8_t* xp;                         // null: the maps alone
+  int32_t *offsets, *row_map, *src_row;
+  const int32_t *counts, *expert_count;
+  int64_t token_blocks, first;         // workgroups of tokens (those of pad rows follow); this launch's first
+};
+
+// Zeros in the pad rows of an expert whose group's pad rows are [r0, r1).
+__device__ __forceinline__ void clear_pad_rows(const PermuteArgs& a, int r0, int r1) {
+  for (int r = r0 + static_cast<int>(threadIdx.x); r < r1; r += kThreads) a.src_row[r] = -1;
+  if (a.xp == nullptr) return;
+  for (int r = r0 + static_cast<int>(threadIdx.x) / kWave; r < r1; r += kWaves) {
+    u32x4_t* row = reinterpret_cast<u32x4_t*>(a.xp) + static_cast<int64_t>(r) * a.chunks;
+    for (int c = threadIdx.x % kWave; c < a.chunks; c += kWave) row[c] = u32x4_t{0u, 0u, 0u, 0u};
+  }
+}
+
+// x[t]'s chunk `lane` where there is one, loaded ahead of the row indices.
+__device__ __forceinline__ u32x4_t first_chunk(const PermuteArgs& a, int64_t t, int lane) {
+  u32x4_t v{0u, 0u, 0u, 0u};
+  if (a.xp != nullptr && t < a.T && lane < a.chunks)
+    v = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(a.x + t * a.x_pitch) + lane);
+  return v;
+}
+template <int TEAM>
+__device__ __forceinline__ void copy_token(const PermuteArgs& a, int64_t t, int lane, u32x4_t v, const int32_t* rows) {
+  const u32x4_t* src = reinterpret_cast<const u32x4_t*>(a.x + t * a.x_pitch);
+  u32x4_t* dst = reinterpret_cast<u32x4_t*>(a.xp);
+  for (int c = lane; c < a.chunks; c += TEAM) {
+    if (c != lane) v = __builtin_nontemporal_load(src + c);
+    for (int j = 0; j < a.k; ++j) {
+      const int r = rows[j];
+      if (r >= 0) __builtin_nontemporal_store(v, dst + static_cast<int64_t>(r) * a.chunks + c);
+    }
+  }
+}
+
+// Up to kRankChunk entries in one launch: a workgroup per token counts the
+// experts of all entries, and those of its own before each of its slots, and
+// scans the padded group sizes, all in LDS.
+__global__ void __launch_bounds__(kThreads)
+permute_few_kernel(PermuteArgs a) {
+  __shared__ int32_t s_count[kMaxE], s_off[kMaxE + 1], s_wave[kWaves], s_below[kWaves][kMaxK], s_row[kMaxK];
+  const int tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave;
+  const bool pads = blockIdx.x >= a.token_blocks;
+  const int64_t t = pads ? a.T : blockIdx.x;
+  const u32x4_t v = first_chunk(a, t, tid);
+  for (int e = tid; e < a.E; e += kThreads) s_count[e] = 0;
+  const int n = static_cast<int>(a.T) * a.k, own0 = static_cast<int>(t) * a.k;
+  int own[kMaxK], below[kMaxK];
+#pragma unroll
+  for (int j = 0; j < kMaxK; ++j) {
+    own[j] = !pads && j < a.k ? a.idx[own0 + j] : -1;
+    below[j] = 0;
+  }
+  __syncthreads();
+  for (int i0 = 0; i0 < n; i0 += kThreads) {
+    const int i = i0 + tid;
+    const int e = i < n ? a.idx[i] : -1;
+    if (static_cast<uint32_t>(e) < static_cast<uint32_t>(a.E)) atomicAdd(&s_count[e], 1);
+#pragma unroll
+    for (int j = 0; j < kMaxK; ++j)
+      if (j < a.k) below[j] += __popcll(__ballot(i < own0 + j && e == own[j]));
+  }
+  if (lane == 0) {
+#pragma unroll
+    for (int j = 0; j < kMaxK; ++j) s_below[wave][j] = below[j];
+  }
+  __syncthreads();
+  // exclusive scan of the padded group sizes: a thread's consecutive experts,
+  // the wave's lanes, the waves
+  const int per = (a.E + kThreads - 1) / kThreads, e0 = min(a.E, tid * per), e1 = min(a.E, e0 + per);
+  int mine = 0;
+  for (int e = e0; e < e1; ++e) mine += (s_count[e] + a.align - 1) / a.align * a.align;
+  int incl = mine;
+#pragma unroll
+  for (int d = 1; d < kWave; d <<= 1) {
+    const int u = __shfl_up(incl, d, kWave);
+    if (lane >= d) incl += u;
+  }
+  if (lane == kWave - 1) s_wave[wave] = incl;
+  __syncthreads();
+  int run = incl - mine;
+  for (int w = 0; w < wave; ++w) run += s_wave[w];
+  for (int e = e0; e < e1; ++e) {
+    s_off[e] = run;
+    run += (s_count[e] + a.align - 1) / a.align * a.align;
+  }
+  if (tid == kThreads - 1) s_off[a.E] = run;   // the last thread's sum is the total
+  __syncthreads();
+  if (blockIdx.x == 0)
+    for (int e = tid; e <= a.E; e += kThreads) a.offsets[e] = s_off[e];
+  if (pads) {
+    const int e = static_cast<int>(blockIdx.x - a.token_blocks);
+    clear_pad_rows(a, s_off[e] + s_count[e], s_off[e + 1]);
+    return;
+  }
+  if (tid < a.k) {
+    const int e = a.idx[own0 + tid];
+    int row = -1;
+    if (static_cast<uint32_t>(e) < static_cast<uint32_t>(a.E)) {
+      row = s_off[e];
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) row += s_below[w][tid];
+      a.src_row[row] = static_cast<int32_t>(t);
+    }
+    a.row_map[own0 + tid] = row;
+    s_row[tid] = row;
+  }
+  __syncthreads();
+  if (a.xp != nullptr) copy_token<kThreads>(a, t, tid, v, s_row);
+}
+
+// After the counts and their scan: TEAM lanes per token.
+template <int TEAM>
+__global__ void __launch_bounds__(kThreads)
+permute_rows_kernel(PermuteArgs a) {
+  constexpr int kTeams = kThreads / TEAM;
+  __shared__ int32_t s_row[kTeams * kMaxK];
+  const int tid = threadIdx.x, lane = tid % TEAM;
+  const int64_t block = a.first + blockIdx.x;
+  if (block >= a.token_blocks) {
+    const int e = static_cast<int>(block - a.token_blocks);
+    clear_pad_rows(a, a.offsets[e] + a.expert_count[e], a.offsets[e + 1]);
+    return;
+  }
+  const int64_t t0 = block * kTeams, t = t0 + tid / TEAM;
+  const u32x4_t v = first_chunk(a, t, lane);
+  const int64_t i = t0 * a.k + tid;
+  if (tid < kTeams * a.k && i < a.T * a.k) {
+    const int e = a.idx[i];
+    int row = -1;
+    if (static_cast<uint32_t>(e) < static_cast<uint32_t>(a.E)) {
+      row = a.offsets[e] + a.counts[i / kRankChunk * a.E + e] + a.row_map[i];
+      a.src_row[row] = static_cast<int32_t>(t0 + tid / a.k);
+    }
+    a.row_map[i] = row;
+    s_row[tid] = row;
+  }
+  __syncthreads();
+  if (t < a.T && a.xp != nullptr) copy_token<TEAM>(a, t, lane, v, s_row + tid / TEAM * a.k);
+}
+
+__global__ void __launch_bounds__(kThreads)
+clear_offsets_kernel(int32_t* offsets, int n) {
+  for (int i = threadIdx.x; i < n; i += kThreads) offsets[i] = 0;
+}
+
+// ------------------------------------------------------------ back to tokens
+struct GatherArgs {
+  int64_t T;
+  int chunks, k;
+  uint32_t rows;
+  const void* src;            // [rows, H]
+  const int32_t* row_map;
+  const float* w;             // null: 1
+  void* out;
+  int64_t out_pitch;          // bytes
+  int64_t first;
+};
+
+// TEAM lanes per token, lane l the chunks l, l + TEAM, ... of its row; a chunk's
+// k loads (at most K) are all in flight.
+template <typename T, int TEAM, int K>
+__global__ void __launch_bounds__(kThreads)
+gather_rows_kernel(GatherArgs a) {
+  constexpr int kTeams = kThreads / TEAM, N = Chunk<T>::N;
+  const int lane = threadIdx.x % TEAM;
+  const int64_t t = (a.first + blockIdx.x) * kTeams + threadIdx.x / TEAM;
+  if (t >= a.T) return;
+  int32_t row[K];
+  float w[K];
+#pragma unroll
+  for (int j = 0; j < K; ++j) {
+    row[j] = j < a.k ? a.row_map[t * a.k + j] : -1;
+    w[j] = a.w != nullptr && j < a.k ? a.w[t * a.k + j] : 1.0f;
+  }
+  const u32x4_t* src = static_cast<const u32x4_t*>(a.src);
+  u32x4_t* out = reinterpret_cast<u32x4_t*>(static_cast<uint8_t*>(a.out) + t * a.out_pitch);
+  for (int c = lane; c < a.chunks; c += TEAM) {
+    Chunk<T> v[K];
+#pragma unroll
+    for (int j = 0; j < K; ++j)
+      if (static_cast<uint32_t>(row[j]) < a.rows)
+        v[j].w = __builtin_nontemporal_load(src + static_cast<int64_t>(row[j]) * a.chunks + c);
+    float acc[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) acc[i] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+      if (static_cast<uint32_t>(row[j]) < a.rows) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc[i] = fmaf(w[j], v[j].get(i), acc[i]);
+      }
+    }
+    Chunk<T> o;
+    o.put(acc);
+    __builtin_nontemporal_store(o.w, out + c);
+  }
+}
+
+// ------------------------------------------------- gradient of the unpermute
+struct UnpermuteBwdArgs {
+  int64_t T;
+  int chunks, k, E;
+  uint32_t rows;
+  const void* dy;
+  int64_t dy_pitch;           // bytes
+  const void* o;              // null: no dp
+  const int32_t* row_map;
+  const float* w;
+  const int32_t *offsets, *src_row;   // where there can be pad rows
+  void* d_o;                  // null: dp alone
+  float* dw;
+  int64_t token_blocks, first;
+};
+
+// Sums of v[0 .. 7] over the wave: lane l gets that of slot l / 8.  Each of the
+// first three steps halves the slots a lane holds: 10 exchanges instead of 48.
+__device__ __forceinline__ float wave_sum8(const float (&v)[8]) {
+  const int lane = threadIdx.x % kWave;
+  float a[4], b[2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float keep = lane & 32 ? v[4 + i] : v[i], give = lane & 32 ? v[i] : v[4 + i];
+    a[i] = keep + __shfl_xor(give, 32, kWave);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float keep = lane & 16 ? a[2 + i] : a[i], give = lane & 16 ? a[i] : a[2 + i];
+    b[i] = keep + __shfl_xor(give, 16, kWave);
+  }
+  float c = (lane & 8 ? b[1] : b[0]) + __shfl_xor(lane & 8 ? b[0] : b[1], 8, kWave);
+#pragma unroll
+  for (int off = 4; off > 0; off >>= 1) c += __shfl_xor(c, off, kWave);
+  return c;
+}
+
+// Pad rows of expert e: up to 127 rows before its group's end with src_row -1.
+__device__ __forceinline__ void clear_pad_rows(const UnpermuteBwdArgs& a, int e) {
+  const int64_t lo = max(a.offsets[e], 0), hi = min(static_cast<int64_t>(a.offsets[e + 1]), static_cast<int64_t>(a.rows));
+  for (int64_t r = max(lo, hi - 127) + threadIdx.x / kWave; r < hi; r += kWaves) {
+    if (a.src_row[r] >= 0) continue;
+    u32x4_t* row = static_cast<u32x4_t*>(a.d_o) + r * a.chunks;
+    for (int c = threadIdx.x % kWave; c < a.chunks; c += kWave) row[c] = u32x4_t{0u, 0u, 0u, 0u};
+  }
+}
+
+// TEAM lanes per token: dy's chunk is loaded once, each slot's row of o is
+// multiplied into that slot's sum and the scaled chunk stored to its row of do.
+// A slot's sum: a lane's chunks in order, the wave's lanes by halves, the waves.
+template <typename T, int TEAM, int K>
+__global__ void __launch_bounds__(kThreads)
+unpermute_bwd_kernel(UnpermuteBwdArgs a) {
+  constexpr int kTeams = kThreads / TEAM, N = Chunk<T>::N;
+  __shared__ float s_sum[kWaves][8];
+  const int64_t block = a.first + blockIdx.x;
+  if (block >= a.token_blocks) {
+    clear_pad_rows(a, static_cast<int>(block - a.token_blocks));
+    return;
+  }
+  const int lane = threadIdx.x % TEAM;
+  const int64_t t = block * kTeams + threadIdx.x / TEAM;
+  const bool live = t < a.T;
+  int32_t row[K];
+  float w[K], sum[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
+#pragma unroll
+  for (int j = 0; j < K; ++j) {
+    row[j] = live && j < a.k ? a.row_map[t * a.k + j] : -1;
+    w[j] = live && j < a.k ? a.w[t * a.k + j] : 0.0f;
+  }
+  if (live) {
+    const u32x4_t* dy = reinterpret_cast<const u32x4_t*>(static_cast<const uint8_t*>(a.dy) + t * a.dy_pitch);
+    const u32x4_t* o = static_cast<const u32x4_t*>(a.o);
+    u32x4_t* d_o = static_cast<u32x4_t*>(a.d_o);
+    for (int c = lane; c < a.chunks; c += TEAM) {
+      Chunk<T> g, v[K];
+      g.w = __builtin_nontemporal_load(dy + c);
+      if (o != nullptr) {
+#pragma unroll
+        for (int j = 0; j < K; ++j)
+          if (static_cast<uint32_t>(row[j]) < a.rows)
+            v[j].w = __builtin_nontemporal_load(o + static_cast<int64_t>(row[j]) * a.chunks + c);
+      }
+#pragma unroll
+      for (int j = 0; j < K; ++j) {
+        if (static_cast<uint32_t>(row[j]) >= a.rows) continue;
+        if (d_o != nullptr) {
+          float p[N];
+#pragma unroll
+          for (int i = 0; i < N; ++i) p[i] = w[j] * g.get(i);
+          Chunk<T> q;
+          q.put(p);
+          __builtin_nontemporal_store(q.w, d_o + static_cast<int64_t>(row[j]) * a.chunks + c);
+        }
+        if (o != nullptr) {
+#pragma unroll
+          for (int i = 0; i < N; ++i) sum[j] = fmaf(g.get(i), v[j].get(i), sum[j]);
+        }
+      }
+    }
+  }
+  if (a.dw == nullptr) return;
+  const float total = wave_sum8(sum);   // slot (lane of the wave) / 8
+  const int wl = threadIdx.x % kWave, j = wl / 8;
+  if constexpr (TEAM == kWave) {
+    if (live && wl % 8 == 0 && j < a.k) a.dw[t * a.k + j] = total;
+  } else {
+    static_assert(TEAM == kThreads, "one token a workgroup");
+    if (wl % 8 == 0) s_sum[threadIdx.x / kWave][j] = total;
+    __syncthreads();
+    if (threadIdx.x < a.k) {
+      float v = s_sum[0][threadIdx.x];
+#pragma unroll
+      for (int u = 1; u < kWaves; ++u) v += s_sum[u][threadIdx.x];
+      a.dw[t * a.k + threadIdx.x] = v;
+    }
+  }
+}
+
+// Lanes per token: a wave for rows of up to 128 chunks (2 KB), else a workgroup.
+// It depends on the row's length alone, so that the sums over a row do.
+bool wave_per_token(int chunks) { return chunks <= 128; }
+
+template <class F>
+void with_slots(int k, F f) {
+  if (k == 1) f(std::integral_constant<int, 1>{});
+  else if (k == 2) f(std::integral_constant<int, 2>{});
+  else if (k <= 4) f(std::integral_constant<int, 4>{});
+  else f(std::integral_constant<int, 8>{});
+}
+
+}  // namespace
+
+size_t permute_workspace_bytes(int64_t T, int k, int E) {
+  return one_launch(T, k) ? 0 : static_cast<size_t>((rank_chunks(T, k) + 1) * E) * sizeof(int32_t);
+}
+
+bool launch_permute(int64_t T, int row_bytes, int k, int E, int row_align, const void* x, int64_t x_pitch,
+                    const int32_t* topk_idx, void* xp, int32_t* offsets, int32_t* row_map, int32_t* src_row, void* ws,
+                    hipStream_t s) {
+  if (T == 0) {
+    launch_kernel("permute_rows", clear_offsets_kernel, dim3(1), dim3(kThreads), 0, s, offsets, E + 1);
+    return launch_ok("permute_rows");
+  }
+  PermuteArgs a{T, row_bytes / 16, k, E, row_align, static_cast<const uint8_t*>(x), x_pitch, topk_idx,
+                static_cast<uint8_t*>(xp), offsets, row_map, src_row, nullptr, nullptr, T, 0};
+  const int pad_blocks = row_align > 1 ? E : 0;
+  if (one_launch(T, k)) {
+    launch_kernel("permute_rows", permute_few_kernel, dim3(static_cast<unsigned>(T + pad_blocks)), dim3(kThreads), 0,
+                  s, a);
+    return launch_ok("permute_rows");
+  }
+  static OncePerDevice lds;
+  if (!set_lds(lds, permute_count_kernel, count_lds_bytes(kMaxE))) return launch_ok("permute_count") && false;
+  const int64_t chunks = rank_chunks(T, k);
+  int32_t* counts = static_cast<int32_t*>(ws);
+  a.counts = counts;
+  a.expert_count = counts + chunks * E;
+  launch_kernel("permute_count", permute_count_kernel, dim3(static_cast<unsigned>(chunks)), dim3(kRankChunk),
+                static_cast<uint32_t>(count_lds_bytes(E)), s, T * k, E, topk_idx, row_map, counts);
+  if (!launch_ok("permute_count")) return false;
+  if (!launch_route_scan(counts, static_cast<int>(chunks), E, row_align, offsets, counts + chunks * E, s)) return false;
+  auto rows = [&](auto team) {
+    constexpr int TEAM = decltype(team)::value, kTeams = kThreads / TEAM;
+    a.token_blocks = (T + kTeams - 1) / kTeams;
+    launch_parts(a.token_blocks + pad_blocks, kThreads, [&](int64_t first, int64_t count) {
+      a.first = first;
+      launch_kernel("permute_rows", permute_rows_kernel<TEAM>, dim3(static_cast<unsigned>(count)), dim3(kThreads), 0, s,
+                    a);
+    });
+  };
+  if (wave_per_token(a.chunks)) rows(std::integral_constant<int, kWave>{});
+  else rows(std::integral_constant<int, kThreads>{});
+  return launch_ok("permute_rows");
+}
+
+bool launch_gather_rows(int64_t T, int H, int k, int64_t rows, bool f32, const void* src, const int32_t* row_map,
+                        const float* w, void* out, int64_t out_pitch, const char* name, hipStream_t s) {
+  if (T == 0) return true;
+  GatherArgs a{T, H / (f32 ? 4 : 8), k, static_cast<uint32_t>(rows), src, row_map, w, out, out_pitch, 0};
+  auto go = [&](auto elem, auto team, auto slots) {
+    using Elem = decltype(elem);
+    constexpr int TEAM = decltype(team)::value, K = decltype(slots)::value, kTeams = kThreads / TEAM;
+    launch_parts((T + kTeams - 1) / kTeams, kThreads, [&](int64_t first, int64_t count) {
+      a.first = first;
+      launch_kernel(name, gather_rows_kernel<Elem, TEAM, K>, dim3(static_cast<unsigned>(count)), dim3(kThreads), 0, s,
+                    a);
+    });
+  };
+  with_slots(k, [&](auto slots) {
+    auto shape = [&](auto elem) {
+      if (wave_per_token(a.chunks)) go(elem, std::integral_constant<int, kWave>{}, slots);
+      else go(elem, std::integral_constant<int, kThreads>{}, slots);
+    };
+    if (f32) shape(float{});
+    else shape(uint16_t{});
+  });
+  return launch_ok(name);
+}
+
+bool launch_unpermute_bwd(int64_t T, int H, int k, int E, int64_t rows, bool f32, const void* dy, int64_t dy_pitch,
+                          const void* o, const int32_t* row_map, const float* w, const int32_t* offsets,
+                          const int32_t* src_row, void* d_o, float* dw, hipStream_t s) {
+  if (T == 0) return true;
+  UnpermuteBwdArgs a{T, H / (f32 ? 4 : 8), k, E, static_cast<uint32_t>(rows), dy, dy_pitch,
+                     dw != nullptr ? o : nullptr, row_map, w, offsets, src_row, d_o, dw, 0, 0};
+  // as many rows as slots: no group has been padded
+  const int pad_blocks = d_o != nullptr && rows > T * k ? E : 0;
+  auto go = [&](auto elem, auto team, auto slots) {
+    using Elem = decltype(elem);
+    constexpr int TEAM = decltype(team)::value, K = decltype(slots)::value, kTeams = kThreads / TEAM;
+    a.token_blocks = (T + kTeams - 1) / kTeams;
+    launch_parts(a.token_blocks + pad_blocks, kThreads, [&](int64_t first, int64_t count) {
+      a.first = first;
+      launch_kernel("unpermute_bwd", unpermute_bwd_kernel<Elem, TEAM, K>, dim3(static_cast<unsigned>(count)),
+                    dim3(kThreads), 0, s, a);
+    });
+  };
+  with_slots(k, [&](auto slots) {
+    auto shape = [&](auto elem) {
+      if (wave_per_token(a.chunks)) go(elem, std::integral_constant<int, kWave>{}, slots);
+      else go(elem, std::integral_constant<int, kThreads>{}, slots);
+    };
+    if (f32) shape(float{});
+    else shape(uint16_t{});
+  });
+  return launch_ok("unpermute_bwd");
+}
+
+}  // namespace w4a4

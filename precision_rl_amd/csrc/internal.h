@@ -59,6 +59,12 @@ bool launch_check_routing(const int32_t* topk_idx, int64_t T, int k, int E, int3
 
 size_t route_workspace_bytes(int64_t T, int E);
 
+// counts [n_chunks, E]: per expert, the exclusive prefix over the chunks in
+// place; expert_count [E] their totals, offsets [E + 1] the groups padded to
+// row_align.  E <= 1024.
+bool launch_route_scan(int32_t* counts, int n_chunks, int E, int row_align, int32_t* offsets, int32_t* expert_count,
+                       hipStream_t s);
+
 // Scratch of the allocation-free quantize+permute: a file-scope device array
 // of kNoAllocScratchBytes per GPU; noalloc_scratch() returns the current
 // device's address of it (looked up once per device; nullptr on failure).
@@ -246,6 +252,46 @@ bool launch_mx_quantize_rows(const uint16_t* x, int64_t x_stride, int64_t T, int
 // K % 128 == 0, N % 8 == 0, y rows y_stride elements apart.
 bool launch_mx_linear(int64_t T, int K, int N, bool x_fp8, const uint8_t* x, const uint8_t* xs, const uint8_t* w,
                       const uint8_t* ws, uint16_t* y, int64_t y_stride, hipStream_t s);
+
+// ------------------------------------- token dispatch and SwiGLU calls of their own
+// Maps of topk_idx (ids outside [0, E): not dispatched) and, with xp, x's rows
+// (row_bytes a multiple of 16, rows x_pitch bytes apart) copied to them, pad rows
+// cleared (dispatch.hip).  ws: permute_workspace_bytes(T, k, E), 0 for few
+// tokens.  k <= 8, E <= 1024.
+size_t permute_workspace_bytes(int64_t T, int k, int E);
+bool launch_permute(int64_t T, int row_bytes, int k, int E, int row_align, const void* x, int64_t x_pitch,
+                    const int32_t* topk_idx, void* xp, int32_t* offsets, int32_t* row_map, int32_t* src_row, void* ws,
+                    hipStream_t s);
+// out[t] = rnd(sum_j w[t,j] src[row_map[t,j]]) over the slots with a row in
+// [0, rows); w null: weights of 1.  Pitches in bytes.
+bool launch_gather_rows(int64_t T, int H, int k, int64_t rows, bool f32, const void* src, const int32_t* row_map,
+                        const float* w, void* out, int64_t out_pitch, const char* name, hipStream_t s);
+// d_o[row_map[t,j]] = rnd(w[t,j] dy[t]) (d_o null: not wanted) and dw[t,j] =
+// <dy[t], o[row_map[t,j]]> (dw null: not wanted); pad rows of d_o, told by
+// offsets and src_row, cleared where rows > T k.
+bool launch_unpermute_bwd(int64_t T, int H, int k, int E, int64_t rows, bool f32, const void* dy, int64_t dy_pitch,
+                          const void* o, const int32_t* row_map, const float* w, const int32_t* offsets,
+                          const int32_t* src_row, void* d_o, float* dw, hipStream_t s);
+
+// SwiGLU of h = (gate, up) [T, 2I] and its backward (swiglu.hip), on the rows
+// below min(T, *rows) (rows null: T).  Optional outputs may be null.  The kept
+// h: bf16 rows h_stride elements apart (h) or MXFP8 (h_codes, h_scales).
+struct SwigluArgs {
+  int64_t T;
+  int I;
+  const int32_t* rows;
+  const uint16_t* h;
+  int64_t h_stride;
+  uint8_t *h_codes, *h_scales;   // forward: out; backward: in
+  const uint16_t* da;
+  uint16_t *a, *dh;
+  uint8_t *codes, *scales;       // MX of a
+  int64_t first;                 // set by the launch: its first workgroup
+  uint32_t magic;                // likewise: 2^32 / chunks of a row, rounded up
+  bool stream;                   // likewise: non-temporal loads
+};
+bool launch_swiglu_fwd(const SwigluArgs& a, int format, hipStream_t s);
+bool launch_swiglu_bwd(const SwigluArgs& a, hipStream_t s);
 
 // dX gather-sum: dX[t] = bf16(sum_j dXp[row_map[t,j]]).
 bool launch_gather_sum(int64_t T, int H, int k, const uint16_t* dXp, const int32_t* row_map,
