@@ -113,7 +113,20 @@ struct PermuteArgs {
   int32_t *offsets, *row_map, *src_row;
   const int32_t *counts, *expert_count;
   int64_t token_blocks, first;         // workgroups of tokens (those of pad rows follow); this launch's first
+  bool stream;                         // x past the caches
 };
+
+// NT: past the caches.  A choice at run time around each load keeps the loads of
+// a lane from being in flight together (the combination below took 110 us with
+// it, 102 without): kernels with several are built both ways.
+template <bool NT>
+__device__ __forceinline__ u32x4_t load16(const u32x4_t* p) {
+  if constexpr (NT) return __builtin_nontemporal_load(p);
+  else return *p;
+}
+__device__ __forceinline__ u32x4_t load16(const u32x4_t* p, bool stream) {
+  return stream ? load16<true>(p) : load16<false>(p);
+}
 
 // Zeros in the pad rows of an expert whose group's pad rows are [r0, r1).
 __device__ __forceinline__ void clear_pad_rows(const PermuteArgs& a, int r0, int r1) {
@@ -129,7 +142,7 @@ __device__ __forceinline__ void clear_pad_rows(const PermuteArgs& a, int r0, int
 __device__ __forceinline__ u32x4_t first_chunk(const PermuteArgs& a, int64_t t, int lane) {
   u32x4_t v{0u, 0u, 0u, 0u};
   if (a.xp != nullptr && t < a.T && lane < a.chunks)
-    v = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(a.x + t * a.x_pitch) + lane);
+    v = load16(reinterpret_cast<const u32x4_t*>(a.x + t * a.x_pitch) + lane, a.stream);
   return v;
 }
 template <int TEAM>
@@ -137,7 +150,7 @@ __device__ __forceinline__ void copy_token(const PermuteArgs& a, int64_t t, int 
   const u32x4_t* src = reinterpret_cast<const u32x4_t*>(a.x + t * a.x_pitch);
   u32x4_t* dst = reinterpret_cast<u32x4_t*>(a.xp);
   for (int c = lane; c < a.chunks; c += TEAM) {
-    if (c != lane) v = __builtin_nontemporal_load(src + c);
+    if (c != lane) v = load16(src + c, a.stream);
     for (int j = 0; j < a.k; ++j) {
       const int r = rows[j];
       if (r >= 0) __builtin_nontemporal_store(v, dst + static_cast<int64_t>(r) * a.chunks + c);
@@ -271,7 +284,7 @@ struct GatherArgs {
 
 // TEAM lanes per token, lane l the chunks l, l + TEAM, ... of its row; a chunk's
 // k loads (at most K) are all in flight.
-template <typename T, int TEAM, int K>
+template <typename T, int TEAM, int K, bool NT>
 __global__ void __launch_bounds__(kThreads)
 gather_rows_kernel(GatherArgs a) {
   constexpr int kTeams = kThreads / TEAM, N = Chunk<T>::N;
@@ -292,7 +305,7 @@ gather_rows_kernel(GatherArgs a) {
 #pragma unroll
     for (int j = 0; j < K; ++j)
       if (static_cast<uint32_t>(row[j]) < a.rows)
-        v[j].w = __builtin_nontemporal_load(src + static_cast<int64_t>(row[j]) * a.chunks + c);
+        v[j].w = load16<NT>(src + static_cast<int64_t>(row[j]) * a.chunks + c);
     float acc[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) acc[i] = 0.0f;
@@ -319,120 +332,120 @@ struct UnpermuteBwdArgs {
   const void* o;              // null: no dp
   const int32_t* row_map;
   const float* w;
-  const int32_t *offsets, *src_row;   // where there can be pad rows
+  const int32_t *offsets, *src_row;   // offsets may be null where no group can be padded
   void* d_o;                  // null: dp alone
   float* dw;
-  int64_t token_blocks, first;
+  int64_t main_blocks, first; // workgroups of entries or tokens (those of pad rows follow); this launch's first
+  bool stream;                // do alone: dy past the caches
 };
 
-// Sums of v[0 .. 7] over the wave: lane l gets that of slot l / 8.  Each of the
-// first three steps halves the slots a lane holds: 10 exchanges instead of 48.
-__device__ __forceinline__ float wave_sum8(const float (&v)[8]) {
-  const int lane = threadIdx.x % kWave;
-  float a[4], b[2];
+// Rows in use: entries of row_map at or past this are not dispatched.
+__device__ __forceinline__ uint32_t used_rows(const UnpermuteBwdArgs& a) {
+  return a.offsets != nullptr ? min(a.rows, static_cast<uint32_t>(max(a.offsets[a.E], 0))) : a.rows;
+}
+
+template <typename T>
+__device__ __forceinline__ void store_scaled(const Chunk<T>& g, float w, u32x4_t* to) {
+  constexpr int N = Chunk<T>::N;
+  float p[N];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float keep = lane & 32 ? v[4 + i] : v[i], give = lane & 32 ? v[i] : v[4 + i];
-    a[i] = keep + __shfl_xor(give, 32, kWave);
-  }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float keep = lane & 16 ? a[2 + i] : a[i], give = lane & 16 ? a[i] : a[2 + i];
-    b[i] = keep + __shfl_xor(give, 16, kWave);
-  }
-  float c = (lane & 8 ? b[1] : b[0]) + __shfl_xor(lane & 8 ? b[0] : b[1], 8, kWave);
-#pragma unroll
-  for (int off = 4; off > 0; off >>= 1) c += __shfl_xor(c, off, kWave);
-  return c;
+  for (int i = 0; i < N; ++i) p[i] = w * g.get(i);
+  Chunk<T> q;
+  q.put(p);
+  __builtin_nontemporal_store(q.w, to);
+}
+
+__device__ __forceinline__ void clear_row(void* rows, int64_t r, int chunks) {
+  u32x4_t* row = static_cast<u32x4_t*>(rows) + r * chunks;
+  for (int c = threadIdx.x % kWave; c < chunks; c += kWave) row[c] = u32x4_t{0u, 0u, 0u, 0u};
 }
 
 // Pad rows of expert e: up to 127 rows before its group's end with src_row -1.
 __device__ __forceinline__ void clear_pad_rows(const UnpermuteBwdArgs& a, int e) {
   const int64_t lo = max(a.offsets[e], 0), hi = min(static_cast<int64_t>(a.offsets[e + 1]), static_cast<int64_t>(a.rows));
-  for (int64_t r = max(lo, hi - 127) + threadIdx.x / kWave; r < hi; r += kWaves) {
-    if (a.src_row[r] >= 0) continue;
-    u32x4_t* row = static_cast<u32x4_t*>(a.d_o) + r * a.chunks;
-    for (int c = threadIdx.x % kWave; c < a.chunks; c += kWave) row[c] = u32x4_t{0u, 0u, 0u, 0u};
-  }
+  for (int64_t r = max(lo, hi - 127) + threadIdx.x / kWave; r < hi; r += kWaves)
+    if (a.src_row[r] < 0) clear_row(a.d_o, r, a.chunks);
 }
 
-// TEAM lanes per token: dy's chunk is loaded once, each slot's row of o is
-// multiplied into that slot's sum and the scaled chunk stored to its row of do.
-// A slot's sum: a lane's chunks in order, the wave's lanes by halves, the waves.
-template <typename T, int TEAM, int K>
-__global__ void __launch_bounds__(kThreads)
-unpermute_bwd_kernel(UnpermuteBwdArgs a) {
-  constexpr int kTeams = kThreads / TEAM, N = Chunk<T>::N;
-  __shared__ float s_sum[kWaves][8];
-  const int64_t block = a.first + blockIdx.x;
-  if (block >= a.token_blocks) {
-    clear_pad_rows(a, static_cast<int>(block - a.token_blocks));
-    return;
-  }
-  const int lane = threadIdx.x % TEAM;
-  const int64_t t = block * kTeams + threadIdx.x / TEAM;
-  const bool live = t < a.T;
-  int32_t row[K];
-  float w[K], sum[8];
+// One wave: do[r] = w[i] dy[t] and dp[i] = <dy[t], o[r]> of entry i = t k + j.
+// Lane l takes the chunks l, l + 64, ... in order (four in flight), the lanes
+// join by halves: dp's bits depend on the row's length and type alone.
+template <typename T, bool NT>
+__device__ __forceinline__ void entry_grad(const UnpermuteBwdArgs& a, int64_t t, int64_t i, uint32_t r) {
+  constexpr int N = Chunk<T>::N, kAhead = 4;
+  const int lane = threadIdx.x % kWave;
+  const u32x4_t* dy = reinterpret_cast<const u32x4_t*>(static_cast<const uint8_t*>(a.dy) + t * a.dy_pitch);
+  const u32x4_t* o = static_cast<const u32x4_t*>(a.o) + static_cast<int64_t>(r) * a.chunks;
+  u32x4_t* d_o = static_cast<u32x4_t*>(a.d_o) + static_cast<int64_t>(r) * a.chunks;
+  const float w = a.w[i];
+  float sum = 0.0f;
+  for (int c0 = lane; c0 < a.chunks; c0 += kAhead * kWave) {
+    Chunk<T> g[kAhead], v[kAhead];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
+    for (int n = 0; n < kAhead; ++n) {
+      const int c = c0 + n * kWave;
+      if (c >= a.chunks) continue;
+      v[n].w = load16<NT>(o + c);
+      g[n].w = dy[c];
+    }
 #pragma unroll
-  for (int j = 0; j < K; ++j) {
-    row[j] = live && j < a.k ? a.row_map[t * a.k + j] : -1;
-    w[j] = live && j < a.k ? a.w[t * a.k + j] : 0.0f;
-  }
-  if (live) {
-    const u32x4_t* dy = reinterpret_cast<const u32x4_t*>(static_cast<const uint8_t*>(a.dy) + t * a.dy_pitch);
-    const u32x4_t* o = static_cast<const u32x4_t*>(a.o);
-    u32x4_t* d_o = static_cast<u32x4_t*>(a.d_o);
-    for (int c = lane; c < a.chunks; c += TEAM) {
-      Chunk<T> g, v[K];
-      g.w = __builtin_nontemporal_load(dy + c);
-      if (o != nullptr) {
+    for (int n = 0; n < kAhead; ++n) {
+      const int c = c0 + n * kWave;
+      if (c >= a.chunks) continue;
+      if (a.d_o != nullptr) store_scaled<T>(g[n], w, d_o + c);
 #pragma unroll
-        for (int j = 0; j < K; ++j)
-          if (static_cast<uint32_t>(row[j]) < a.rows)
-            v[j].w = __builtin_nontemporal_load(o + static_cast<int64_t>(row[j]) * a.chunks + c);
-      }
-#pragma unroll
-      for (int j = 0; j < K; ++j) {
-        if (static_cast<uint32_t>(row[j]) >= a.rows) continue;
-        if (d_o != nullptr) {
-          float p[N];
-#pragma unroll
-          for (int i = 0; i < N; ++i) p[i] = w[j] * g.get(i);
-          Chunk<T> q;
-          q.put(p);
-          __builtin_nontemporal_store(q.w, d_o + static_cast<int64_t>(row[j]) * a.chunks + c);
-        }
-        if (o != nullptr) {
-#pragma unroll
-          for (int i = 0; i < N; ++i) sum[j] = fmaf(g.get(i), v[j].get(i), sum[j]);
-        }
-      }
+      for (int q = 0; q < N; ++q) sum = fmaf(g[n].get(q), v[n].get(q), sum);
     }
   }
-  if (a.dw == nullptr) return;
-  const float total = wave_sum8(sum);   // slot (lane of the wave) / 8
-  const int wl = threadIdx.x % kWave, j = wl / 8;
-  if constexpr (TEAM == kWave) {
-    if (live && wl % 8 == 0 && j < a.k) a.dw[t * a.k + j] = total;
-  } else {
-    static_assert(TEAM == kThreads, "one token a workgroup");
-    if (wl % 8 == 0) s_sum[threadIdx.x / kWave][j] = total;
-    __syncthreads();
-    if (threadIdx.x < a.k) {
-      float v = s_sum[0][threadIdx.x];
 #pragma unroll
-      for (int u = 1; u < kWaves; ++u) v += s_sum[u][threadIdx.x];
-      a.dw[t * a.k + threadIdx.x] = v;
+  for (int off = kWave / 2; off > 0; off >>= 1) sum += __shfl_xor(sum, off, kWave);
+  if (lane == 0) a.dw[i] = sum;
+}
+
+// A wave per entry; pad rows by workgroups of their own.
+template <typename T, bool NT>
+__global__ void __launch_bounds__(kThreads)
+unpermute_bwd_entries_kernel(UnpermuteBwdArgs a) {
+  const int64_t block = a.first + blockIdx.x;
+  if (block >= a.main_blocks) {
+    clear_pad_rows(a, static_cast<int>(block - a.main_blocks));
+    return;
+  }
+  const int64_t i = block * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  if (i >= a.T * a.k) return;
+  const uint32_t r = static_cast<uint32_t>(a.row_map[i]);
+  if (r < used_rows(a)) entry_grad<T, NT>(a, i / a.k, i, r);
+  else if (threadIdx.x % kWave == 0) a.dw[i] = 0.0f;
+}
+
+// do alone: a workgroup per token, dy read once.
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+unpermute_bwd_scatter_kernel(UnpermuteBwdArgs a) {
+  const int64_t t = a.first + blockIdx.x;
+  if (t >= a.main_blocks) {
+    clear_pad_rows(a, static_cast<int>(t - a.main_blocks));
+    return;
+  }
+  const uint32_t used = used_rows(a);
+  const u32x4_t* dy = reinterpret_cast<const u32x4_t*>(static_cast<const uint8_t*>(a.dy) + t * a.dy_pitch);
+  for (int c = threadIdx.x; c < a.chunks; c += kThreads) {
+    Chunk<T> g;
+    g.w = load16(dy + c, a.stream);
+    for (int j = 0; j < a.k; ++j) {
+      const uint32_t r = static_cast<uint32_t>(a.row_map[t * a.k + j]);
+      if (r < used)
+        store_scaled<T>(g, a.w[t * a.k + j], static_cast<u32x4_t*>(a.d_o) + static_cast<int64_t>(r) * a.chunks + c);
     }
   }
 }
 
 // Lanes per token: a wave for rows of up to 128 chunks (2 KB), else a workgroup.
-// It depends on the row's length alone, so that the sums over a row do.
 bool wave_per_token(int chunks) { return chunks <= 128; }
+
+// Whether loads of so many bytes go past the 256 MiB memory-side cache, which
+// cannot hold them all from their producer.
+bool streams(double bytes) { return bytes > 0.75 * 256 * 1024 * 1024; }
 
 template <class F>
 void with_slots(int k, F f) {
@@ -456,7 +469,8 @@ bool launch_permute(int64_t T, int row_bytes, int k, int E, int row_align, const
     return launch_ok("permute_rows");
   }
   PermuteArgs a{T, row_bytes / 16, k, E, row_align, static_cast<const uint8_t*>(x), x_pitch, topk_idx,
-                static_cast<uint8_t*>(xp), offsets, row_map, src_row, nullptr, nullptr, T, 0};
+                static_cast<uint8_t*>(xp), offsets, row_map, src_row, nullptr, nullptr, T, 0,
+                streams(static_cast<double>(T) * row_bytes)};
   const int pad_blocks = row_align > 1 ? E : 0;
   if (one_launch(T, k)) {
     launch_kernel("permute_rows", permute_few_kernel, dim3(static_cast<unsigned>(T + pad_blocks)), dim3(kThreads), 0,
@@ -491,13 +505,14 @@ bool launch_gather_rows(int64_t T, int H, int k, int64_t rows, bool f32, const v
                         const float* w, void* out, int64_t out_pitch, const char* name, hipStream_t s) {
   if (T == 0) return true;
   GatherArgs a{T, H / (f32 ? 4 : 8), k, static_cast<uint32_t>(rows), src, row_map, w, out, out_pitch, 0};
+  const bool nt = streams(static_cast<double>(T) * k * H * (f32 ? 4 : 2));
   auto go = [&](auto elem, auto team, auto slots) {
     using Elem = decltype(elem);
     constexpr int TEAM = decltype(team)::value, K = decltype(slots)::value, kTeams = kThreads / TEAM;
     launch_parts((T + kTeams - 1) / kTeams, kThreads, [&](int64_t first, int64_t count) {
       a.first = first;
-      launch_kernel(name, gather_rows_kernel<Elem, TEAM, K>, dim3(static_cast<unsigned>(count)), dim3(kThreads), 0, s,
-                    a);
+      launch_kernel(name, nt ? gather_rows_kernel<Elem, TEAM, K, true> : gather_rows_kernel<Elem, TEAM, K, false>,
+                    dim3(static_cast<unsigned>(count)), dim3(kThreads), 0, s, a);
     });
   };
   with_slots(k, [&](auto slots) {
@@ -515,28 +530,31 @@ bool launch_unpermute_bwd(int64_t T, int H, int k, int E, int64_t rows, bool f32
                           const void* o, const int32_t* row_map, const float* w, const int32_t* offsets,
                           const int32_t* src_row, void* d_o, float* dw, hipStream_t s) {
   if (T == 0) return true;
-  UnpermuteBwdArgs a{T, H / (f32 ? 4 : 8), k, E, static_cast<uint32_t>(rows), dy, dy_pitch,
-                     dw != nullptr ? o : nullptr, row_map, w, offsets, src_row, d_o, dw, 0, 0};
-  // as many rows as slots: no group has been padded
-  const int pad_blocks = d_o != nullptr && rows > T * k ? E : 0;
-  auto go = [&](auto elem, auto team, auto slots) {
-    using Elem = decltype(elem);
-    constexpr int TEAM = decltype(team)::value, K = decltype(slots)::value, kTeams = kThreads / TEAM;
-    a.token_blocks = (T + kTeams - 1) / kTeams;
-    launch_parts(a.token_blocks + pad_blocks, kThreads, [&](int64_t first, int64_t count) {
+  UnpermuteBwdArgs a{T, H / (f32 ? 4 : 8), k, E, static_cast<uint32_t>(rows), dy, dy_pitch, o, row_map, w, offsets,
+                     src_row, d_o, dw, 0, 0, false};
+  const double row_bytes = 16.0 * a.chunks;
+  auto go = [&](int64_t main_blocks, int64_t others, auto kernel) {
+    a.main_blocks = main_blocks;
+    launch_parts(main_blocks + others, kThreads, [&](int64_t first, int64_t count) {
       a.first = first;
-      launch_kernel("unpermute_bwd", unpermute_bwd_kernel<Elem, TEAM, K>, dim3(static_cast<unsigned>(count)),
-                    dim3(kThreads), 0, s, a);
+      launch_kernel("unpermute_bwd", kernel, dim3(static_cast<unsigned>(count)), dim3(kThreads), 0, s, a);
     });
   };
-  with_slots(k, [&](auto slots) {
-    auto shape = [&](auto elem) {
-      if (wave_per_token(a.chunks)) go(elem, std::integral_constant<int, kWave>{}, slots);
-      else go(elem, std::integral_constant<int, kThreads>{}, slots);
-    };
-    if (f32) shape(float{});
-    else shape(uint16_t{});
-  });
+  // as many rows as slots: no group has been padded
+  const int pad_blocks = d_o != nullptr && rows > T * k ? E : 0;
+  if (dw == nullptr) {
+    a.stream = streams(T * row_bytes);
+    if (f32) go(T, pad_blocks, unpermute_bwd_scatter_kernel<float>);
+    else go(T, pad_blocks, unpermute_bwd_scatter_kernel<uint16_t>);
+    return launch_ok("unpermute_bwd");
+  }
+  const int64_t entry_blocks = (T * k + kWaves - 1) / kWaves;
+  auto entries = [&](auto nt) {
+    if (f32) go(entry_blocks, pad_blocks, unpermute_bwd_entries_kernel<float, decltype(nt)::value>);
+    else go(entry_blocks, pad_blocks, unpermute_bwd_entries_kernel<uint16_t, decltype(nt)::value>);
+  };
+  if (streams(T * k * row_bytes * (d_o != nullptr ? 2 : 1))) entries(std::true_type{});
+  else entries(std::false_type{});
   return launch_ok("unpermute_bwd");
 }
 
