@@ -36,8 +36,14 @@ constexpr int kRankChunk = 1024;
 
 int64_t rank_chunks(int64_t T, int k) { return (T * k + kRankChunk - 1) / kRankChunk; }
 
-// Whether every workgroup finds its own ranks in the whole list of entries.
-bool one_launch(int64_t T, int k) { return T * k <= kRankChunk; }
+// Whether every workgroup counts all entries itself, in one launch: T / 8
+// workgroups of T k entries each.  Against count, scan and copy in three launches
+// (rows of 512 bytes, on the device): 2048 tokens with 8 experts each 8.7 us
+// against 10.5, 4096 with one 7.6 against 10.1; 8192 with two 24.5 against 11.3.
+bool one_launch(int64_t T, int k) { return T <= 5792 && T * T * k <= int64_t{1} << 25; }
+// Up to how many tokens a workgroup takes one of them instead of eight: 256
+// tokens 4.9 us against 5.3, 512 6.2 against 5.8.
+constexpr int kOneTokenAWorkgroup = 256;
 
 // A 16-byte chunk of a row.
 template <typename T>
@@ -66,42 +72,117 @@ struct Chunk<float> {
 };
 
 // --------------------------------------------------------------- the maps
-// Per chunk of 1024 entries, one thread each: a bit per entry in the mask of
-// its expert and wave; an entry's rank within the chunk is the number of set
-// bits before its own (ascending t * k + j, also where a token names an expert
-// twice), parked in row_map, and the chunk's counts go to `counts`.
+// Lanes of the wave with the same e (below 1024) as this one, among `live` ones:
+// one vote per bit of e.
+__device__ __forceinline__ uint64_t same_lanes(int e, bool live) {
+  uint64_t m = __ballot(live);
+#pragma unroll
+  for (int bit = 0; bit < 10; ++bit) {
+    const uint64_t v = __ballot((e >> bit) & 1);
+    m &= (e >> bit) & 1 ? v : ~v;
+  }
+  return m;
+}
+__device__ __forceinline__ uint64_t lanes_below() {
+  return (uint64_t{1} << (threadIdx.x % kWave)) - 1;
+}
+__device__ __forceinline__ bool in_range(int e, int E) { return static_cast<uint32_t>(e) < static_cast<uint32_t>(E); }
+
+// Per chunk of 1024 entries, one thread each: an entry's rank within the chunk
+// among those of its expert (ascending t * k + j, also where a token names an
+// expert twice), parked in row_map, and the chunk's counts.  The waves' counts
+// per expert meet in LDS.
 __global__ void __launch_bounds__(kRankChunk)
 permute_count_kernel(int64_t n, int E, const int32_t* __restrict__ idx, int32_t* __restrict__ row_map,
                      int32_t* __restrict__ counts) {
   constexpr int W = kRankChunk / kWave;
-  extern __shared__ __attribute__((aligned(16))) uint32_t count_lds[];   // [W][E] 64-bit masks, then [W][E] prefixes
-  uint32_t* const mask = count_lds;
-  uint16_t* const prefix = reinterpret_cast<uint16_t*>(count_lds + 2 * W * E);
-  const int tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave;
-  for (int i = tid; i < 2 * W * E; i += kRankChunk) mask[i] = 0u;
+  extern __shared__ __attribute__((aligned(16))) uint16_t s_count[];   // [W][E]
+  const int tid = threadIdx.x;
   const int64_t i = static_cast<int64_t>(blockIdx.x) * kRankChunk + tid;
   const int e = i < n ? idx[i] : -1;
-  const bool live = static_cast<uint32_t>(e) < static_cast<uint32_t>(E);
+  const bool live = in_range(e, E);
+  for (int c = tid; c < W * E / 2; c += kRankChunk) reinterpret_cast<uint32_t*>(s_count)[c] = 0u;
   __syncthreads();
-  const int m = wave * E + e;
-  if (live) atomicOr(&mask[2 * m + lane / 32], 1u << (lane % 32));
+  const uint64_t same = same_lanes(e, live);
+  uint16_t* const mine = s_count + tid / kWave * E + e;
+  if (live && (same & lanes_below()) == 0) *mine = static_cast<uint16_t>(__popcll(same));
   __syncthreads();
   if (tid < E) {
     int run = 0;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
-      prefix[w * E + tid] = static_cast<uint16_t>(run);
-      run += __popc(mask[2 * (w * E + tid)]) + __popc(mask[2 * (w * E + tid) + 1]);
+      const int v = s_count[w * E + tid];
+      s_count[w * E + tid] = static_cast<uint16_t>(run);
+      run += v;
     }
     counts[static_cast<int64_t>(blockIdx.x) * E + tid] = run;
   }
   __syncthreads();
-  if (live) {
-    const uint32_t lo = mask[2 * m], hi = mask[2 * m + 1], below = (1u << (lane % 32)) - 1u;
-    row_map[i] = prefix[m] + (lane < 32 ? __popc(lo & below) : __popc(lo) + __popc(hi & below));
+  if (live) row_map[i] = *mine + __popcll(same & lanes_below());
+}
+inline uint32_t count_lds_bytes(int E) { return static_cast<uint32_t>(kRankChunk / kWave * E) * 2u; }
+
+// One workgroup of 1024 threads: thread (s, e) sums a segment of the chunks'
+// counts of expert e (the first kKeep stay in registers), the segments of an
+// expert are scanned in LDS, the chunks' running sums written over the counts,
+// and the experts' padded totals scanned by a thread each.  cols: E rounded up
+// to a power of two.
+constexpr int kScanThreads = 1024;
+__global__ void __launch_bounds__(kScanThreads)
+permute_scan_kernel(int32_t* __restrict__ counts, int n_chunks, int E, int cols, int align,
+                    int32_t* __restrict__ offsets, int32_t* __restrict__ expert_count) {
+  constexpr int kKeep = 16;
+  __shared__ int32_t s_sum[kScanThreads], s_wave[kScanThreads / kWave];
+  const int tid = threadIdx.x, e = tid & (cols - 1), seg = tid / cols, segs = kScanThreads / cols;
+  const int per = (n_chunks + segs - 1) / segs;
+  const int c0 = min(n_chunks, seg * per), c1 = e < E ? min(n_chunks, c0 + per) : c0;
+  int keep[kKeep];
+  int sum = 0;
+#pragma unroll
+  for (int i = 0; i < kKeep; ++i) {
+    keep[i] = c0 + i < c1 ? counts[static_cast<int64_t>(c0 + i) * E + e] : 0;
+    sum += keep[i];
+  }
+  for (int c = c0 + kKeep; c < c1; ++c) sum += counts[static_cast<int64_t>(c) * E + e];
+  int run = sum;
+  for (int d = cols; d < kScanThreads; d <<= 1) {
+    s_sum[tid] = run;
+    __syncthreads();
+    const int u = tid >= d ? s_sum[tid - d] : 0;
+    __syncthreads();
+    run += u;
+  }
+  s_sum[tid] = run;
+  run -= sum;
+#pragma unroll
+  for (int i = 0; i < kKeep; ++i) {
+    if (c0 + i < c1) counts[static_cast<int64_t>(c0 + i) * E + e] = run;
+    run += keep[i];
+  }
+  for (int c = c0 + kKeep; c < c1; ++c) {
+    const int64_t i = static_cast<int64_t>(c) * E + e;
+    const int v = counts[i];
+    counts[i] = run;
+    run += v;
+  }
+  __syncthreads();
+  const int total = tid < E ? s_sum[kScanThreads - cols + tid] : 0;
+  const int padded = (total + align - 1) / align * align;
+  int incl = padded;
+#pragma unroll
+  for (int d = 1; d < kWave; d <<= 1) {
+    const int u = __shfl_up(incl, d, kWave);
+    if (tid % kWave >= d) incl += u;
+  }
+  if (tid % kWave == kWave - 1) s_wave[tid / kWave] = incl;
+  __syncthreads();
+  for (int w = 0; w < tid / kWave; ++w) incl += s_wave[w];
+  if (tid < E) {
+    expert_count[tid] = total;
+    offsets[tid + 1] = incl;
+    if (tid == 0) offsets[0] = 0;
   }
 }
-inline int count_lds_bytes(int E) { return kRankChunk / kWave * E * 10; }
 
 struct PermuteArgs {
   int64_t T;
@@ -129,10 +210,11 @@ __device__ __forceinline__ u32x4_t load16(const u32x4_t* p, bool stream) {
 }
 
 // Zeros in the pad rows of an expert whose group's pad rows are [r0, r1).
+template <int THREADS>
 __device__ __forceinline__ void clear_pad_rows(const PermuteArgs& a, int r0, int r1) {
-  for (int r = r0 + static_cast<int>(threadIdx.x); r < r1; r += kThreads) a.src_row[r] = -1;
+  for (int r = r0 + static_cast<int>(threadIdx.x); r < r1; r += THREADS) a.src_row[r] = -1;
   if (a.xp == nullptr) return;
-  for (int r = r0 + static_cast<int>(threadIdx.x) / kWave; r < r1; r += kWaves) {
+  for (int r = r0 + static_cast<int>(threadIdx.x) / kWave; r < r1; r += THREADS / kWave) {
     u32x4_t* row = reinterpret_cast<u32x4_t*>(a.xp) + static_cast<int64_t>(r) * a.chunks;
     for (int c = threadIdx.x % kWave; c < a.chunks; c += kWave) row[c] = u32x4_t{0u, 0u, 0u, 0u};
   }
@@ -158,43 +240,33 @@ __device__ __forceinline__ void copy_token(const PermuteArgs& a, int64_t t, int 
   }
 }
 
-// Up to kRankChunk entries in one launch: a workgroup per token counts the
-// experts of all entries, and those of its own before each of its slots, and
-// scans the padded group sizes, all in LDS.
-__global__ void __launch_bounds__(kThreads)
+// Few entries in one launch: each workgroup counts all of them by expert in LDS,
+// those before its own G tokens apart, scans the padded group sizes, and copies
+// its tokens, 256 threads each.
+template <int THREADS, int G>
+__global__ void __launch_bounds__(THREADS)
 permute_few_kernel(PermuteArgs a) {
-  __shared__ int32_t s_count[kMaxE], s_off[kMaxE + 1], s_wave[kWaves], s_below[kWaves][kMaxK], s_row[kMaxK];
-  const int tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave;
+  constexpr int W = THREADS / kWave, kTeams = THREADS / kThreads;
+  static_assert(G * kMaxK <= kWave && G % kTeams == 0, "one wave ranks the workgroup's entries");
+  __shared__ int32_t s_before[kMaxE], s_after[kMaxE], s_off[kMaxE + 1], s_wave[W], s_row[G * kMaxK];
+  const int tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave, team = tid / kThreads, tl = tid % kThreads;
   const bool pads = blockIdx.x >= a.token_blocks;
-  const int64_t t = pads ? a.T : blockIdx.x;
-  const u32x4_t v = first_chunk(a, t, tid);
-  for (int e = tid; e < a.E; e += kThreads) s_count[e] = 0;
-  const int n = static_cast<int>(a.T) * a.k, own0 = static_cast<int>(t) * a.k;
-  int own[kMaxK], below[kMaxK];
-#pragma unroll
-  for (int j = 0; j < kMaxK; ++j) {
-    own[j] = !pads && j < a.k ? a.idx[own0 + j] : -1;
-    below[j] = 0;
-  }
+  const int64_t t0 = pads ? a.T : static_cast<int64_t>(blockIdx.x) * G;
+  const u32x4_t v = first_chunk(a, t0 + team, tl);
+  for (int e = tid; e < a.E; e += THREADS) s_before[e] = s_after[e] = 0;
+  const int n = static_cast<int>(a.T) * a.k, own0 = static_cast<int>(t0) * a.k;
   __syncthreads();
-  for (int i0 = 0; i0 < n; i0 += kThreads) {
-    const int i = i0 + tid;
-    const int e = i < n ? a.idx[i] : -1;
-    if (static_cast<uint32_t>(e) < static_cast<uint32_t>(a.E)) atomicAdd(&s_count[e], 1);
-#pragma unroll
-    for (int j = 0; j < kMaxK; ++j)
-      if (j < a.k) below[j] += __popcll(__ballot(i < own0 + j && e == own[j]));
-  }
-  if (lane == 0) {
-#pragma unroll
-    for (int j = 0; j < kMaxK; ++j) s_below[wave][j] = below[j];
+  for (int i = tid; i < n; i += THREADS) {
+    const int e = a.idx[i];
+    if (in_range(e, a.E)) atomicAdd(i < own0 ? &s_before[e] : &s_after[e], 1);
   }
   __syncthreads();
   // exclusive scan of the padded group sizes: a thread's consecutive experts,
   // the wave's lanes, the waves
-  const int per = (a.E + kThreads - 1) / kThreads, e0 = min(a.E, tid * per), e1 = min(a.E, e0 + per);
+  const int per = (a.E + THREADS - 1) / THREADS, e0 = min(a.E, tid * per), e1 = min(a.E, e0 + per);
+  auto padded = [&](int e) { return (s_before[e] + s_after[e] + a.align - 1) / a.align * a.align; };
   int mine = 0;
-  for (int e = e0; e < e1; ++e) mine += (s_count[e] + a.align - 1) / a.align * a.align;
+  for (int e = e0; e < e1; ++e) mine += padded(e);
   int incl = mine;
 #pragma unroll
   for (int d = 1; d < kWave; d <<= 1) {
@@ -207,31 +279,41 @@ permute_few_kernel(PermuteArgs a) {
   for (int w = 0; w < wave; ++w) run += s_wave[w];
   for (int e = e0; e < e1; ++e) {
     s_off[e] = run;
-    run += (s_count[e] + a.align - 1) / a.align * a.align;
+    run += padded(e);
   }
-  if (tid == kThreads - 1) s_off[a.E] = run;   // the last thread's sum is the total
+  if (tid == THREADS - 1) s_off[a.E] = run;   // the last thread's sum is the total
   __syncthreads();
   if (blockIdx.x == 0)
-    for (int e = tid; e <= a.E; e += kThreads) a.offsets[e] = s_off[e];
+    for (int e = tid; e <= a.E; e += THREADS) a.offsets[e] = s_off[e];
   if (pads) {
     const int e = static_cast<int>(blockIdx.x - a.token_blocks);
-    clear_pad_rows(a, s_off[e] + s_count[e], s_off[e + 1]);
+    clear_pad_rows<THREADS>(a, s_off[e] + s_before[e] + s_after[e], s_off[e + 1]);
     return;
   }
-  if (tid < a.k) {
-    const int e = a.idx[own0 + tid];
+  if (wave == 0) {
+    const int i = own0 + lane;
+    const bool own = lane < G * a.k && i < n;
+    const int e = own ? a.idx[i] : -1;
+    const bool live = in_range(e, a.E);
+    const uint64_t same = same_lanes(e, live);
     int row = -1;
-    if (static_cast<uint32_t>(e) < static_cast<uint32_t>(a.E)) {
-      row = s_off[e];
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) row += s_below[w][tid];
-      a.src_row[row] = static_cast<int32_t>(t);
+    if (live) {
+      row = s_off[e] + s_before[e] + __popcll(same & lanes_below());
+      a.src_row[row] = static_cast<int32_t>(t0) + lane / a.k;
     }
-    a.row_map[own0 + tid] = row;
-    s_row[tid] = row;
+    if (own) {
+      a.row_map[i] = row;
+      s_row[lane] = row;
+    }
   }
   __syncthreads();
-  if (a.xp != nullptr) copy_token<kThreads>(a, t, tid, v, s_row);
+  if (a.xp == nullptr) return;
+#pragma unroll
+  for (int g = 0; g < G / kTeams; ++g) {
+    const int own = g * kTeams + team;
+    const int64_t t = t0 + own;
+    if (t < a.T) copy_token<kThreads>(a, t, tl, g == 0 ? v : first_chunk(a, t, tl), s_row + own * a.k);
+  }
 }
 
 // After the counts and their scan: TEAM lanes per token.
@@ -244,7 +326,7 @@ permute_rows_kernel(PermuteArgs a) {
   const int64_t block = a.first + blockIdx.x;
   if (block >= a.token_blocks) {
     const int e = static_cast<int>(block - a.token_blocks);
-    clear_pad_rows(a, a.offsets[e] + a.expert_count[e], a.offsets[e + 1]);
+    clear_pad_rows<kThreads>(a, a.offsets[e] + a.expert_count[e], a.offsets[e + 1]);
     return;
   }
   const int64_t t0 = block * kTeams, t = t0 + tid / TEAM;
@@ -253,7 +335,7 @@ permute_rows_kernel(PermuteArgs a) {
   if (tid < kTeams * a.k && i < a.T * a.k) {
     const int e = a.idx[i];
     int row = -1;
-    if (static_cast<uint32_t>(e) < static_cast<uint32_t>(a.E)) {
+    if (in_range(e, a.E)) {
       row = a.offsets[e] + a.counts[i / kRankChunk * a.E + e] + a.row_map[i];
       a.src_row[row] = static_cast<int32_t>(t0 + tid / a.k);
     }
@@ -473,20 +555,28 @@ bool launch_permute(int64_t T, int row_bytes, int k, int E, int row_align, const
                 streams(static_cast<double>(T) * row_bytes)};
   const int pad_blocks = row_align > 1 ? E : 0;
   if (one_launch(T, k)) {
-    launch_kernel("permute_rows", permute_few_kernel, dim3(static_cast<unsigned>(T + pad_blocks)), dim3(kThreads), 0,
-                  s, a);
+    auto few = [&](auto threads, auto tokens) {
+      constexpr int THREADS = decltype(threads)::value, G = decltype(tokens)::value;
+      a.token_blocks = (T + G - 1) / G;
+      launch_kernel("permute_rows", permute_few_kernel<THREADS, G>,
+                    dim3(static_cast<unsigned>(a.token_blocks + pad_blocks)), dim3(THREADS), 0, s, a);
+    };
+    if (T <= kOneTokenAWorkgroup) few(std::integral_constant<int, kThreads>{}, std::integral_constant<int, 1>{});
+    else few(std::integral_constant<int, 1024>{}, std::integral_constant<int, 8>{});
     return launch_ok("permute_rows");
   }
-  static OncePerDevice lds;
-  if (!set_lds(lds, permute_count_kernel, count_lds_bytes(kMaxE))) return launch_ok("permute_count") && false;
   const int64_t chunks = rank_chunks(T, k);
   int32_t* counts = static_cast<int32_t*>(ws);
   a.counts = counts;
   a.expert_count = counts + chunks * E;
   launch_kernel("permute_count", permute_count_kernel, dim3(static_cast<unsigned>(chunks)), dim3(kRankChunk),
-                static_cast<uint32_t>(count_lds_bytes(E)), s, T * k, E, topk_idx, row_map, counts);
+                count_lds_bytes(E), s, T * k, E, topk_idx, row_map, counts);
   if (!launch_ok("permute_count")) return false;
-  if (!launch_route_scan(counts, static_cast<int>(chunks), E, row_align, offsets, counts + chunks * E, s)) return false;
+  int cols = 1;
+  while (cols < E) cols *= 2;
+  launch_kernel("permute_scan", permute_scan_kernel, dim3(1), dim3(kScanThreads), 0, s, counts,
+                static_cast<int>(chunks), E, cols, row_align, offsets, counts + chunks * E);
+  if (!launch_ok("permute_scan")) return false;
   auto rows = [&](auto team) {
     constexpr int TEAM = decltype(team)::value, kTeams = kThreads / TEAM;
     a.token_blocks = (T + kTeams - 1) / kTeams;

@@ -59,12 +59,6 @@ bool launch_check_routing(const int32_t* topk_idx, int64_t T, int k, int E, int3
 
 size_t route_workspace_bytes(int64_t T, int E);
 
-// counts [n_chunks, E]: per expert, the exclusive prefix over the chunks in
-// place; expert_count [E] their totals, offsets [E + 1] the groups padded to
-// row_align.  E <= 1024.
-bool launch_route_scan(int32_t* counts, int n_chunks, int E, int row_align, int32_t* offsets, int32_t* expert_count,
-                       hipStream_t s);
-
 // Scratch of the allocation-free quantize+permute: a file-scope device array
 // of kNoAllocScratchBytes per GPU; noalloc_scratch() returns the current
 // device's address of it (looked up once per device; nullptr on failure).

@@ -1025,13 +1025,6 @@ size_t route_workspace_bytes(int64_t T, int E) {
   return static_cast<size_t>(n_chunks * E + E) * sizeof(int32_t);
 }
 
-bool launch_route_scan(int32_t* counts, int n_chunks, int E, int row_align, int32_t* offsets, int32_t* expert_count,
-                       hipStream_t s) {
-  launch_kernel("route_scan", route_scan_kernel, dim3(1), dim3(kScanThreads), 0, s, counts, n_chunks, E, row_align,
-                offsets, expert_count);
-  return launch_ok("route_scan");
-}
-
 bool launch_quantize_permute(const uint16_t* x, int64_t T, int K, const int32_t* topk_idx,
                              int k, int E, int row_align, uint8_t* codes, uint8_t* scales,
                              float* outer, int32_t* offsets, int32_t* row_map, int32_t* src_row,

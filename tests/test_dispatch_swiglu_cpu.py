@@ -65,12 +65,12 @@ def _base(order, **sizes):
     (dict(x=None), INVALID, "x is NULL"), (dict(idx=None), INVALID, "topk_idx"), (dict(offsets=None), INVALID, "offsets"),
     (dict(row_map=None), INVALID, "row_map"), (dict(src_row=None), INVALID, "src_row"),
     (dict(x="x+2"), INVALID, "x is not 16"), (dict(xp="xp+8"), INVALID, "xp is not 16"),
-    (dict(idx="idx+2"), INVALID, "4-byte"), (dict(T=4096, ws=None, wsb=0), WORKSPACE, "workspace"),
-    (dict(T=4096, wsb=64), WORKSPACE, "workspace"), (dict(T=4096, ws="ws+4"), INVALID, "workspace"),
+    (dict(idx="idx+2"), INVALID, "4-byte"), (dict(T=1 << 20, ws=None, wsb=0), WORKSPACE, "workspace"),
+    (dict(T=1 << 20, wsb=64), WORKSPACE, "workspace"), (dict(T=1 << 20, ws="ws+4"), INVALID, "workspace"),
     (dict(xp="x"), INVALID, "share"), (dict(row_map="idx"), INVALID, "share"), (dict(src_row="row_map"), INVALID, "share"),
-    (dict(offsets="idx"), INVALID, "share"), (dict(T=4096, ws="idx"), INVALID, "share")])
+    (dict(offsets="idx"), INVALID, "share"), (dict(T=1 << 20, ws="idx"), INVALID, "share")])
 def test_permute(lib, at, change, status, says):
-    base = _base(PERMUTE, T=4, H=64, k=2, E=8, align=1, dtype=BF16, stride=64, wsb=1 << 20)
+    base = _base(PERMUTE, T=4, H=64, k=2, E=8, align=1, dtype=BF16, stride=64, wsb=1 << 24)
     assert _status(lib, at, "w4a4_permute_fwd", PERMUTE, base, change) == status
     assert says in lib.w4a4_last_error().decode()
 

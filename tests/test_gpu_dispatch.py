@@ -71,14 +71,18 @@ def _perm(off, row, src, cap, k):
             for n, v in (("offsets", off), ("row_map", row), ("src_row", pad))}
 
 
-# one token; fewer and more entries than one launch ranks (1024), its edges; one
-# expert, a thousand; every alignment; rows of one chunk, of the two teams, and
-# beyond a chunk a lane
+# one token; batches of one launch with a token or eight a workgroup (border at
+# 256 tokens) and of three (2048 tokens with 8 slots, 5792 with one), chunks of
+# 1024 entries and their borders; one expert, a thousand; every alignment; rows
+# of one chunk, of the two teams, and beyond a chunk a lane
 CASES = [(1, 8, 2048, 128, 1, "distinct"), (1, 1, 8, 1, 1, "any"), (128, 8, 64, 16, 1, "distinct"),
          (129, 8, 1032, 16, 16, "any"), (61, 8, 2048, 128, 128, "distinct"), (341, 3, 264, 7, 32, "partial"),
          (342, 3, 512, 7, 64, "partial"), (1024, 1, 72, 1024, 1, "any"), (1025, 1, 72, 1024, 16, "any"),
          (500, 5, 1024, 33, 1, "partial"), (40, 2, 4104, 5, 16, "none"), (700, 4, 256, 3, 16, "one"),
-         (3001, 8, 40, 128, 32, "partial"), (2, 6, 8200, 3, 1, "any")]
+         (3001, 8, 40, 128, 32, "partial"), (2, 6, 8200, 3, 1, "any"), (4096, 8, 16, 1000, 1, "any"),
+         (4099, 8, 16, 1024, 16, "partial"), (16400, 2, 8, 1, 128, "any"), (33001, 1, 24, 300, 1, "partial"),
+         (6500, 7, 520, 12, 64, "one"), (256, 4, 80, 11, 16, "any"), (257, 4, 80, 11, 16, "any"),
+         (2048, 8, 72, 500, 32, "partial"), (2049, 8, 72, 500, 32, "partial"), (5792, 1, 8, 5, 16, "any")]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -376,7 +380,7 @@ def test_refusals(b):
                  lambda: b.w4a4_permute_fwd(x, ids.cpu(), E), lambda: b.w4a4_permute_fwd(x, ids, 0),
                  lambda: b.w4a4_permute_fwd(x, ids, E, 3), lambda: b.w4a4_permute_fwd(x.t(), ids, E),
                  lambda: b.w4a4_permute_fwd(x, ids, E, out=dict(xp=x)), lambda: b.w4a4_permute_fwd(x[:, :60], ids, E),
-                 lambda: b.w4a4_permute_fwd(x.repeat(200, 1), ids.repeat(200, 1), E,
+                 lambda: b.w4a4_permute_fwd(x.repeat(8000, 1), ids.repeat(8000, 1), E,
                                             workspace=torch.empty(16, dtype=torch.uint8, device="cuda")),
                  lambda: b.w4a4_permute_bwd(perm["xp"].half(), perm), lambda: b.w4a4_permute_bwd(perm["xp"], perm, dx=x[:4]),
                  lambda: b.w4a4_unpermute_fwd(perm["xp"], perm, w.double()),
