@@ -355,7 +355,7 @@ clear_offsets_kernel(int32_t* offsets, int n) {
 struct GatherArgs {
   int64_t T;
   int chunks, k;
-  uint32_t rows;
+  uint32_t magic, rows;       // magic: 2^32 / chunks, rounded up
   const void* src;            // [rows, H]
   const int32_t* row_map;
   const float* w;             // null: 1
@@ -364,44 +364,44 @@ struct GatherArgs {
   int64_t first;
 };
 
-// TEAM lanes per token, lane l the chunks l, l + TEAM, ... of its row; a chunk's
-// k loads (at most K) are all in flight.
-template <typename T, int TEAM, int K, bool NT>
+// A lane per output chunk, in flat order over the tokens' rows: its k loads (at
+// most K) are all in flight, no lane is idle whatever the row length, and a wide
+// row is work for several workgroups.
+template <typename T, int K, bool NT>
 __global__ void __launch_bounds__(kThreads)
 gather_rows_kernel(GatherArgs a) {
-  constexpr int kTeams = kThreads / TEAM, N = Chunk<T>::N;
-  const int lane = threadIdx.x % TEAM;
-  const int64_t t = (a.first + blockIdx.x) * kTeams + threadIdx.x / TEAM;
+  constexpr int N = Chunk<T>::N;
+  const int64_t base = (a.first + blockIdx.x) * kThreads, t0 = base / a.chunks;
+  const uint32_t i = static_cast<uint32_t>(base - t0 * a.chunks) + threadIdx.x;   // below chunks + 256: magic divides exactly
+  const uint32_t q = a.chunks > 1 ? __umulhi(i, a.magic) : i;
+  const int64_t t = t0 + q;
+  const int c = static_cast<int>(i - q * a.chunks);
   if (t >= a.T) return;
+  const u32x4_t* src = static_cast<const u32x4_t*>(a.src) + c;
   int32_t row[K];
   float w[K];
+  Chunk<T> v[K];
 #pragma unroll
   for (int j = 0; j < K; ++j) {
     row[j] = j < a.k ? a.row_map[t * a.k + j] : -1;
     w[j] = a.w != nullptr && j < a.k ? a.w[t * a.k + j] : 1.0f;
   }
-  const u32x4_t* src = static_cast<const u32x4_t*>(a.src);
-  u32x4_t* out = reinterpret_cast<u32x4_t*>(static_cast<uint8_t*>(a.out) + t * a.out_pitch);
-  for (int c = lane; c < a.chunks; c += TEAM) {
-    Chunk<T> v[K];
 #pragma unroll
-    for (int j = 0; j < K; ++j)
-      if (static_cast<uint32_t>(row[j]) < a.rows)
-        v[j].w = load16<NT>(src + static_cast<int64_t>(row[j]) * a.chunks + c);
-    float acc[N];
+  for (int j = 0; j < K; ++j)
+    if (static_cast<uint32_t>(row[j]) < a.rows) v[j].w = load16<NT>(src + static_cast<int64_t>(row[j]) * a.chunks);
+  float acc[N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) acc[i] = 0.0f;
+  for (int i = 0; i < N; ++i) acc[i] = 0.0f;
 #pragma unroll
-    for (int j = 0; j < K; ++j) {
-      if (static_cast<uint32_t>(row[j]) < a.rows) {
+  for (int j = 0; j < K; ++j) {
+    if (static_cast<uint32_t>(row[j]) < a.rows) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) acc[i] = fmaf(w[j], v[j].get(i), acc[i]);
-      }
+      for (int i = 0; i < N; ++i) acc[i] = fmaf(w[j], v[j].get(i), acc[i]);
     }
-    Chunk<T> o;
-    o.put(acc);
-    __builtin_nontemporal_store(o.w, out + c);
   }
+  Chunk<T> o;
+  o.put(acc);
+  __builtin_nontemporal_store(o.w, reinterpret_cast<u32x4_t*>(static_cast<uint8_t*>(a.out) + t * a.out_pitch) + c);
 }
 
 // ------------------------------------------------- gradient of the unpermute
@@ -522,9 +522,6 @@ unpermute_bwd_scatter_kernel(UnpermuteBwdArgs a) {
   }
 }
 
-// Lanes per token: a wave for rows of up to 128 chunks (2 KB), else a workgroup.
-bool wave_per_token(int chunks) { return chunks <= 128; }
-
 // Whether loads of so many bytes go past the 256 MiB memory-side cache, which
 // cannot hold them all from their producer.
 bool streams(double bytes) { return bytes > 0.75 * 256 * 1024 * 1024; }
@@ -586,7 +583,9 @@ bool launch_permute(int64_t T, int row_bytes, int k, int E, int row_align, const
                     a);
     });
   };
-  if (wave_per_token(a.chunks)) rows(std::integral_constant<int, kWave>{});
+  // lanes per token
+  if (a.chunks <= 16) rows(std::integral_constant<int, 16>{});
+  else if (a.chunks <= 128) rows(std::integral_constant<int, kWave>{});
   else rows(std::integral_constant<int, kThreads>{});
   return launch_ok("permute_rows");
 }
@@ -594,24 +593,21 @@ bool launch_permute(int64_t T, int row_bytes, int k, int E, int row_align, const
 bool launch_gather_rows(int64_t T, int H, int k, int64_t rows, bool f32, const void* src, const int32_t* row_map,
                         const float* w, void* out, int64_t out_pitch, const char* name, hipStream_t s) {
   if (T == 0) return true;
-  GatherArgs a{T, H / (f32 ? 4 : 8), k, static_cast<uint32_t>(rows), src, row_map, w, out, out_pitch, 0};
+  GatherArgs a{T, H / (f32 ? 4 : 8), k, 0, static_cast<uint32_t>(rows), src, row_map, w, out, out_pitch, 0};
+  a.magic = static_cast<uint32_t>(((uint64_t{1} << 32) + a.chunks - 1) / a.chunks);
   const bool nt = streams(static_cast<double>(T) * k * H * (f32 ? 4 : 2));
-  auto go = [&](auto elem, auto team, auto slots) {
+  auto go = [&](auto elem, auto slots) {
     using Elem = decltype(elem);
-    constexpr int TEAM = decltype(team)::value, K = decltype(slots)::value, kTeams = kThreads / TEAM;
-    launch_parts((T + kTeams - 1) / kTeams, kThreads, [&](int64_t first, int64_t count) {
+    constexpr int K = decltype(slots)::value;
+    launch_parts((T * a.chunks + kThreads - 1) / kThreads, kThreads, [&](int64_t first, int64_t count) {
       a.first = first;
-      launch_kernel(name, nt ? gather_rows_kernel<Elem, TEAM, K, true> : gather_rows_kernel<Elem, TEAM, K, false>,
+      launch_kernel(name, nt ? gather_rows_kernel<Elem, K, true> : gather_rows_kernel<Elem, K, false>,
                     dim3(static_cast<unsigned>(count)), dim3(kThreads), 0, s, a);
     });
   };
   with_slots(k, [&](auto slots) {
-    auto shape = [&](auto elem) {
-      if (wave_per_token(a.chunks)) go(elem, std::integral_constant<int, kWave>{}, slots);
-      else go(elem, std::integral_constant<int, kThreads>{}, slots);
-    };
-    if (f32) shape(float{});
-    else shape(uint16_t{});
+    if (f32) go(float{}, slots);
+    else go(uint16_t{}, slots);
   });
   return launch_ok(name);
 }
