@@ -24,8 +24,6 @@ namespace w4a4 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 2;                       // 8-element chunks of gate and up per lane
-constexpr int kBlockChunks = kThreads * kUnroll;
 
 // 2^X of the scale byte X + 127 (255, E8M0's NaN: NaN).
 __device__ __forceinline__ float mx_scale(uint32_t byte) {
@@ -58,30 +56,22 @@ __device__ __forceinline__ u32x4_t pack8(const float (&v)[8]) {
   return w;
 }
 
-// The rows' chunks in flat order, kBlockChunks a workgroup: chunk u of this lane
-// is chunk col[u] of row[u] (I / 8 a row); row[u] = T where there is none.
-// I % 32 == 0 wherever blocks are encoded or read, so that a quad's lanes hold
-// one block of one row.
+// The rows' 8-element chunks in flat order, one a lane (I / 8 a row; two a lane
+// took 145 us against 142 for the forward below, four 152).  I % 32 == 0 wherever
+// blocks are encoded or read, so that a quad's lanes hold one block of one row.
 struct Place {
-  int64_t row[kUnroll];
-  int col[kUnroll];
+  int64_t row;
+  int col;
 };
 __device__ __forceinline__ bool place(const SwigluArgs& a, Place& p) {
   const int chunks = a.I / 8;
   const int64_t T = a.rows != nullptr ? min(a.T, static_cast<int64_t>(max(*a.rows, 0))) : a.T;
-  const int64_t base = (a.first + blockIdx.x) * kBlockChunks;
-  const int64_t row0 = base / chunks;
-  if (row0 >= T) return false;
-  const uint32_t col0 = static_cast<uint32_t>(base - row0 * chunks);
-#pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    const uint32_t i = col0 + u * kThreads + threadIdx.x;   // below chunks + kBlockChunks: magic divides exactly
-    const uint32_t q = chunks > 1 ? __umulhi(i, a.magic) : i;
-    const int64_t row = row0 + q;
-    p.row[u] = row < T ? row : a.T;
-    p.col[u] = static_cast<int>(i - q * chunks);
-  }
-  return true;
+  const int64_t base = (a.first + blockIdx.x) * kThreads, row0 = base / chunks;
+  const uint32_t i = static_cast<uint32_t>(base - row0 * chunks) + threadIdx.x;   // below chunks + 256: magic divides exactly
+  const uint32_t q = chunks > 1 ? __umulhi(i, a.magic) : i;
+  p.row = row0 + q;
+  p.col = static_cast<int>(i - q * chunks);
+  return p.row < T;
 }
 
 template <bool NT>
@@ -90,50 +80,49 @@ __device__ __forceinline__ u32x4_t load16(const void* p) {
   else return *static_cast<const u32x4_t*>(p);
 }
 
+// The MXFP8 of 8 elements of h to the checkpoint.
+__device__ __forceinline__ void keep8(const SwigluArgs& a, const u32x4_t& v, int64_t chunk) {
+  uint32_t code[2];
+  const uint32_t byte = mx_encode8<kMxFp8>(v, code);
+  const u32x2_t c{code[0], code[1]};
+  u32x2_t* to = reinterpret_cast<u32x2_t*>(a.h_codes) + chunk;
+  if (a.whole_lines) __builtin_nontemporal_store(c, to);
+  else *to = c;
+  if ((chunk & 3) == 0) a.h_scales[chunk >> 2] = static_cast<uint8_t>(byte);
+}
+
 template <int FMT, bool CKPT>
 __global__ void __launch_bounds__(kThreads)
 swiglu_fwd_kernel(SwigluArgs a) {
   Place p;
   if (!place(a, p)) return;
   const int chunks = a.I / 8;
-  u32x4_t g[kUnroll], v[kUnroll];
-#pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    g[u] = v[u] = u32x4_t{0u, 0u, 0u, 0u};
-    if (p.row[u] >= a.T) continue;
-    const uint16_t* h = a.h + p.row[u] * a.h_stride + p.col[u] * 8;
-    if (a.stream) {
-      g[u] = load16<true>(h);
-      v[u] = load16<true>(h + a.I);
-    } else {
-      g[u] = load16<false>(h);
-      v[u] = load16<false>(h + a.I);
-    }
+  const uint16_t* h = a.h + p.row * a.h_stride + p.col * 8;
+  u32x4_t g, v;
+  if (a.stream) {
+    g = load16<true>(h);
+    v = load16<true>(h + a.I);
+  } else {
+    g = load16<false>(h);
+    v = load16<false>(h + a.I);
   }
+  const int64_t at = p.row * chunks + p.col;
+  if constexpr (CKPT) {
+    const int64_t hat = p.row * 2 * chunks + p.col;
+    keep8(a, g, hat);
+    keep8(a, v, hat + chunks);
+  }
+  float gate[8], up[8], y[8];
+  unpack8(g, gate);
+  unpack8(v, up);
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    if (p.row[u] >= a.T) continue;
-    const int64_t at = p.row[u] * chunks + p.col[u];
-    if constexpr (CKPT) {
-      const int64_t hat = p.row[u] * 2 * chunks + p.col[u];
-      uint32_t code[2];
-      uint32_t byte = mx_encode8<kMxFp8>(g[u], code);
-      mx_store8<kMxFp8>(a.h_codes, a.h_scales, hat, code, byte);
-      byte = mx_encode8<kMxFp8>(v[u], code);
-      mx_store8<kMxFp8>(a.h_codes, a.h_scales, hat + chunks, code, byte);
-    }
-    float gate[8], up[8], y[8];
-    unpack8(g[u], gate);
-    unpack8(v[u], up);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = gate[i] * sigmoid_fast(gate[i]) * up[i];
-    const u32x4_t w = pack8(y);
-    if (a.a != nullptr) __builtin_nontemporal_store(w, reinterpret_cast<u32x4_t*>(a.a) + at);
-    if constexpr (FMT != kMxNone) {
-      uint32_t code[2];
-      const uint32_t byte = mx_encode8<FMT>(w, code);
-      mx_store8<FMT>(a.codes, a.scales, at, code, byte);
-    }
+  for (int i = 0; i < 8; ++i) y[i] = gate[i] * sigmoid_fast(gate[i]) * up[i];
+  const u32x4_t w = pack8(y);
+  if (a.a != nullptr) __builtin_nontemporal_store(w, reinterpret_cast<u32x4_t*>(a.a) + at);
+  if constexpr (FMT != kMxNone) {
+    uint32_t code[2];
+    const uint32_t byte = mx_encode8<FMT>(w, code);
+    mx_store8<FMT>(a.codes, a.scales, at, code, byte);
   }
 }
 
@@ -143,61 +132,54 @@ swiglu_bwd_kernel(SwigluArgs a) {
   Place p;
   if (!place(a, p)) return;
   const int chunks = a.I / 8;
-  u32x4_t d[kUnroll], g[kUnroll], v[kUnroll];
-  u32x2_t gc[kUnroll], vc[kUnroll];
-  uint32_t gs[kUnroll], vs[kUnroll];
+  const int64_t at = p.row * chunks + p.col, hat = p.row * 2 * chunks + p.col;
+  u32x4_t d{0u, 0u, 0u, 0u}, g, v;
+  u32x2_t gc, vc;
+  uint32_t gs, vs;
   auto load = [&](auto nt) {
     constexpr bool NT = decltype(nt)::value;
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      if (p.row[u] >= a.T) continue;
-      if (a.da != nullptr) d[u] = load16<NT>(a.da + (p.row[u] * chunks + p.col[u]) * 8);
-      if constexpr (CKPT) {
-        const int64_t hat = p.row[u] * 2 * chunks + p.col[u];
-        const u32x2_t* c = reinterpret_cast<const u32x2_t*>(a.h_codes) + hat;
-        gc[u] = NT ? __builtin_nontemporal_load(c) : *c;
-        vc[u] = NT ? __builtin_nontemporal_load(c + chunks) : c[chunks];
-        gs[u] = a.h_scales[hat >> 2];
-        vs[u] = a.h_scales[(hat + chunks) >> 2];
-      } else {
-        const uint16_t* h = a.h + p.row[u] * a.h_stride + p.col[u] * 8;
-        g[u] = load16<NT>(h);
-        v[u] = load16<NT>(h + a.I);
-      }
+    if (a.da != nullptr) d = load16<NT>(a.da + at * 8);
+    if constexpr (CKPT) {
+      const u32x2_t* c = reinterpret_cast<const u32x2_t*>(a.h_codes) + hat;
+      gc = NT ? __builtin_nontemporal_load(c) : *c;
+      vc = NT ? __builtin_nontemporal_load(c + chunks) : c[chunks];
+      gs = a.h_scales[hat >> 2];
+      vs = a.h_scales[(hat + chunks) >> 2];
+    } else {
+      const uint16_t* h = a.h + p.row * a.h_stride + p.col * 8;
+      g = load16<NT>(h);
+      v = load16<NT>(h + a.I);
     }
   };
   if (a.stream) load(std::true_type{});
   else load(std::false_type{});
+  float gate[8], up[8], s[8];
+  if constexpr (CKPT) {
+    mx_decode8(gc, gs, gate);
+    mx_decode8(vc, vs, up);
+  } else {
+    unpack8(g, gate);
+    unpack8(v, up);
+  }
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    if (p.row[u] >= a.T) continue;
-    float gate[8], up[8], s[8], y[8];
-    if constexpr (CKPT) {
-      mx_decode8(gc[u], gs[u], gate);
-      mx_decode8(vc[u], vs[u], up);
-    } else {
-      unpack8(g[u], gate);
-      unpack8(v[u], up);
+  for (int i = 0; i < 8; ++i) s[i] = sigmoid_fast(gate[i]);
+  if (a.a != nullptr) {
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = gate[i] * s[i] * up[i];
+    __builtin_nontemporal_store(pack8(y), reinterpret_cast<u32x4_t*>(a.a) + at);
+  }
+  if (a.dh != nullptr) {
+    float da[8], dg[8], du[8];
+    unpack8(d, da);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      dg[i] = da[i] * up[i] * s[i] * (1.0f + gate[i] * (1.0f - s[i]));
+      du[i] = da[i] * gate[i] * s[i];
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s[i] = sigmoid_fast(gate[i]);
-    if (a.a != nullptr) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = gate[i] * s[i] * up[i];
-      __builtin_nontemporal_store(pack8(y), reinterpret_cast<u32x4_t*>(a.a) + p.row[u] * chunks + p.col[u]);
-    }
-    if (a.dh != nullptr) {
-      float da[8], dg[8], du[8];
-      unpack8(d[u], da);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        dg[i] = da[i] * up[i] * s[i] * (1.0f + gate[i] * (1.0f - s[i]));
-        du[i] = da[i] * gate[i] * s[i];
-      }
-      u32x4_t* dh = reinterpret_cast<u32x4_t*>(a.dh) + p.row[u] * 2 * chunks + p.col[u];
-      __builtin_nontemporal_store(pack8(dg), dh);
-      __builtin_nontemporal_store(pack8(du), dh + chunks);
-    }
+    u32x4_t* dh = reinterpret_cast<u32x4_t*>(a.dh) + hat;
+    __builtin_nontemporal_store(pack8(dg), dh);
+    __builtin_nontemporal_store(pack8(du), dh + chunks);
   }
 }
 
@@ -210,7 +192,7 @@ bool launch_chunks(SwigluArgs a, const char* name, hipStream_t s, F kernel) {
   const int chunks = a.I / 8;
   a.magic = static_cast<uint32_t>(((uint64_t{1} << 32) + chunks - 1) / chunks);
   const int64_t total = a.T * chunks;
-  launch_parts((total + kBlockChunks - 1) / kBlockChunks, kThreads, [&](int64_t first, int64_t count) {
+  launch_parts((total + kThreads - 1) / kThreads, kThreads, [&](int64_t first, int64_t count) {
     a.first = first;
     launch_kernel(name, kernel, dim3(static_cast<unsigned>(count)), dim3(kThreads), 0, s, a);
   });
@@ -223,6 +205,11 @@ bool launch_swiglu_fwd(const SwigluArgs& args, int format, hipStream_t s) {
   if (args.T == 0) return true;
   SwigluArgs a = args;
   const bool ckpt = a.h_codes != nullptr;
+  // The checkpoint is read again much later: its codes are stored past the caches
+  // where both halves of a row are whole cache lines (131072 rows of 768: 137 us
+  // against 142; with I = 96, whose lines are written in two parts, 18.5 against
+  // 17.1).
+  a.whole_lines = a.I % 128 == 0;
   a.stream = streams(static_cast<double>(a.T) * a.I * (4 + (a.a ? 2 : 0) + (ckpt ? 2 : 0) + (a.codes ? 1 : 0)));
   auto go = [&](auto keep) {
     constexpr bool CKPT = decltype(keep)::value;
