@@ -282,8 +282,6 @@ struct SwigluArgs {
   uint8_t *codes, *scales;       // MX of a
   int64_t first;                 // set by the launch: its first workgroup
   uint32_t magic;                // likewise: 2^32 / chunks of a row, rounded up
-  bool stream;                   // likewise: non-temporal loads
-  bool whole_lines;              // likewise: non-temporal stores of the checkpoint
 };
 bool launch_swiglu_fwd(const SwigluArgs& a, int format, hipStream_t s);
 bool launch_swiglu_bwd(const SwigluArgs& a, hipStream_t s);

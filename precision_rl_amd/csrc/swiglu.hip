@@ -15,6 +15,7 @@
 // few.
 
 #include <algorithm>
+#include <type_traits>
 
 #include "internal.h"
 #include "launch_parts.h"
@@ -80,37 +81,38 @@ __device__ __forceinline__ u32x4_t load16(const void* p) {
   else return *static_cast<const u32x4_t*>(p);
 }
 
+// What becomes of h in the forward: nothing, or its checkpoint, stored past the
+// caches where both halves of a row of codes are whole cache lines.
+enum Keep { kDrop, kKeep, kKeepLines };
+
 // The MXFP8 of 8 elements of h to the checkpoint.
+template <Keep KEEP>
 __device__ __forceinline__ void keep8(const SwigluArgs& a, const u32x4_t& v, int64_t chunk) {
   uint32_t code[2];
   const uint32_t byte = mx_encode8<kMxFp8>(v, code);
   const u32x2_t c{code[0], code[1]};
   u32x2_t* to = reinterpret_cast<u32x2_t*>(a.h_codes) + chunk;
-  if (a.whole_lines) __builtin_nontemporal_store(c, to);
+  if constexpr (KEEP == kKeepLines) __builtin_nontemporal_store(c, to);
   else *to = c;
   if ((chunk & 3) == 0) a.h_scales[chunk >> 2] = static_cast<uint8_t>(byte);
 }
 
-template <int FMT, bool CKPT>
+// NT: loads past the caches.  It and the outputs of the backward pass are chosen
+// outside the kernels: branches around single loads and stores took 142 us where
+// this takes 133 (131072 rows of 768 with the checkpoint), 168 for 160 backward.
+template <int FMT, Keep KEEP, bool NT>
 __global__ void __launch_bounds__(kThreads)
 swiglu_fwd_kernel(SwigluArgs a) {
   Place p;
   if (!place(a, p)) return;
   const int chunks = a.I / 8;
   const uint16_t* h = a.h + p.row * a.h_stride + p.col * 8;
-  u32x4_t g, v;
-  if (a.stream) {
-    g = load16<true>(h);
-    v = load16<true>(h + a.I);
-  } else {
-    g = load16<false>(h);
-    v = load16<false>(h + a.I);
-  }
+  const u32x4_t g = load16<NT>(h), v = load16<NT>(h + a.I);
   const int64_t at = p.row * chunks + p.col;
-  if constexpr (CKPT) {
+  if constexpr (KEEP != kDrop) {
     const int64_t hat = p.row * 2 * chunks + p.col;
-    keep8(a, g, hat);
-    keep8(a, v, hat + chunks);
+    keep8<KEEP>(a, g, hat);
+    keep8<KEEP>(a, v, hat + chunks);
   }
   float gate[8], up[8], y[8];
   unpack8(g, gate);
@@ -126,50 +128,38 @@ swiglu_fwd_kernel(SwigluArgs a) {
   }
 }
 
-template <bool CKPT>
+// DH, A: which outputs are wanted.
+template <bool CKPT, bool DH, bool A, bool NT>
 __global__ void __launch_bounds__(kThreads)
 swiglu_bwd_kernel(SwigluArgs a) {
   Place p;
   if (!place(a, p)) return;
   const int chunks = a.I / 8;
   const int64_t at = p.row * chunks + p.col, hat = p.row * 2 * chunks + p.col;
-  u32x4_t d{0u, 0u, 0u, 0u}, g, v;
-  u32x2_t gc, vc;
-  uint32_t gs, vs;
-  auto load = [&](auto nt) {
-    constexpr bool NT = decltype(nt)::value;
-    if (a.da != nullptr) d = load16<NT>(a.da + at * 8);
-    if constexpr (CKPT) {
-      const u32x2_t* c = reinterpret_cast<const u32x2_t*>(a.h_codes) + hat;
-      gc = NT ? __builtin_nontemporal_load(c) : *c;
-      vc = NT ? __builtin_nontemporal_load(c + chunks) : c[chunks];
-      gs = a.h_scales[hat >> 2];
-      vs = a.h_scales[(hat + chunks) >> 2];
-    } else {
-      const uint16_t* h = a.h + p.row * a.h_stride + p.col * 8;
-      g = load16<NT>(h);
-      v = load16<NT>(h + a.I);
-    }
-  };
-  if (a.stream) load(std::true_type{});
-  else load(std::false_type{});
+  u32x4_t d;
+  if constexpr (DH) d = load16<NT>(a.da + at * 8);
   float gate[8], up[8], s[8];
   if constexpr (CKPT) {
-    mx_decode8(gc, gs, gate);
-    mx_decode8(vc, vs, up);
+    const u32x2_t* c = reinterpret_cast<const u32x2_t*>(a.h_codes) + hat;
+    const u32x2_t g = NT ? __builtin_nontemporal_load(c) : *c, v = NT ? __builtin_nontemporal_load(c + chunks) : c[chunks];
+    const uint32_t gs = a.h_scales[hat >> 2], vs = a.h_scales[(hat + chunks) >> 2];
+    mx_decode8(g, gs, gate);
+    mx_decode8(v, vs, up);
   } else {
+    const uint16_t* h = a.h + p.row * a.h_stride + p.col * 8;
+    const u32x4_t g = load16<NT>(h), v = load16<NT>(h + a.I);
     unpack8(g, gate);
     unpack8(v, up);
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) s[i] = sigmoid_fast(gate[i]);
-  if (a.a != nullptr) {
+  if constexpr (A) {
     float y[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i] = gate[i] * s[i] * up[i];
     __builtin_nontemporal_store(pack8(y), reinterpret_cast<u32x4_t*>(a.a) + at);
   }
-  if (a.dh != nullptr) {
+  if constexpr (DH) {
     float da[8], dg[8], du[8];
     unpack8(d, da);
 #pragma unroll
@@ -201,32 +191,45 @@ bool launch_chunks(SwigluArgs a, const char* name, hipStream_t s, F kernel) {
 
 }  // namespace
 
-bool launch_swiglu_fwd(const SwigluArgs& args, int format, hipStream_t s) {
-  if (args.T == 0) return true;
-  SwigluArgs a = args;
-  const bool ckpt = a.h_codes != nullptr;
-  // The checkpoint is read again much later: its codes are stored past the caches
-  // where both halves of a row are whole cache lines (131072 rows of 768: 137 us
-  // against 142; with I = 96, whose lines are written in two parts, 18.5 against
-  // 17.1).
-  a.whole_lines = a.I % 128 == 0;
-  a.stream = streams(static_cast<double>(a.T) * a.I * (4 + (a.a ? 2 : 0) + (ckpt ? 2 : 0) + (a.codes ? 1 : 0)));
-  auto go = [&](auto keep) {
-    constexpr bool CKPT = decltype(keep)::value;
-    if (format == kMxFp8) return launch_chunks(a, "swiglu_fwd", s, swiglu_fwd_kernel<kMxFp8, CKPT>);
-    if (format == kMxFp4) return launch_chunks(a, "swiglu_fwd", s, swiglu_fwd_kernel<kMxFp4, CKPT>);
-    return launch_chunks(a, "swiglu_fwd", s, swiglu_fwd_kernel<kMxNone, CKPT>);
+bool launch_swiglu_fwd(const SwigluArgs& a, int format, hipStream_t s) {
+  if (a.T == 0) return true;
+  // The checkpoint is read again much later.  With lines that are written in two
+  // parts (I = 96) stores past the caches took 18.5 us against 17.1, with whole
+  // ones 137 against 142.
+  const Keep keep = a.h_codes == nullptr ? kDrop : a.I % 128 == 0 ? kKeepLines : kKeep;
+  const bool nt = streams(static_cast<double>(a.T) * a.I *
+                          (4 + (a.a ? 2 : 0) + (keep != kDrop ? 2 : 0) + (a.codes ? 1 : 0)));
+  auto go = [&](auto fmt, auto kept) {
+    constexpr int FMT = decltype(fmt)::value;
+    constexpr Keep KEEP = decltype(kept)::value;
+    return nt ? launch_chunks(a, "swiglu_fwd", s, swiglu_fwd_kernel<FMT, KEEP, true>)
+              : launch_chunks(a, "swiglu_fwd", s, swiglu_fwd_kernel<FMT, KEEP, false>);
   };
-  return ckpt ? go(std::true_type{}) : go(std::false_type{});
+  auto with_format = [&](auto kept) {
+    if (format == kMxFp8) return go(std::integral_constant<int, kMxFp8>{}, kept);
+    if (format == kMxFp4) return go(std::integral_constant<int, kMxFp4>{}, kept);
+    return go(std::integral_constant<int, kMxNone>{}, kept);
+  };
+  if (keep == kKeepLines) return with_format(std::integral_constant<Keep, kKeepLines>{});
+  if (keep == kKeep) return with_format(std::integral_constant<Keep, kKeep>{});
+  return with_format(std::integral_constant<Keep, kDrop>{});
 }
 
-bool launch_swiglu_bwd(const SwigluArgs& args, hipStream_t s) {
-  if (args.T == 0) return true;
-  SwigluArgs a = args;
+bool launch_swiglu_bwd(const SwigluArgs& a, hipStream_t s) {
+  if (a.T == 0) return true;
   const bool ckpt = a.h_codes != nullptr;
-  a.stream = streams(static_cast<double>(a.T) * a.I * ((ckpt ? 2 : 4) + (a.a ? 2 : 0) + (a.dh ? 6 : 0)));
-  return ckpt ? launch_chunks(a, "swiglu_bwd", s, swiglu_bwd_kernel<true>)
-              : launch_chunks(a, "swiglu_bwd", s, swiglu_bwd_kernel<false>);
+  const bool nt = streams(static_cast<double>(a.T) * a.I * ((ckpt ? 2 : 4) + (a.a ? 2 : 0) + (a.dh ? 6 : 0)));
+  auto go = [&](auto kept, auto dh, auto out) {
+    constexpr bool CKPT = decltype(kept)::value, DH = decltype(dh)::value, A = decltype(out)::value;
+    return nt ? launch_chunks(a, "swiglu_bwd", s, swiglu_bwd_kernel<CKPT, DH, A, true>)
+              : launch_chunks(a, "swiglu_bwd", s, swiglu_bwd_kernel<CKPT, DH, A, false>);
+  };
+  auto outputs = [&](auto kept) {
+    if (a.a == nullptr) return go(kept, std::true_type{}, std::false_type{});
+    if (a.dh == nullptr) return go(kept, std::false_type{}, std::true_type{});
+    return go(kept, std::true_type{}, std::true_type{});
+  };
+  return ckpt ? outputs(std::true_type{}) : outputs(std::false_type{});
 }
 
 }  // namespace w4a4
