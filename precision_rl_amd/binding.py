@@ -5,6 +5,7 @@ kernels.  PyTorch provides device memory and the current stream.  Loading
 fails loudly when the library has not been built.
 """
 import ctypes
+import functools
 import json
 import os
 
@@ -608,8 +609,14 @@ def w4a4_mx_linear_fwd(xq, wq, T, K, N, y=None):
 def _row(t):
     """(T, k) of a routing tensor."""
     if not isinstance(t, torch.Tensor) or t.dim() != 2 or not t.is_cuda:
-        raise W4A4Error("topk_idx, topk_w and row_map must be 2-d tensors on the GPU")
+        raise W4A4Error("topk_idx and row_map must be 2-d tensors on the GPU")
     return t.shape
+
+
+@functools.lru_cache(maxsize=1024)
+def _permute_workspace(T, k, E):
+    """Its bytes (a call into the library takes as long as all checks of two tensors)."""
+    return workspace_size(WS_PERMUTE, T, 0, 0, E, k)
 
 
 def w4a4_permute_fwd(x, topk_idx, E, row_align=1, out=None, workspace=None):
@@ -623,30 +630,33 @@ def w4a4_permute_fwd(x, topk_idx, E, row_align=1, out=None, workspace=None):
     given.  workspace: at least workspace_size(WS_PERMUTE, T, 0, 0, E, k) bytes (uint8), allocated where it is not
     given."""
     T, k = _row(topk_idx)
-    dev = topk_idx.device
+    dev, i32 = topk_idx.device, torch.int32
     res = {} if out is None else dict(out)
     cap = max(0, T * k + E * (row_align - 1))
-    H, dtype, pitch, xptr, xp = 8, 0, 8, None, None
+    H, dtype, pitch, xptr, xpptr = 8, 0, 8, None, None
     if x is not None:
-        (_, H), _ = _matrix(x, "x")
+        H = _matrix(x, "x")[0][1]
         dtype, pitch = _dtype(x, "x"), _pitch(x)
         xptr = _ptr(x, "x", (T, H), x.dtype, dev, rows=True)
         xp = res.get("xp")
         if xp is None:
             xp = res["xp"] = torch.empty(cap, H, dtype=x.dtype, device=dev)
-        xp = _ptr(xp, "xp", (cap, H), x.dtype, dev)
-    for name, shape in (("offsets", (E + 1,)), ("row_map", (T, k)), ("src_row", (cap,))):
-        if res.get(name) is None:
-            res[name] = torch.empty(shape, dtype=torch.int32, device=dev)
-    nbytes = load().w4a4_workspace_size(WS_PERMUTE, T, 0, 0, E, k, 1)
+        xpptr = _ptr(xp, "xp", (cap, H), x.dtype, dev)
+    offsets, row_map, src_row = res.get("offsets"), res.get("row_map"), res.get("src_row")
+    if offsets is None:
+        offsets = res["offsets"] = torch.empty(max(0, E) + 1, dtype=i32, device=dev)
+    if row_map is None:
+        row_map = res["row_map"] = torch.empty(T, k, dtype=i32, device=dev)
+    if src_row is None:
+        src_row = res["src_row"] = torch.empty(cap, dtype=i32, device=dev)
+    nbytes = _permute_workspace(T, k, E)
     if workspace is not None:
         _check_workspace(workspace, nbytes, dev.index)
     elif nbytes:
         workspace = _workspace(nbytes, dev)
-    i32 = torch.int32
     _call(_lib.w4a4_permute_fwd, dev, T, H, k, E, row_align, dtype, xptr, pitch,
-          _ptr(topk_idx, "topk_idx", (T, k), i32, dev), xp, _ptr(res["offsets"], "offsets", (E + 1,), i32, dev),
-          _ptr(res["row_map"], "row_map", (T, k), i32, dev), _ptr(res["src_row"], "src_row", (cap,), i32, dev),
+          _ptr(topk_idx, "topk_idx", (T, k), i32, dev), xpptr, _ptr(offsets, "offsets", (E + 1,), i32, dev),
+          _ptr(row_map, "row_map", (T, k), i32, dev), _ptr(src_row, "src_row", (cap,), i32, dev),
           workspace.data_ptr() if nbytes else None, workspace.numel() if nbytes else 0)
     return res
 
