@@ -86,7 +86,8 @@ typedef enum {
   W4A4_WS_QUANTIZE_PERMUTE_DOMAIN = 4,  /* w4a4_quantize_permute_domain, any group_rows; H = K */
   W4A4_WS_MX8_BACKWARD = 5,             /* w4a4_mx8_expert_bwd */
   W4A4_WS_RMSNORM_BACKWARD = 6,         /* w4a4_add_rmsnorm_bwd with dgamma; I, E, k, row_align unused */
-  W4A4_WS_PERMUTE = 8                   /* w4a4_permute_fwd: T, E and k; the others unused (0 bytes for few tokens) */
+  W4A4_WS_PERMUTE = 8,                  /* w4a4_permute_fwd: T, E and k; the others unused (0 bytes for few tokens) */
+  W4A4_WS_BACKWARD_CKPT = 9             /* w4a4_expert_bwd_ckpt */
 } w4a4_workspace_kind;
 
 /* Element formats of the MX calls with a format argument. */
@@ -289,6 +290,29 @@ w4a4_status w4a4_expert_bwd(
     const void* dy, const void* x,
     const void* w1, const void* w2,
     const void* save_h, const void* save_a, const float* topk_w,
+    const int32_t* expert_offsets, const int32_t* row_map, const int32_t* src_row,
+    void* dx, void* dw1, void* dw2,
+    void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * w4a4_expert_bwd_ckpt -- w4a4_expert_bwd from h in MXFP8 in place of the bf16
+ * save_h and save_a, so that a layer keeps 33/16 I bytes a dispatched row
+ * instead of 6 I between its forward and its backward (207 MB instead of 604 at
+ * 131072 rows, I = 768).  The checkpoint's values stand for h throughout: the
+ * FC2 dgrad's epilogue decodes them for the SwiGLU backward and makes a =
+ * bf16(SwiGLU(h)) once more for dW2.  The results are those of w4a4_expert_bwd
+ * on the decoded h and that a.
+ *   h_codes [cap, 2I], h_scales [cap, 2I/32]: w4a4_swiglu_fwd's checkpoint of
+ *              the forward's save_h (rows = expert_offsets + E), or
+ *              w4a4_mx_quantize_rows of it, W4A4_MX_FP8.
+ *   The other arguments and the requirements are w4a4_expert_bwd's; workspace:
+ *   W4A4_WS_BACKWARD_CKPT (a beside the other's).
+ */
+w4a4_status w4a4_expert_bwd_ckpt(
+    int64_t T, int H, int I, int E, int k, int row_align,
+    const void* dy, const void* x,
+    const void* w1, const void* w2,
+    const uint8_t* h_codes, const uint8_t* h_scales, const float* topk_w,
     const int32_t* expert_offsets, const int32_t* row_map, const int32_t* src_row,
     void* dx, void* dw1, void* dw2,
     void* workspace, size_t workspace_bytes, void* stream);

@@ -30,6 +30,9 @@ _SIGS = {
     "w4a4_expert_bwd": (c_int, [c_i64, c_int, c_int, c_int, c_int, c_int,
                                 c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp,
                                 c_vp, c_vp, c_vp, c_vp, c_sz, c_vp]),
+    "w4a4_expert_bwd_ckpt": (c_int, [c_i64, c_int, c_int, c_int, c_int, c_int,
+                                     c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp,
+                                     c_vp, c_vp, c_vp, c_vp, c_sz, c_vp]),
     "w4a4_quantize_permute_domain": (c_int, [c_vp, c_i64, c_int, c_vp, c_int, c_int, c_int, c_i64,
                                              c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_sz, c_vp]),
     "w4a4_linear_fwd": (c_int, [c_i64, c_int, c_int, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp,
@@ -75,6 +78,7 @@ WS_QUANTIZE_PERMUTE_DOMAIN = 4
 WS_MX8_BACKWARD = 5
 WS_RMSNORM_BACKWARD = 6
 WS_PERMUTE = 8
+WS_BACKWARD_CKPT = 9
 
 # Element formats of the MX calls (w4a4_mx_format) and types (w4a4_dtype)
 MX_NONE, MX_FP4, MX_FP8 = -1, 0, 1
@@ -776,6 +780,33 @@ def w4a4_swiglu_bwd(da, kept, a=False, dh=True, rows=None, out=None):
           hc, hs, _ptr(rows, "rows", (1,), torch.int32, dev),
           _ptr(res["dh"], "dh", (T, W), torch.bfloat16, dev) if dh else None,
           _ptr(res["a"], "a", (T, I), torch.bfloat16, dev) if a else None)
+    return res
+
+
+def w4a4_expert_bwd_ckpt(dy, x, w1, w2, kept, topk_w, xq, T, H, I, E, k, row_align=1, out=None, workspace=None):  # noqa: E741
+    """``w4a4_expert_bwd`` from an MXFP8 checkpoint of h in place of the bf16 h and a: kept is a dict with h_codes
+    [cap, 2I] and h_scales [cap, 2I/32] uint8, as ``w4a4_swiglu_fwd(h, a=False, checkpoint=True,
+    rows=xq["offsets"][E:])`` makes it of the forward's h.  Returns dict(dx [T, H], dw1 [E, 2I, H], dw2 [E, H, I])
+    bf16.  workspace: at least workspace_size(WS_BACKWARD_CKPT, T, H, I, E, k, row_align) bytes (uint8)."""
+    dev, bf16, i32 = w1.device, torch.bfloat16, torch.int32
+    cap = rows_capacity(T, k, E, row_align)
+    res = {} if out is None else dict(out)
+    for name, shape in (("dx", (T, H)), ("dw1", (E, 2 * I, H)), ("dw2", (E, H, I))):
+        if res.get(name) is None:
+            res[name] = torch.empty(shape, dtype=bf16, device=dev)
+    nbytes = workspace_size(WS_BACKWARD_CKPT, T, H, I, E, k, row_align)
+    if workspace is not None:
+        _check_workspace(workspace, nbytes, dev.index)
+    else:
+        workspace = _workspace(nbytes, dev)
+    codes, scales = _checkpoint(kept, cap, 2 * I, dev)
+    _call(load().w4a4_expert_bwd_ckpt, dev, T, H, I, E, k, row_align, _ptr(dy, "dy", (T, H), bf16, dev),
+          _ptr(x, "x", (T, H), bf16, dev), _ptr(w1, "w1", (E, 2 * I, H), bf16, dev),
+          _ptr(w2, "w2", (E, H, I), bf16, dev), codes, scales, _ptr(topk_w, "topk_w", (T, k), torch.float32, dev),
+          _ptr(xq["offsets"], "offsets", (E + 1,), i32, dev), _ptr(xq["row_map"], "row_map", (T, k), i32, dev),
+          _ptr(xq["src_row"], "src_row", (cap,), i32, dev), _ptr(res["dx"], "dx", (T, H), bf16, dev),
+          _ptr(res["dw1"], "dw1", (E, 2 * I, H), bf16, dev), _ptr(res["dw2"], "dw2", (E, H, I), bf16, dev),
+          workspace.data_ptr(), workspace.numel())
     return res
 
 

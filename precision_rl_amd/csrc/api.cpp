@@ -129,9 +129,9 @@ FwdWs fwd_ws(int64_t cap, int H, int I) {
   return w;
 }
 struct BwdWs {
-  size_t sched, dO, dH, dXp, xp, total;
+  size_t sched, dO, dH, dXp, xp, a, total;   // a: from a checkpoint alone
 };
-BwdWs bwd_ws(int64_t cap, int H, int I, int E) {
+BwdWs bwd_ws(int64_t cap, int H, int I, int E, bool ckpt = false) {
   BwdWs w;
   size_t off = 0;
   w.sched = off; off += round_up(wgrad_schedule_ints(H, I, E) * 4);
@@ -139,6 +139,7 @@ BwdWs bwd_ws(int64_t cap, int H, int I, int E) {
   w.dH = off; off += round_up(static_cast<size_t>(cap) * 2 * I * 2);
   w.dXp = off; off += round_up(static_cast<size_t>(cap) * H * 2);
   w.xp = off; off += round_up(static_cast<size_t>(cap) * H * 2);
+  w.a = off; off += ckpt ? round_up(static_cast<size_t>(cap) * I * 2) : 0;
   w.total = off;
   return w;
 }
@@ -273,6 +274,9 @@ size_t w4a4_workspace_size(int kind, int64_t T, int H, int I, int E, int k, int 
     case W4A4_WS_BACKWARD:
       if (I <= 0) return 0;
       return bwd_ws(cap, H, I, E).total;
+    case W4A4_WS_BACKWARD_CKPT:
+      if (I <= 0) return 0;
+      return bwd_ws(cap, H, I, E, true).total;
     case W4A4_WS_MX8_BACKWARD:
       if (I <= 0) return 0;
       return mx8_ws(cap, H, I, E).total;
@@ -452,26 +456,18 @@ w4a4_status w4a4_grouped_expert_fwd(
   return W4A4_OK;
 }
 
-w4a4_status w4a4_expert_bwd(int64_t T, int H, int I, int E, int k, int row_align, const void* dy,
-                            const void* x, const void* w1, const void* w2, const void* save_h,
-                            const void* save_a, const float* topk_w,
-                            const int32_t* expert_offsets, const int32_t* row_map,
-                            const int32_t* src_row, void* dx, void* dw1, void* dw2,
-                            void* workspace, size_t workspace_bytes, void* stream) {
-  g_last_error.clear();
-  w4a4_status st = check_moe_shape(T, H, I, E, k, row_align);
-  if (st != W4A4_OK) return st;
-  REQUIRE_PTR(expert_offsets);
-  REQUIRE_PTR(w1); REQUIRE_PTR(w2); REQUIRE_PTR(dw1); REQUIRE_PTR(dw2);
-  if (T > 0) {
-    REQUIRE_PTR(dy); REQUIRE_PTR(x); REQUIRE_PTR(save_h); REQUIRE_PTR(save_a);
-    REQUIRE_PTR(topk_w); REQUIRE_PTR(row_map); REQUIRE_PTR(src_row); REQUIRE_PTR(dx);
-  }
+namespace {
+// The straight-through backward from the saved bf16 h and a, or (h_codes not
+// null) from h in MXFP8.
+struct SavedH {
+  const void *h, *a;
+  const uint8_t *h_codes, *h_scales;
+};
+w4a4_status expert_bwd(int64_t T, int H, int I, int E, int k, int row_align, const void* dy, const void* x,
+                       const void* w1, const void* w2, const SavedH& saved, const float* topk_w,
+                       const int32_t* expert_offsets, const int32_t* row_map, void* dx, void* dw1, void* dw2,
+                       const int32_t* src_row, void* workspace, const BwdWs& L, void* stream) {
   const int64_t cap = w4a4_rows_capacity(T, k, E, row_align);
-  const BwdWs L = bwd_ws(cap, H, I, E);
-  if (workspace == nullptr || workspace_bytes < L.total)
-    return fail(W4A4_ERR_WORKSPACE, "workspace needs %zu bytes", L.total);
-  OPTIONAL_PTR(workspace);
   hipStream_t s = static_cast<hipStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   int32_t* sched = reinterpret_cast<int32_t*>(ws + L.sched);
@@ -479,8 +475,9 @@ w4a4_status w4a4_expert_bwd(int64_t T, int H, int I, int E, int k, int row_align
   uint16_t* dH = reinterpret_cast<uint16_t*>(ws + L.dH);
   uint16_t* dXp = reinterpret_cast<uint16_t*>(ws + L.dXp);
   uint16_t* xp = reinterpret_cast<uint16_t*>(ws + L.xp);
-  const uint16_t* h = static_cast<const uint16_t*>(save_h);
-  const uint16_t* a = static_cast<const uint16_t*>(save_a);
+  const uint16_t* h = static_cast<const uint16_t*>(saved.h);
+  uint16_t* a_made = saved.h_codes != nullptr ? reinterpret_cast<uint16_t*>(ws + L.a) : nullptr;
+  const uint16_t* a = a_made != nullptr ? a_made : static_cast<const uint16_t*>(saved.a);
   const uint16_t* W1 = static_cast<const uint16_t*>(w1);
   const uint16_t* W2 = static_cast<const uint16_t*>(w2);
 
@@ -508,7 +505,11 @@ w4a4_status w4a4_expert_bwd(int64_t T, int H, int I, int E, int k, int row_align
     return W4A4_ERR_LAUNCH;
   if (row_align > 1 && !launch_zero_pad_rows(cap, H, src_row, expert_offsets, E, dO, s))
     return W4A4_ERR_LAUNCH;
-  if (cap > 0 && !launch_dgrad_fc2(cap, H, I, E, expert_offsets, dO, W2, h, dH, s)) return W4A4_ERR_LAUNCH;
+  if (cap > 0 && !(saved.h_codes != nullptr
+                       ? launch_dgrad_fc2_ckpt(cap, H, I, E, expert_offsets, dO, W2, saved.h_codes, saved.h_scales, dH,
+                                               a_made, s)
+                       : launch_dgrad_fc2(cap, H, I, E, expert_offsets, dO, W2, h, dH, s)))
+    return W4A4_ERR_LAUNCH;
   // (forked after the FC2 dgrad: beside the persistent FC2 wgrad the copy
   // costs the GEMM little; beside the FC2 dgrad it took that kernel's slots.
   // The wait for the schedule comes before the fork, so that the FC2 wgrad
@@ -533,6 +534,52 @@ w4a4_status w4a4_expert_bwd(int64_t T, int H, int I, int E, int k, int row_align
   if (!launch_gather_sum(T, H, k, dXp, row_map, static_cast<uint16_t*>(dx), s))
     return W4A4_ERR_LAUNCH;
   return W4A4_OK;
+}
+}  // namespace
+
+w4a4_status w4a4_expert_bwd(int64_t T, int H, int I, int E, int k, int row_align, const void* dy,
+                            const void* x, const void* w1, const void* w2, const void* save_h,
+                            const void* save_a, const float* topk_w,
+                            const int32_t* expert_offsets, const int32_t* row_map,
+                            const int32_t* src_row, void* dx, void* dw1, void* dw2,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+  g_last_error.clear();
+  w4a4_status st = check_moe_shape(T, H, I, E, k, row_align);
+  if (st != W4A4_OK) return st;
+  REQUIRE_PTR(expert_offsets);
+  REQUIRE_PTR(w1); REQUIRE_PTR(w2); REQUIRE_PTR(dw1); REQUIRE_PTR(dw2);
+  if (T > 0) {
+    REQUIRE_PTR(dy); REQUIRE_PTR(x); REQUIRE_PTR(save_h); REQUIRE_PTR(save_a);
+    REQUIRE_PTR(topk_w); REQUIRE_PTR(row_map); REQUIRE_PTR(src_row); REQUIRE_PTR(dx);
+  }
+  const BwdWs L = bwd_ws(w4a4_rows_capacity(T, k, E, row_align), H, I, E);
+  if (workspace == nullptr || workspace_bytes < L.total)
+    return fail(W4A4_ERR_WORKSPACE, "workspace needs %zu bytes", L.total);
+  OPTIONAL_PTR(workspace);
+  return expert_bwd(T, H, I, E, k, row_align, dy, x, w1, w2, SavedH{save_h, save_a, nullptr, nullptr}, topk_w,
+                    expert_offsets, row_map, dx, dw1, dw2, src_row, workspace, L, stream);
+}
+
+w4a4_status w4a4_expert_bwd_ckpt(int64_t T, int H, int I, int E, int k, int row_align, const void* dy, const void* x,
+                                 const void* w1, const void* w2, const uint8_t* h_codes, const uint8_t* h_scales,
+                                 const float* topk_w, const int32_t* expert_offsets, const int32_t* row_map,
+                                 const int32_t* src_row, void* dx, void* dw1, void* dw2, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+  g_last_error.clear();
+  w4a4_status st = check_moe_shape(T, H, I, E, k, row_align);
+  if (st != W4A4_OK) return st;
+  REQUIRE_PTR(expert_offsets);
+  REQUIRE_PTR(w1); REQUIRE_PTR(w2); REQUIRE_PTR(dw1); REQUIRE_PTR(dw2);
+  if (T > 0) {
+    REQUIRE_PTR(dy); REQUIRE_PTR(x); REQUIRE_PTR(h_codes); REQUIRE_PTR(h_scales);
+    REQUIRE_PTR(topk_w); REQUIRE_PTR(row_map); REQUIRE_PTR(src_row); REQUIRE_PTR(dx);
+  }
+  const BwdWs L = bwd_ws(w4a4_rows_capacity(T, k, E, row_align), H, I, E, true);
+  if (workspace == nullptr || workspace_bytes < L.total)
+    return fail(W4A4_ERR_WORKSPACE, "workspace needs %zu bytes", L.total);
+  OPTIONAL_PTR(workspace);
+  return expert_bwd(T, H, I, E, k, row_align, dy, x, w1, w2, SavedH{nullptr, nullptr, h_codes, h_scales}, topk_w,
+                    expert_offsets, row_map, dx, dw1, dw2, src_row, workspace, L, stream);
 }
 
 namespace {

@@ -47,9 +47,11 @@
 // halves the copy traffic per flop.
 
 #include <algorithm>
+#include <type_traits>
 
 #include "gemm_common.h"
 #include "internal.h"
+#include "mx_encode.h"
 
 namespace w4a4 {
 namespace {
@@ -198,7 +200,7 @@ __device__ __forceinline__ void ring_idle_barrier() {
 }
 
 // ------------------------------------------------------------------ dgrad
-enum class DgradMode { FC2_SWIGLU, FC1 };
+enum class DgradMode { FC2_SWIGLU, FC2_SWIGLU_CKPT, FC1 };
 
 struct DgradArgs {
   int64_t rows_alloc;
@@ -208,6 +210,31 @@ struct DgradArgs {
   const uint16_t* w;   // [E, K, N]   W2[e] ([H, I]) or W1[e] ([2I, H])
   const uint16_t* h;   // [rows, 2I]  saved FC1 output (FC2_SWIGLU)
   uint16_t* out;       // dH [rows, 2I] or dXp [rows, H]
+  // FC2_SWIGLU_CKPT: h in MXFP8 [rows, 2I], and where a goes [rows, I]
+  const uint8_t* h_codes;
+  const uint8_t* h_scales;
+  uint16_t* a_out;
+};
+
+// Eight elements of the saved h: bf16, or an MXFP8 block's codes and scale.
+struct HBf16 {
+  u32x4_t w;
+  __device__ __forceinline__ void load(const DgradArgs& args, int64_t at) {
+    w = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(args.h + at));
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = bf16_to_f32(static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1))));
+  }
+};
+struct HMx8 {
+  u32x2_t c;
+  uint32_t scale;
+  __device__ __forceinline__ void load(const DgradArgs& args, int64_t at) {
+    c = __builtin_nontemporal_load(reinterpret_cast<const u32x2_t*>(args.h_codes + at));
+    scale = args.h_scales[at >> 5];
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const { mx_decode8(c, scale, v); }
 };
 
 using BCol = KCol<kBN>;
@@ -391,15 +418,18 @@ dgrad_kernel(DgradArgs args) {
       __builtin_nontemporal_store(v, reinterpret_cast<u32x4_t*>(args.out + (tc.m0 + lrow) * args.N + n));
     }
   } else {
-    // SwiGLU backward on bf16 dA, gate / up from the saved bf16 h, in two
+    // SwiGLU backward on bf16 dA, gate / up from the saved h, in two
     // batches of chunks: the first batch's h loads go out before the
     // accumulators are staged (their HBM latency runs under the staging),
-    // the second's before the first batch is computed.
+    // the second's before the first batch is computed.  From a checkpoint in
+    // MXFP8 the same values give a once more, the FC2 wgrad's operand.
+    constexpr bool kCkpt = MODE == DgradMode::FC2_SWIGLU_CKPT;
+    using Saved = std::conditional_t<kCkpt, HMx8, HBf16>;
     const int I = args.I;
     constexpr int kBatch = kIters / 2;
     static_assert(kIters % 2 == 0, "two whole batches");
-    u32x4_t hg0[kBatch], hu0[kBatch], hg1[kBatch], hu1[kBatch];
-    auto load_h = [&](int b0, u32x4_t (&hg)[kBatch], u32x4_t (&hu)[kBatch]) {
+    Saved hg0[kBatch], hu0[kBatch], hg1[kBatch], hu1[kBatch];
+    auto load_h = [&](int b0, Saved (&hg)[kBatch], Saved (&hu)[kBatch]) {
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         // unconditional (clamped to the tile's last row and the last column
@@ -407,12 +437,12 @@ dgrad_kernel(DgradArgs args) {
         const int c = tid + (b0 + i) * kThreads;
         const int lrow = min(c / kChunksPerRow, rows - 1);
         const int n = min(n0 + (c % kChunksPerRow) * 8, args.N - 8);
-        const uint16_t* hr = args.h + (tc.m0 + lrow) * (2 * I) + n;
-        hg[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(hr));
-        hu[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(hr + I));
+        const int64_t at = (tc.m0 + lrow) * (2 * I) + n;
+        hg[i].load(args, at);
+        hu[i].load(args, at + I);
       }
     };
-    auto swiglu_store = [&](int b0, const u32x4_t (&hg)[kBatch], const u32x4_t (&hu)[kBatch]) {
+    auto swiglu_store = [&](int b0, const Saved (&hg)[kBatch], const Saved (&hu)[kBatch]) {
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         const int c = tid + (b0 + i) * kThreads;
@@ -420,24 +450,30 @@ dgrad_kernel(DgradArgs args) {
         if (lrow >= rows || n >= args.N) continue;
         const int64_t row = tc.m0 + lrow;
         const u32x4_t v = *reinterpret_cast<const u32x4_t*>(lds + lrow * kOutPitch + (n - n0) * 2);
-        u32x4_t dg, du;
+        float gate[8], upv[8];
+        hg[i].get(gate);
+        hu[i].get(upv);
+        u32x4_t dg, du, av;
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
-          float rg[2], ru[2];
+          float rg[2], ru[2], ra[2];
 #pragma unroll
           for (int p = 0; p < 2; ++p) {
             const float da = bf16_to_f32(static_cast<uint16_t>(v[d] >> (16 * p)));
-            const float gt = bf16_to_f32(static_cast<uint16_t>(hg[i][d] >> (16 * p)));
-            const float up = bf16_to_f32(static_cast<uint16_t>(hu[i][d] >> (16 * p)));
+            const float gt = gate[2 * d + p];
+            const float up = upv[2 * d + p];
             const float sg = sigmoid_fast(gt);
             rg[p] = da * up * sg * (1.0f + gt * (1.0f - sg));
             ru[p] = da * gt * sg;
+            if constexpr (kCkpt) ra[p] = gt * sg * up;
           }
           dg[d] = pack_bf16x2(rg[0], rg[1]);
           du[d] = pack_bf16x2(ru[0], ru[1]);
+          if constexpr (kCkpt) av[d] = pack_bf16x2(ra[0], ra[1]);
         }
         __builtin_nontemporal_store(dg, reinterpret_cast<u32x4_t*>(args.out + row * (2 * I) + n));
         __builtin_nontemporal_store(du, reinterpret_cast<u32x4_t*>(args.out + row * (2 * I) + I + n));
+        if constexpr (kCkpt) __builtin_nontemporal_store(av, reinterpret_cast<u32x4_t*>(args.a_out + row * I + n));
       }
     };
     load_h(0, hg0, hu0);
@@ -1140,13 +1176,20 @@ bool launch_wgrad(const wg::WgradArgs& a, const char* name, hipStream_t s, int s
 bool launch_dgrad_fc2(int64_t rows_alloc, int H, int I, int E, const int32_t* offsets,
                       const uint16_t* dO, const uint16_t* w2, const uint16_t* h, uint16_t* dH,
                       hipStream_t s) {
-  dg::DgradArgs a{rows_alloc, H, I, I, E, offsets, dO, w2, h, dH};
+  dg::DgradArgs a{rows_alloc, H, I, I, E, offsets, dO, w2, h, dH, nullptr, nullptr, nullptr};
   return launch_dgrad<dg::DgradMode::FC2_SWIGLU>(a, "gemm_dgrad_fc2", s);
+}
+
+bool launch_dgrad_fc2_ckpt(int64_t rows_alloc, int H, int I, int E, const int32_t* offsets, const uint16_t* dO,
+                           const uint16_t* w2, const uint8_t* h_codes, const uint8_t* h_scales, uint16_t* dH,
+                           uint16_t* a_out, hipStream_t s) {
+  dg::DgradArgs a{rows_alloc, H, I, I, E, offsets, dO, w2, nullptr, dH, h_codes, h_scales, a_out};
+  return launch_dgrad<dg::DgradMode::FC2_SWIGLU_CKPT>(a, "gemm_dgrad_fc2", s);
 }
 
 bool launch_dgrad_fc1(int64_t rows_alloc, int H, int I, int E, const int32_t* offsets,
                       const uint16_t* dH, const uint16_t* w1, uint16_t* dXp, hipStream_t s) {
-  dg::DgradArgs a{rows_alloc, 2 * I, H, I, E, offsets, dH, w1, nullptr, dXp};
+  dg::DgradArgs a{rows_alloc, 2 * I, H, I, E, offsets, dH, w1, nullptr, dXp, nullptr, nullptr, nullptr};
   return launch_dgrad<dg::DgradMode::FC1>(a, "gemm_dgrad_fc1", s);
 }
 
@@ -1186,7 +1229,7 @@ size_t linear_wgrad_schedule_ints(int K, int N) {
 
 bool launch_linear_dgrad(int64_t T, int K, int N, const int32_t* offsets, const uint16_t* dy,
                          const uint16_t* w, uint16_t* dx, hipStream_t s) {
-  dg::DgradArgs a{T, N, K, N / 2, 1, offsets, dy, w, nullptr, dx};
+  dg::DgradArgs a{T, N, K, N / 2, 1, offsets, dy, w, nullptr, dx, nullptr, nullptr, nullptr};
   return launch_dgrad<dg::DgradMode::FC1>(a, "gemm_linear_dgrad", s);
 }
 

@@ -164,6 +164,11 @@ bool launch_dgrad_fc2(int64_t rows_alloc, int H, int I, int E, const int32_t* of
                       const uint16_t* dO, const uint16_t* w2, const uint16_t* h, uint16_t* dH,
                       hipStream_t s);
 
+// The same from h in MXFP8 [rows, 2I]; also writes a = bf16(SwiGLU(h)) [rows, I].
+bool launch_dgrad_fc2_ckpt(int64_t rows_alloc, int H, int I, int E, const int32_t* offsets, const uint16_t* dO,
+                           const uint16_t* w2, const uint8_t* h_codes, const uint8_t* h_scales, uint16_t* dH,
+                           uint16_t* a_out, hipStream_t s);
+
 // FC1 dgrad: dXp = bf16(dH_e W1[e]).
 bool launch_dgrad_fc1(int64_t rows_alloc, int H, int I, int E, const int32_t* offsets,
                       const uint16_t* dH, const uint16_t* w1, uint16_t* dXp, hipStream_t s);

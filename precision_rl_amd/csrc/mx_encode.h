@@ -1,4 +1,5 @@
-// Device encoders of MX blocks (OCP Microscaling Formats v1.0, section 6.3)
+// Device encoders of MX blocks (OCP Microscaling Formats v1.0, section 6.3), and
+// the decoder of MXFP8 ones,
 // in the lane layout of the row operators: a lane holds 8 consecutive bf16
 // elements of a row (16 bytes), a block of 32 is a quad of lanes.
 //   X = floor(log2 amax) - emax clamped to [-127, 127], scale byte X + 127,
@@ -93,4 +94,21 @@ __device__ __forceinline__ void mx_store8(uint8_t* codes, uint8_t* scales, int64
   if ((chunk & 3) == 0) scales[chunk >> 2] = static_cast<uint8_t>(byte);
 }
 
+// 2^X of the scale byte X + 127 (255, E8M0's NaN: NaN).
+__device__ __forceinline__ float mx_scale(uint32_t byte) {
+  return __uint_as_float(byte == 0u ? 0x00400000u : byte == 255u ? 0x7FC00000u : byte << 23);
+}
+// The values of a lane's eight E4M3 codes of a block.
+__device__ __forceinline__ void mx_decode8(const u32x2_t& c, uint32_t byte, float (&v)[8]) {
+  const float scale = mx_scale(byte);
+#pragma unroll
+  for (int d = 0; d < 2; ++d) {
+    const float2_t lo = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(c[d]), false);
+    const float2_t hi = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(c[d]), true);
+    v[4 * d] = lo[0] * scale;
+    v[4 * d + 1] = lo[1] * scale;
+    v[4 * d + 2] = hi[0] * scale;
+    v[4 * d + 3] = hi[1] * scale;
+  }
+}
 }  // namespace w4a4

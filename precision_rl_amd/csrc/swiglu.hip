@@ -26,23 +26,6 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// 2^X of the scale byte X + 127 (255, E8M0's NaN: NaN).
-__device__ __forceinline__ float mx_scale(uint32_t byte) {
-  return __uint_as_float(byte == 0u ? 0x00400000u : byte == 255u ? 0x7FC00000u : byte << 23);
-}
-__device__ __forceinline__ void mx_decode8(const u32x2_t& c, uint32_t byte, float (&v)[8]) {
-  typedef float f32x2_t __attribute__((ext_vector_type(2)));
-  const float scale = mx_scale(byte);
-#pragma unroll
-  for (int d = 0; d < 2; ++d) {
-    const f32x2_t lo = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(c[d]), false);
-    const f32x2_t hi = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(c[d]), true);
-    v[4 * d] = lo[0] * scale;
-    v[4 * d + 1] = lo[1] * scale;
-    v[4 * d + 2] = hi[0] * scale;
-    v[4 * d + 3] = hi[1] * scale;
-  }
-}
 __device__ __forceinline__ void unpack8(const u32x4_t& w, float (&v)[8]) {
 #pragma unroll
   for (int d = 0; d < 4; ++d) {

@@ -158,3 +158,24 @@ def test_workspace_sizes(lib):
     assert size(1, 8, 128) == 0 and size(0, 8, 128) == 0
     assert size(16384, 8, 128) >= 4 * 128 * (16384 * 8 // 1024 + 1)
     assert size(16384, 9, 128) == size(16384, 8, 1025) == size(-1, 8, 128) == size(16384, 0, 128) == 0
+
+
+CKPT = ("T", "H", "I", "E", "k", "align", "dy", "x", "w1", "w2", "hc", "hs", "p", "offsets", "row_map", "src_row", "dx",
+        "dw1", "dw2", "ws", "wsb")
+
+
+@pytest.mark.parametrize("change,status,says", [
+    (dict(T=-1), INVALID, "T=-1"), (dict(H=250), INVALID, "multiples of 32"), (dict(H=288), UNSUPPORTED, "256"),
+    (dict(I=96), UNSUPPORTED, "128"), (dict(k=9, E=16), UNSUPPORTED, "k <= 8"), (dict(align=2), INVALID, "row_align"),
+    (dict(hc=None), INVALID, "h_codes"), (dict(hs=None), INVALID, "h_scales"), (dict(hc="hc+8"), INVALID, "h_codes"),
+    (dict(dw2=None), INVALID, "dw2"), (dict(ws=None), WORKSPACE, "workspace"), (dict(wsb=1 << 10), WORKSPACE, "workspace"),
+    (dict(ws="ws+4"), INVALID, "workspace")])
+def test_expert_backward_from_a_checkpoint(lib, at, change, status, says):
+    base = _base(CKPT, T=4, H=256, I=128, E=8, k=2, align=1, wsb=1 << 30)
+    assert _status(lib, at, "w4a4_expert_bwd_ckpt", CKPT, base, change) == status
+    assert says in lib.w4a4_last_error().decode()
+
+
+def test_expert_backward_workspace_holds_a_beside_the_others(lib):
+    size = lambda kind: lib.w4a4_workspace_size(kind, 64, 256, 128, 8, 2, 16)  # noqa: E731
+    assert size(9) == size(2) + -(-(64 * 2 + 8 * 15) * 128 * 2 // 256) * 256
