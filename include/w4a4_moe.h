@@ -260,6 +260,26 @@ w4a4_status w4a4_grouped_expert_fwd(
     void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * w4a4_grouped_expert_fwd_ckpt -- w4a4_grouped_expert_fwd that keeps h in MXFP8
+ * for w4a4_expert_bwd_ckpt in place of bf16 h and a: FC1's epilogue writes the
+ * checkpoint (the bytes of w4a4_mx_quantize_rows on the bf16 h) instead of h.
+ *   h_codes [cap, 2I], h_scales [cap, 2I/32] uint8 out; rows at or past
+ *              expert_offsets[E] are not written.
+ *   save_o     optional [cap, H] bf16 out: the experts' outputs o, which the
+ *              gradient of topk_w needs (w4a4_unpermute_bwd).
+ *   y and every other argument as in w4a4_grouped_expert_fwd, with its bits.
+ */
+w4a4_status w4a4_grouped_expert_fwd_ckpt(
+    int64_t T, int H, int I, int E, int k, int row_align,
+    const uint8_t* x_codes, const uint8_t* x_scales, const float* x_outer,
+    const int32_t* expert_offsets, const int32_t* row_map, const int32_t* src_row,
+    const float* topk_w,
+    const uint8_t* w1_codes, const uint8_t* w1_scales, const float* w1_outer,
+    const uint8_t* w2_codes, const uint8_t* w2_scales, const float* w2_outer,
+    void* y, uint8_t* h_codes, uint8_t* h_scales, void* save_o,
+    void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * w4a4_expert_bwd -- the straight-through BF16 backward on the
  * saved high-precision operands (no backward quantisation).
  *   Defined by: AI summary, "Methodology in Plain English" (the quantisers'
@@ -302,9 +322,9 @@ w4a4_status w4a4_expert_bwd(
  * FC2 dgrad's epilogue decodes them for the SwiGLU backward and makes a =
  * bf16(SwiGLU(h)) once more for dW2.  The results are those of w4a4_expert_bwd
  * on the decoded h and that a.
- *   h_codes [cap, 2I], h_scales [cap, 2I/32]: w4a4_swiglu_fwd's checkpoint of
- *              the forward's save_h (rows = expert_offsets + E), or
- *              w4a4_mx_quantize_rows of it, W4A4_MX_FP8.
+ *   h_codes [cap, 2I], h_scales [cap, 2I/32]: of w4a4_grouped_expert_fwd_ckpt
+ *              or w4a4_mx_grouped_expert_fwd_ckpt, or w4a4_swiglu_fwd's
+ *              checkpoint of a bf16 h (rows = expert_offsets + E).
  *   The other arguments and the requirements are w4a4_expert_bwd's; workspace:
  *   W4A4_WS_BACKWARD_CKPT (a beside the other's).
  */
@@ -413,6 +433,18 @@ w4a4_status w4a4_mx_grouped_expert_fwd(
     const uint8_t* w2_codes, const uint8_t* w2_scales,
     void* y, void* save_h, void* save_a, float* dbg_fc1_f32,
     uint8_t* dbg_a_codes, uint8_t* dbg_a_scales,
+    void* workspace, size_t workspace_bytes, void* stream);
+
+/* w4a4_mx_grouped_expert_fwd_ckpt -- w4a4_mx_grouped_expert_fwd that keeps h in
+ * MXFP8, and o where it is wanted, as w4a4_grouped_expert_fwd_ckpt does. */
+w4a4_status w4a4_mx_grouped_expert_fwd_ckpt(
+    int64_t T, int H, int I, int E, int k, int row_align,
+    const uint8_t* x_codes, const uint8_t* x_scales,
+    const int32_t* expert_offsets, const int32_t* row_map, const int32_t* src_row,
+    const float* topk_w,
+    const uint8_t* w1_codes, const uint8_t* w1_scales,
+    const uint8_t* w2_codes, const uint8_t* w2_scales,
+    void* y, uint8_t* h_codes, uint8_t* h_scales, void* save_o,
     void* workspace, size_t workspace_bytes, void* stream);
 
 /*
@@ -587,7 +619,9 @@ w4a4_status w4a4_mx_linear_fwd(
  * all-to-all, experts in bf16) and for training the router.  Beside the
  * library's own expert calls: rows [0, cap) of xp quantised with identity
  * routing are the rows of w4a4_quantize_permute, and the expert calls run on
- * them as cap tokens with k = 1 and row_map[r] = r.
+ * them as cap tokens with k = 1 and row_map[r] = r.  The maps of a quantising
+ * permute serve here too: with the o that w4a4_grouped_expert_fwd_ckpt keeps,
+ * w4a4_unpermute_bwd gives the gradient of the router's weights.
  *   Layout as in w4a4_quantize_permute (Expert-contiguous layout above), with
  *   these additions.  An id outside [0, E) is a slot that is not dispatched
  *   (another rank's expert, a dropped token): its row_map entry is -1, it takes

@@ -27,6 +27,14 @@ _SIGS = {
                                         c_vp, c_vp, c_vp, c_vp, c_vp, c_vp,
                                         c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp,
                                         c_vp, c_sz, c_vp]),
+    "w4a4_grouped_expert_fwd_ckpt": (c_int, [c_i64, c_int, c_int, c_int, c_int, c_int,
+                                             c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp,
+                                             c_vp, c_vp, c_vp, c_vp, c_vp, c_vp,
+                                             c_vp, c_vp, c_vp, c_vp, c_vp, c_sz, c_vp]),
+    "w4a4_mx_grouped_expert_fwd_ckpt": (c_int, [c_i64, c_int, c_int, c_int, c_int, c_int,
+                                                c_vp, c_vp, c_vp, c_vp, c_vp, c_vp,
+                                                c_vp, c_vp, c_vp, c_vp,
+                                                c_vp, c_vp, c_vp, c_vp, c_vp, c_sz, c_vp]),
     "w4a4_expert_bwd": (c_int, [c_i64, c_int, c_int, c_int, c_int, c_int,
                                 c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp,
                                 c_vp, c_vp, c_vp, c_vp, c_sz, c_vp]),
@@ -783,10 +791,50 @@ def w4a4_swiglu_bwd(da, kept, a=False, dh=True, rows=None, out=None):
     return res
 
 
+def w4a4_grouped_expert_fwd_ckpt(xq, topk_w, w1q, w2q, T, H, I, E, k, row_align=1, save_o=False, out=None,  # noqa: E741
+                                 workspace=None):
+    """``w4a4_grouped_expert_fwd``, or with xq of ``w4a4_mx_quantize_permute`` (which has no outer scales)
+    ``w4a4_mx_grouped_expert_fwd``, that keeps h in MXFP8 for ``w4a4_expert_bwd_ckpt`` in place of bf16 h and a.
+
+    Returns dict(y [T, H], h_codes [cap, 2I] and h_scales [cap, 2I/32] uint8, and with `save_o` the experts' outputs o
+    [cap, H] bf16, which ``w4a4_unpermute_bwd`` takes for the gradient of topk_w); rows of h and o from
+    offsets[E] on are not written.  Tensors of `out` are used where given.  workspace: at least
+    workspace_size(WS_FORWARD, T, H, I, E, k, row_align) bytes (uint8)."""
+    dev, bf16, i32, u8, f32 = xq["codes"].device, torch.bfloat16, torch.int32, torch.uint8, torch.float32
+    mx = "outer" not in xq
+    cap, block = rows_capacity(T, k, E, row_align), 32 if mx else 16
+    res = {} if out is None else dict(out)
+    for name, shape, dtype in (("y", (T, H), bf16), ("h_codes", (cap, 2 * I), u8), ("h_scales", (cap, 2 * I // 32), u8)):
+        if res.get(name) is None:
+            res[name] = torch.empty(shape, dtype=dtype, device=dev)
+    if save_o and res.get("o") is None:
+        res["o"] = torch.empty(cap, H, dtype=bf16, device=dev)
+    nbytes = workspace_size(WS_FORWARD, T, H, I, E, k, row_align)
+    if workspace is not None:
+        _check_workspace(workspace, nbytes, dev.index)
+    else:
+        workspace = _workspace(nbytes, dev)
+
+    def operand(q, name, *rows, width):
+        got = [_ptr(q["codes"], f"{name} codes", (*rows, width // 2), u8, dev),
+               _ptr(q["scales"], f"{name} scales", (*rows, width // block), u8, dev)]
+        return got if mx else got + [_ptr(q["outer"], f"{name} outer", rows, f32, dev)]
+
+    lib = load()
+    _call(lib.w4a4_mx_grouped_expert_fwd_ckpt if mx else lib.w4a4_grouped_expert_fwd_ckpt, dev, T, H, I, E, k,
+          row_align, *operand(xq, "xq", cap, width=H), _ptr(xq["offsets"], "offsets", (E + 1,), i32, dev),
+          _ptr(xq["row_map"], "row_map", (T, k), i32, dev), _ptr(xq["src_row"], "src_row", (cap,), i32, dev),
+          _ptr(topk_w, "topk_w", (T, k), f32, dev), *operand(w1q, "w1q", E, 2 * I, width=H),
+          *operand(w2q, "w2q", E, H, width=I), _ptr(res["y"], "y", (T, H), bf16, dev),
+          *_checkpoint(res, cap, 2 * I, dev), _ptr(res["o"], "o", (cap, H), bf16, dev) if save_o else None,
+          workspace.data_ptr(), workspace.numel())
+    return res
+
+
 def w4a4_expert_bwd_ckpt(dy, x, w1, w2, kept, topk_w, xq, T, H, I, E, k, row_align=1, out=None, workspace=None):  # noqa: E741
     """``w4a4_expert_bwd`` from an MXFP8 checkpoint of h in place of the bf16 h and a: kept is a dict with h_codes
-    [cap, 2I] and h_scales [cap, 2I/32] uint8, as ``w4a4_swiglu_fwd(h, a=False, checkpoint=True,
-    rows=xq["offsets"][E:])`` makes it of the forward's h.  Returns dict(dx [T, H], dw1 [E, 2I, H], dw2 [E, H, I])
+    [cap, 2I] and h_scales [cap, 2I/32] uint8, of ``w4a4_grouped_expert_fwd_ckpt`` (or ``w4a4_swiglu_fwd(h, a=False,
+    checkpoint=True, rows=xq["offsets"][E:])`` of a bf16 h).  Returns dict(dx [T, H], dw1 [E, 2I, H], dw2 [E, H, I])
     bf16.  workspace: at least workspace_size(WS_BACKWARD_CKPT, T, H, I, E, k, row_align) bytes (uint8)."""
     dev, bf16, i32 = w1.device, torch.bfloat16, torch.int32
     cap = rows_capacity(T, k, E, row_align)

@@ -405,15 +405,20 @@ w4a4_status w4a4_quantize_permute(const void* x, int64_t T, int K, const int32_t
   return W4A4_OK;
 }
 
-w4a4_status w4a4_grouped_expert_fwd(
+namespace {
+// What a forward keeps beside (or in place of) bf16 h and a: h in MXFP8, and o.
+struct Kept {
+  uint8_t *h_codes = nullptr, *h_scales = nullptr;
+  void* o = nullptr;
+};
+w4a4_status grouped_fwd(
     int64_t T, int H, int I, int E, int k, int row_align, const uint8_t* x_codes,
     const uint8_t* x_scales, const float* x_outer, const int32_t* expert_offsets,
     const int32_t* row_map, const int32_t* src_row, const float* topk_w, const uint8_t* w1_codes,
     const uint8_t* w1_scales, const float* w1_outer, const uint8_t* w2_codes,
     const uint8_t* w2_scales, const float* w2_outer, void* y, void* save_h, void* save_a,
     float* dbg_fc1_f32, uint8_t* dbg_a_codes, uint8_t* dbg_a_scales, float* dbg_a_outer,
-    void* workspace, size_t workspace_bytes, void* stream) {
-  g_last_error.clear();
+    void* workspace, size_t workspace_bytes, void* stream, const Kept& kept) {
   w4a4_status st = check_moe_shape(T, H, I, E, k, row_align);
   if (st != W4A4_OK) return st;
   REQUIRE_PTR(expert_offsets);
@@ -423,6 +428,7 @@ w4a4_status w4a4_grouped_expert_fwd(
     REQUIRE_PTR(x_codes); REQUIRE_PTR(x_scales); REQUIRE_PTR(x_outer);
     REQUIRE_PTR(row_map); REQUIRE_PTR(src_row); REQUIRE_PTR(topk_w); REQUIRE_PTR(y);
   }
+  OPTIONAL_PTR(kept.h_codes); OPTIONAL_PTR(kept.h_scales); OPTIONAL_PTR(kept.o);
   OPTIONAL_PTR(save_h); OPTIONAL_PTR(save_a); OPTIONAL_PTR(dbg_fc1_f32);
   OPTIONAL_PTR(dbg_a_codes); OPTIONAL_PTR(dbg_a_scales); OPTIONAL_PTR(dbg_a_outer);
   const int nd = (dbg_a_codes != nullptr) + (dbg_a_scales != nullptr) + (dbg_a_outer != nullptr);
@@ -440,11 +446,11 @@ w4a4_status w4a4_grouped_expert_fwd(
   uint8_t* a_codes = nd ? dbg_a_codes : ws + L.a_codes;
   uint8_t* a_scales = nd ? dbg_a_scales : ws + L.a_scales;
   float* a_outer = nd ? dbg_a_outer : reinterpret_cast<float*>(ws + L.a_outer);
-  uint16_t* o_buf = reinterpret_cast<uint16_t*>(ws + L.o);
+  uint16_t* o_buf = kept.o ? static_cast<uint16_t*>(kept.o) : reinterpret_cast<uint16_t*>(ws + L.o);
 
   if (!launch_fc1(cap, H, I, E, expert_offsets, Fp4Operand{x_codes, x_scales, x_outer},
                   Fp4Operand{w1_codes, w1_scales, w1_outer}, static_cast<uint16_t*>(save_h), a_buf,
-                  dbg_fc1_f32, s))
+                  dbg_fc1_f32, kept.h_codes, kept.h_scales, s))
     return W4A4_ERR_LAUNCH;
   if (!launch_requant(a_buf, cap, I, expert_offsets, E, src_row, a_codes, a_scales, a_outer, s))
     return W4A4_ERR_LAUNCH;
@@ -454,6 +460,38 @@ w4a4_status w4a4_grouped_expert_fwd(
   if (!launch_unpermute(T, H, k, o_buf, row_map, topk_w, static_cast<uint16_t*>(y), s))
     return W4A4_ERR_LAUNCH;
   return W4A4_OK;
+}
+}  // namespace
+
+w4a4_status w4a4_grouped_expert_fwd(
+    int64_t T, int H, int I, int E, int k, int row_align, const uint8_t* x_codes,
+    const uint8_t* x_scales, const float* x_outer, const int32_t* expert_offsets,
+    const int32_t* row_map, const int32_t* src_row, const float* topk_w, const uint8_t* w1_codes,
+    const uint8_t* w1_scales, const float* w1_outer, const uint8_t* w2_codes,
+    const uint8_t* w2_scales, const float* w2_outer, void* y, void* save_h, void* save_a,
+    float* dbg_fc1_f32, uint8_t* dbg_a_codes, uint8_t* dbg_a_scales, float* dbg_a_outer,
+    void* workspace, size_t workspace_bytes, void* stream) {
+  g_last_error.clear();
+  return grouped_fwd(T, H, I, E, k, row_align, x_codes, x_scales, x_outer, expert_offsets, row_map, src_row, topk_w,
+                     w1_codes, w1_scales, w1_outer, w2_codes, w2_scales, w2_outer, y, save_h, save_a, dbg_fc1_f32,
+                     dbg_a_codes, dbg_a_scales, dbg_a_outer, workspace, workspace_bytes, stream, Kept{});
+}
+
+w4a4_status w4a4_grouped_expert_fwd_ckpt(
+    int64_t T, int H, int I, int E, int k, int row_align, const uint8_t* x_codes,
+    const uint8_t* x_scales, const float* x_outer, const int32_t* expert_offsets,
+    const int32_t* row_map, const int32_t* src_row, const float* topk_w, const uint8_t* w1_codes,
+    const uint8_t* w1_scales, const float* w1_outer, const uint8_t* w2_codes,
+    const uint8_t* w2_scales, const float* w2_outer, void* y, uint8_t* h_codes, uint8_t* h_scales,
+    void* save_o, void* workspace, size_t workspace_bytes, void* stream) {
+  g_last_error.clear();
+  if (T > 0 && check_moe_shape(T, H, I, E, k, row_align) == W4A4_OK) {
+    REQUIRE_PTR(h_codes);
+    REQUIRE_PTR(h_scales);
+  }
+  return grouped_fwd(T, H, I, E, k, row_align, x_codes, x_scales, x_outer, expert_offsets, row_map, src_row, topk_w,
+                     w1_codes, w1_scales, w1_outer, w2_codes, w2_scales, w2_outer, y, nullptr, nullptr, nullptr,
+                     nullptr, nullptr, nullptr, workspace, workspace_bytes, stream, Kept{h_codes, h_scales, save_o});
 }
 
 namespace {
@@ -658,14 +696,14 @@ w4a4_status w4a4_mx_quantize_permute(const void* x, int64_t T, int K, const int3
   return W4A4_OK;
 }
 
-w4a4_status w4a4_mx_grouped_expert_fwd(
+namespace {
+w4a4_status mx_grouped_fwd(
     int64_t T, int H, int I, int E, int k, int row_align, const uint8_t* x_codes,
     const uint8_t* x_scales, const int32_t* expert_offsets, const int32_t* row_map,
     const int32_t* src_row, const float* topk_w, const uint8_t* w1_codes, const uint8_t* w1_scales,
     const uint8_t* w2_codes, const uint8_t* w2_scales, void* y, void* save_h, void* save_a,
     float* dbg_fc1_f32, uint8_t* dbg_a_codes, uint8_t* dbg_a_scales, void* workspace,
-    size_t workspace_bytes, void* stream) {
-  g_last_error.clear();
+    size_t workspace_bytes, void* stream, const Kept& kept) {
   w4a4_status st = check_moe_shape(T, H, I, E, k, row_align);
   if (st != W4A4_OK) return st;
   REQUIRE_PTR(expert_offsets);
@@ -675,6 +713,7 @@ w4a4_status w4a4_mx_grouped_expert_fwd(
     REQUIRE_PTR(x_codes); REQUIRE_PTR(x_scales);
     REQUIRE_PTR(row_map); REQUIRE_PTR(src_row); REQUIRE_PTR(topk_w); REQUIRE_PTR(y);
   }
+  OPTIONAL_PTR(kept.h_codes); OPTIONAL_PTR(kept.h_scales); OPTIONAL_PTR(kept.o);
   OPTIONAL_PTR(save_h); OPTIONAL_PTR(save_a); OPTIONAL_PTR(dbg_fc1_f32);
   OPTIONAL_PTR(dbg_a_codes); OPTIONAL_PTR(dbg_a_scales);
   const int nd = (dbg_a_codes != nullptr) + (dbg_a_scales != nullptr);
@@ -693,11 +732,11 @@ w4a4_status w4a4_mx_grouped_expert_fwd(
   // the NVFP4 layout's code and scale areas hold the MXFP4 ones (fewer scale bytes)
   uint8_t* a_codes = nd ? dbg_a_codes : ws + L.a_codes;
   uint8_t* a_scales = nd ? dbg_a_scales : ws + L.a_scales;
-  uint16_t* o_buf = reinterpret_cast<uint16_t*>(ws + L.o);
+  uint16_t* o_buf = kept.o ? static_cast<uint16_t*>(kept.o) : reinterpret_cast<uint16_t*>(ws + L.o);
 
   if (!launch_fc1_mx(cap, H, I, E, expert_offsets, Fp4Operand{x_codes, x_scales, nullptr},
                      Fp4Operand{w1_codes, w1_scales, nullptr}, static_cast<uint16_t*>(save_h), a_buf,
-                     dbg_fc1_f32, s))
+                     dbg_fc1_f32, kept.h_codes, kept.h_scales, s))
     return W4A4_ERR_LAUNCH;
   if (!launch_requant_mx(a_buf, cap, I, expert_offsets, E, a_codes, a_scales, s)) return W4A4_ERR_LAUNCH;
   if (!launch_fc2_mx(cap, H, I, E, expert_offsets, Fp4Operand{a_codes, a_scales, nullptr},
@@ -706,6 +745,36 @@ w4a4_status w4a4_mx_grouped_expert_fwd(
   if (!launch_unpermute(T, H, k, o_buf, row_map, topk_w, static_cast<uint16_t*>(y), s))
     return W4A4_ERR_LAUNCH;
   return W4A4_OK;
+}
+}  // namespace
+
+w4a4_status w4a4_mx_grouped_expert_fwd(
+    int64_t T, int H, int I, int E, int k, int row_align, const uint8_t* x_codes,
+    const uint8_t* x_scales, const int32_t* expert_offsets, const int32_t* row_map,
+    const int32_t* src_row, const float* topk_w, const uint8_t* w1_codes, const uint8_t* w1_scales,
+    const uint8_t* w2_codes, const uint8_t* w2_scales, void* y, void* save_h, void* save_a,
+    float* dbg_fc1_f32, uint8_t* dbg_a_codes, uint8_t* dbg_a_scales, void* workspace,
+    size_t workspace_bytes, void* stream) {
+  g_last_error.clear();
+  return mx_grouped_fwd(T, H, I, E, k, row_align, x_codes, x_scales, expert_offsets, row_map, src_row, topk_w,
+                        w1_codes, w1_scales, w2_codes, w2_scales, y, save_h, save_a, dbg_fc1_f32, dbg_a_codes,
+                        dbg_a_scales, workspace, workspace_bytes, stream, Kept{});
+}
+
+w4a4_status w4a4_mx_grouped_expert_fwd_ckpt(
+    int64_t T, int H, int I, int E, int k, int row_align, const uint8_t* x_codes,
+    const uint8_t* x_scales, const int32_t* expert_offsets, const int32_t* row_map,
+    const int32_t* src_row, const float* topk_w, const uint8_t* w1_codes, const uint8_t* w1_scales,
+    const uint8_t* w2_codes, const uint8_t* w2_scales, void* y, uint8_t* h_codes, uint8_t* h_scales,
+    void* save_o, void* workspace, size_t workspace_bytes, void* stream) {
+  g_last_error.clear();
+  if (T > 0 && check_moe_shape(T, H, I, E, k, row_align) == W4A4_OK) {
+    REQUIRE_PTR(h_codes);
+    REQUIRE_PTR(h_scales);
+  }
+  return mx_grouped_fwd(T, H, I, E, k, row_align, x_codes, x_scales, expert_offsets, row_map, src_row, topk_w,
+                        w1_codes, w1_scales, w2_codes, w2_scales, y, nullptr, nullptr, nullptr, nullptr, nullptr,
+                        workspace, workspace_bytes, stream, Kept{h_codes, h_scales, save_o});
 }
 
 w4a4_status w4a4_mx8_expert_bwd(int64_t T, int H, int I, int E, int k, int row_align, const void* dy,

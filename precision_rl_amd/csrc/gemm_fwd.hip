@@ -36,6 +36,7 @@
 
 #include "gemm_common.h"
 #include "internal.h"
+#include "mx_encode.h"
 
 namespace w4a4 {
 namespace {
@@ -99,6 +100,8 @@ struct FwdArgs {
   uint16_t* out;     // FC1: h [rows, 2I] (may be null); FC2: o [rows, N]
   uint16_t* act;     // FC1: a [rows, I]
   float* dbg;        // FC1: pre-cast [rows, 2I] (may be null)
+  uint8_t* h_codes;  // FC1: h in MXFP8 [rows, 2I] and its scales, in place of out (may be null)
+  uint8_t* h_scales;
 };
 
 // Global row of B (weights) staged into LDS row p of the tile: lane j of wave
@@ -140,7 +143,9 @@ __device__ __forceinline__ void scale_pairs(uint32_t pair, half2_t& d0, half2_t&
 // products; 1.0 factors where the recipe has no outer scales), FC1 with the
 // SwiGLU.  s_gx: the tile's row outer scales in LDS; gw: this lane's four
 // weight outer scales; lds: the idle ring, used as staging.
-template <FwdMode MODE>
+// CKPT (FC1): h leaves in MXFP8 instead of bf16.  A template, not a branch beside
+// the other: that took the forward that saves bf16 h 0.6% more.
+template <FwdMode MODE, bool CKPT = false>
 __device__ __forceinline__ void fwd_epilogue(const FwdArgs& args, floatx16_t (&acc)[2][4], const TileCoord& tc,
                                              const float* s_gx, const float (&gw)[4], uint8_t* lds) {
   const int tid = threadIdx.x;
@@ -220,7 +225,7 @@ __device__ __forceinline__ void fwd_epilogue(const FwdArgs& args, floatx16_t (&a
         const u32x4_t hg = *reinterpret_cast<const u32x4_t*>(so + s * kOutPitch + ch * 16);
         const u32x4_t hu = *reinterpret_cast<const u32x4_t*>(so + s * kOutPitch + 256 + ch * 16);
         const int64_t col = tc.n_tile * 128 + ch * 8;
-        if (args.out != nullptr) {
+        if (!CKPT && args.out != nullptr) {
           uint16_t* h = args.out + row * (2 * I) + col;
           __builtin_nontemporal_store(hg, reinterpret_cast<u32x4_t*>(h));
           __builtin_nontemporal_store(hu, reinterpret_cast<u32x4_t*>(h + I));
@@ -236,12 +241,20 @@ __device__ __forceinline__ void fwd_epilogue(const FwdArgs& args, floatx16_t (&a
           a[w] = pack_bf16x2(bg0 * sigmoid_fast(bg0) * bu0, bg1 * sigmoid_fast(bg1) * bu1);
         }
         __builtin_nontemporal_store(a, reinterpret_cast<u32x4_t*>(args.act + row * I + col));
+        if constexpr (CKPT) {   // a block of 32 features is four lanes of one row
+          const int64_t chunk = (row * (2 * I) + col) >> 3;
+          uint32_t code[2];
+          uint32_t byte = mx_encode8<kMxFp8>(hg, code);
+          mx_store8<kMxFp8, true>(args.h_codes, args.h_scales, chunk, code, byte);
+          byte = mx_encode8<kMxFp8>(hu, code);
+          mx_store8<kMxFp8, true>(args.h_codes, args.h_scales, chunk + (I >> 3), code, byte);
+        }
       }
     }
   }
 }
 
-template <FwdMode MODE, bool GS>
+template <FwdMode MODE, bool GS, bool CKPT>
 __global__ void __launch_bounds__(kThreads, 2)
 fwd_gemm_kernel(FwdArgs args) {
   using L = FwdLds<GS>;
@@ -491,7 +504,7 @@ fwd_gemm_kernel(FwdArgs args) {
   if (tid < kBM) s_gx[tid] = gx_row;
   __syncthreads();   // s_gx visible; every wave is past its last read of the ring
 
-  fwd_epilogue<MODE>(args, acc, tc, s_gx, gw, lds);
+  fwd_epilogue<MODE, CKPT>(args, acc, tc, s_gx, gw, lds);
 }
 
 // ------------------------------------------------------------ MXFP4 recipe
@@ -524,7 +537,7 @@ static_assert(kOutRows * kOutPitch <= kMxStages * kMxStageBytes, "staging fits i
 
 __device__ __forceinline__ int mx_code_slot(int r, int c) { return c ^ ((r >> 2) & 3); }
 
-template <FwdMode MODE>
+template <FwdMode MODE, bool CKPT>
 __global__ void __launch_bounds__(kThreads, 2)
 fwd_mx_kernel(FwdArgs args) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
@@ -649,16 +662,16 @@ fwd_mx_kernel(FwdArgs args) {
   if (tid < kBM) s_gx[tid] = 1.0f;   // no outer scales: the epilogue's factors are 1
   __syncthreads();   // s_gx visible; every wave is past its last read of the ring
   const float gw[4] = {1.0f, 1.0f, 1.0f, 1.0f};
-  fwd_epilogue<MODE>(args, acc, tc, s_gx, gw, lds);
+  fwd_epilogue<MODE, CKPT>(args, acc, tc, s_gx, gw, lds);
 }
 
-template <FwdMode MODE>
+template <FwdMode MODE, bool CKPT = false>
 bool launch_fwd_mx(const FwdArgs& args, int n_tiles, const char* name, hipStream_t s) {
   static OncePerDevice lds;
-  if (!set_lds(lds, &fwd_mx_kernel<MODE>, kMxLdsBytes)) return launch_ok(name) && false;
+  if (!set_lds(lds, &fwd_mx_kernel<MODE, CKPT>, kMxLdsBytes)) return launch_ok(name) && false;
   const int64_t tiles = grouped_m_tiles_bound(args.rows_alloc, args.E, kBM) * n_tiles;
   if (tiles == 0) return true;
-  launch_kernel(name, fwd_mx_kernel<MODE>, dim3(xcd_grid(tiles)), dim3(kThreads), kMxLdsBytes, s, args);
+  launch_kernel(name, fwd_mx_kernel<MODE, CKPT>, dim3(xcd_grid(tiles)), dim3(kThreads), kMxLdsBytes, s, args);
   return launch_ok(name);
 }
 
@@ -886,57 +899,61 @@ bool launch_mx8(const Mx8Args& args, int64_t tiles, const char* name, hipStream_
   return launch_ok(name);
 }
 
-template <FwdMode MODE, bool GS>
+template <FwdMode MODE, bool GS, bool CKPT>
 bool launch_fwd_variant(const FwdArgs& args, int64_t tiles, const char* name, hipStream_t s) {
   static OncePerDevice lds;
-  if (!set_lds(lds, &fwd_gemm_kernel<MODE, GS>, FwdLds<GS>::kBytes)) return launch_ok(name) && false;
-  launch_kernel(name, fwd_gemm_kernel<MODE, GS>, dim3(xcd_grid(tiles)), dim3(kThreads), FwdLds<GS>::kBytes, s,
+  if (!set_lds(lds, &fwd_gemm_kernel<MODE, GS, CKPT>, FwdLds<GS>::kBytes)) return launch_ok(name) && false;
+  launch_kernel(name, fwd_gemm_kernel<MODE, GS, CKPT>, dim3(xcd_grid(tiles)), dim3(kThreads), FwdLds<GS>::kBytes, s,
                 args);
   return launch_ok(name);
 }
 
-template <FwdMode MODE>
+template <FwdMode MODE, bool CKPT = false>
 bool launch_fwd(const FwdArgs& args, int n_tiles, const char* name, hipStream_t s) {
   const int64_t tiles = grouped_m_tiles_bound(args.rows_alloc, args.E, kBM) * n_tiles;
   if (tiles == 0) return true;
   // codes arrive in pairs of 64-k stages: every caller's K (H, I, the dense
   // layer's K) is a multiple of 128, which the shape checks enforce
   if (args.K % (2 * kBK) != 0) return false;
-  if (args.K % (kGroup * kBK) == 0) return launch_fwd_variant<MODE, true>(args, tiles, name, s);
-  return launch_fwd_variant<MODE, false>(args, tiles, name, s);
+  if (args.K % (kGroup * kBK) == 0) return launch_fwd_variant<MODE, true, CKPT>(args, tiles, name, s);
+  return launch_fwd_variant<MODE, false, CKPT>(args, tiles, name, s);
 }
 
 }  // namespace
 
 bool launch_fc1(int64_t rows_alloc, int H, int I, int E, const int32_t* offsets, Fp4Operand x,
-                Fp4Operand w1, uint16_t* h_out, uint16_t* a_out, float* dbg_f32, hipStream_t s) {
-  FwdArgs args{rows_alloc, H, 2 * I, I, E, offsets, x, w1, h_out, a_out, dbg_f32};
+                Fp4Operand w1, uint16_t* h_out, uint16_t* a_out, float* dbg_f32, uint8_t* h_codes, uint8_t* h_scales,
+                hipStream_t s) {
+  FwdArgs args{rows_alloc, H, 2 * I, I, E, offsets, x, w1, h_out, a_out, dbg_f32, h_codes, h_scales};
+  if (h_codes != nullptr) return launch_fwd<FwdMode::FC1, true>(args, I / 128, "gemm_fc1", s);
   return launch_fwd<FwdMode::FC1>(args, I / 128, "gemm_fc1", s);
 }
 
 bool launch_fc2(int64_t rows_alloc, int H, int I, int E, const int32_t* offsets, Fp4Operand a,
                 Fp4Operand w2, uint16_t* o_out, hipStream_t s) {
-  FwdArgs args{rows_alloc, I, H, I, E, offsets, a, w2, o_out, nullptr, nullptr};
+  FwdArgs args{rows_alloc, I, H, I, E, offsets, a, w2, o_out, nullptr, nullptr, nullptr, nullptr};
   return launch_fwd<FwdMode::FC2>(args, H / kBN, "gemm_fc2", s);
 }
 
 bool launch_linear_fwd(int64_t T, int K, int N, const int32_t* offsets, Fp4Operand x, Fp4Operand w,
                        uint16_t* y, hipStream_t s) {
-  FwdArgs args{T, K, N, K, 1, offsets, x, w, y, nullptr, nullptr};
+  FwdArgs args{T, K, N, K, 1, offsets, x, w, y, nullptr, nullptr, nullptr, nullptr};
   return launch_fwd<FwdMode::FC2>(args, N / kBN, "gemm_linear", s);
 }
 
 bool launch_fc1_mx(int64_t rows_alloc, int H, int I, int E, const int32_t* offsets, Fp4Operand x,
-                   Fp4Operand w1, uint16_t* h_out, uint16_t* a_out, float* dbg_f32, hipStream_t s) {
+                   Fp4Operand w1, uint16_t* h_out, uint16_t* a_out, float* dbg_f32, uint8_t* h_codes,
+                   uint8_t* h_scales, hipStream_t s) {
   if (H % kMxBK) return false;
-  FwdArgs args{rows_alloc, H, 2 * I, I, E, offsets, x, w1, h_out, a_out, dbg_f32};
+  FwdArgs args{rows_alloc, H, 2 * I, I, E, offsets, x, w1, h_out, a_out, dbg_f32, h_codes, h_scales};
+  if (h_codes != nullptr) return launch_fwd_mx<FwdMode::FC1, true>(args, I / 128, "mx_gemm_fc1", s);
   return launch_fwd_mx<FwdMode::FC1>(args, I / 128, "mx_gemm_fc1", s);
 }
 
 bool launch_fc2_mx(int64_t rows_alloc, int H, int I, int E, const int32_t* offsets, Fp4Operand a,
                    Fp4Operand w2, uint16_t* o_out, hipStream_t s) {
   if (I % kMxBK) return false;
-  FwdArgs args{rows_alloc, I, H, I, E, offsets, a, w2, o_out, nullptr, nullptr};
+  FwdArgs args{rows_alloc, I, H, I, E, offsets, a, w2, o_out, nullptr, nullptr, nullptr, nullptr};
   return launch_fwd_mx<FwdMode::FC2>(args, H / kBN, "mx_gemm_fc2", s);
 }
 

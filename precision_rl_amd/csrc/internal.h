@@ -104,8 +104,10 @@ struct Fp4Operand {
 };
 
 // FC1 (SwiGLU fused into the epilogue): over expert groups, SwiGLU in the epilogue.
+// h_out, dbg_f32 and h in MXFP8 (h_codes, h_scales: in place of h_out) may be null.
 bool launch_fc1(int64_t rows_alloc, int H, int I, int E, const int32_t* offsets, Fp4Operand x,
-                Fp4Operand w1, uint16_t* h_out, uint16_t* a_out, float* dbg_f32, hipStream_t s);
+                Fp4Operand w1, uint16_t* h_out, uint16_t* a_out, float* dbg_f32, uint8_t* h_codes, uint8_t* h_scales,
+                hipStream_t s);
 
 // FC2 over expert groups.
 bool launch_fc2(int64_t rows_alloc, int H, int I, int E, const int32_t* offsets, Fp4Operand a,
@@ -114,7 +116,8 @@ bool launch_fc2(int64_t rows_alloc, int H, int I, int E, const int32_t* offsets,
 // MXFP4 FC1 / FC2 (scaled FP4 MFMA; operands' outer pointers unused).  The
 // reduction length (H for FC1, I for FC2) must be a multiple of 128.
 bool launch_fc1_mx(int64_t rows_alloc, int H, int I, int E, const int32_t* offsets, Fp4Operand x,
-                   Fp4Operand w1, uint16_t* h_out, uint16_t* a_out, float* dbg_f32, hipStream_t s);
+                   Fp4Operand w1, uint16_t* h_out, uint16_t* a_out, float* dbg_f32, uint8_t* h_codes, uint8_t* h_scales,
+                hipStream_t s);
 bool launch_fc2_mx(int64_t rows_alloc, int H, int I, int E, const int32_t* offsets, Fp4Operand a,
                    Fp4Operand w2, uint16_t* o_out, hipStream_t s);
 

@@ -84,10 +84,13 @@ __device__ __forceinline__ uint32_t mx_encode8(const u32x4_t& v, uint32_t (&c)[2
 
 // Stores the lane's codes and, from the quad's first lane, the scale byte of
 // the chunk with flat index `chunk` (8 elements each) of a dense [T, K] matrix.
-template <int FMT>
+// NT: E4M3 codes past the caches.
+template <int FMT, bool NT = false>
 __device__ __forceinline__ void mx_store8(uint8_t* codes, uint8_t* scales, int64_t chunk, const uint32_t (&c)[2],
                                           uint32_t byte) {
-  if constexpr (FMT == kMxFp8)
+  if constexpr (FMT == kMxFp8 && NT)
+    __builtin_nontemporal_store(u32x2_t{c[0], c[1]}, reinterpret_cast<u32x2_t*>(codes + chunk * 8));
+  else if constexpr (FMT == kMxFp8)
     *reinterpret_cast<u32x2_t*>(codes + chunk * 8) = u32x2_t{c[0], c[1]};
   else
     *reinterpret_cast<uint32_t*>(codes + chunk * 4) = c[0];

@@ -73,11 +73,7 @@ template <Keep KEEP>
 __device__ __forceinline__ void keep8(const SwigluArgs& a, const u32x4_t& v, int64_t chunk) {
   uint32_t code[2];
   const uint32_t byte = mx_encode8<kMxFp8>(v, code);
-  const u32x2_t c{code[0], code[1]};
-  u32x2_t* to = reinterpret_cast<u32x2_t*>(a.h_codes) + chunk;
-  if constexpr (KEEP == kKeepLines) __builtin_nontemporal_store(c, to);
-  else *to = c;
-  if ((chunk & 3) == 0) a.h_scales[chunk >> 2] = static_cast<uint8_t>(byte);
+  mx_store8<kMxFp8, KEEP == kKeepLines>(a.h_codes, a.h_scales, chunk, code, byte);
 }
 
 // NT: loads past the caches.  It and the outputs of the backward pass are chosen

@@ -179,3 +179,21 @@ def test_expert_backward_from_a_checkpoint(lib, at, change, status, says):
 def test_expert_backward_workspace_holds_a_beside_the_others(lib):
     size = lambda kind: lib.w4a4_workspace_size(kind, 64, 256, 128, 8, 2, 16)  # noqa: E731
     assert size(9) == size(2) + -(-(64 * 2 + 8 * 15) * 128 * 2 // 256) * 256
+
+
+FWD = ("T", "H", "I", "E", "k", "align", "xc", "xs", "xo", "offsets", "row_map", "src_row", "p", "w1c", "w1s", "w1o", "w2c",
+       "w2s", "w2o", "y", "hc", "hs", "o", "ws", "wsb")
+
+
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("change,status,says", [
+    (dict(T=-1), INVALID, "T=-1"), (dict(H=288), UNSUPPORTED, "256"), (dict(I=96), UNSUPPORTED, "128"),
+    (dict(hc=None), INVALID, "h_codes"), (dict(hs=None), INVALID, "h_scales"), (dict(hs="hs+8"), INVALID, "h_scales"),
+    (dict(o="o+8"), INVALID, "o is not"), (dict(y=None), INVALID, "y"), (dict(ws=None), WORKSPACE, "workspace"),
+    (dict(wsb=1 << 10), WORKSPACE, "workspace")])
+def test_expert_forward_that_keeps_a_checkpoint(lib, at, mx, change, status, says):
+    order = tuple(n for n in FWD if not mx or n not in ("xo", "w1o", "w2o"))
+    base = _base(order, T=4, H=256, I=128, E=8, k=2, align=1, wsb=1 << 30)
+    name = "w4a4_mx_grouped_expert_fwd_ckpt" if mx else "w4a4_grouped_expert_fwd_ckpt"
+    assert _status(lib, at, name, order, base, change) == status
+    assert says in lib.w4a4_last_error().decode()

@@ -83,6 +83,72 @@ def test_against_the_bf16_checkpoint(b):
         assert 0 < rel_l2(bf16_host(g[m]), bf16_host(r[m])) <= 0.125, m
 
 
+@pytest.mark.parametrize("T,H,E,k,I,align,mx,how", [
+    (200, 512, 12, 3, 256, 1, False, dict(routing="zipf", n_empty=2)), (333, 256, 5, 4, 384, 128, False, {}),
+    (1, 256, 4, 4, 128, 16, True, {}), (700, 1024, 16, 8, 640, 32, True, {}), (2048, 2048, 128, 8, 768, 1, False, {})])
+def test_forward_that_keeps_the_checkpoint(b, T, H, E, k, I, align, mx, how):  # noqa: E741
+    """Its y is the forward's, its checkpoint the row encoding of the forward's h,
+    its o what the combination weights; rows behind the last group are left."""
+    L = _layer(b, T, H, E, k, I, align, 3 * T + I, mx, **how)
+    n, cap, xq = int(L["xq"]["offsets"][-1]), L["cap"], L["xq"]
+    quant = b.quantize_weights_mx if mx else b.quantize_weights
+    w1q, w2q = quant(L["w1"]), quant(L["w2"])
+    print_case("expert_fwd_ckpt", T=T, H=H, E=E, k=k, I=I, align=align, mx=mx, rows=n)
+    out = dict(h_codes=torch.full((cap, 2 * I), 9, dtype=torch.uint8, device="cuda"),
+               h_scales=torch.full((cap, 2 * I // 32), 9, dtype=torch.uint8, device="cuda"),
+               o=torch.full((cap, H), 9.0, dtype=torch.bfloat16, device="cuda"))
+    f = b.w4a4_grouped_expert_fwd_ckpt(xq, L["p"], w1q, w2q, T, H, I, E, k, align, save_o=True, out=out)
+    fwd = b.w4a4_mx_grouped_expert_fwd if mx else b.w4a4_grouped_expert_fwd
+    assert torch.equal(f["y"], fwd(xq, L["p"], w1q, w2q, T, H, I, E, k, align)["y"])
+    for m in ("h_codes", "h_scales"):
+        assert torch.equal(f[m][:n], L["kept"][m][:n]) and bool((f[m][n:] == 9).all()), m
+    assert bool((f["o"][n:] == 9).all()) and torch.equal(b.w4a4_unpermute_fwd(f["o"], xq, L["p"]), f["y"])
+    alone = b.w4a4_grouped_expert_fwd_ckpt(xq, L["p"], w1q, w2q, T, H, I, E, k, align)
+    assert "o" not in alone and torch.equal(alone["y"], f["y"]) and torch.equal(alone["h_codes"][:n], f["h_codes"][:n])
+
+
+def test_training_step_of_a_layer(b):
+    """Forward that keeps 8 bits and o, backward of the experts and of the router's
+    weights: twice in one captured graph's replays and eagerly, the same bits; the
+    weights' gradient against differences of the oracle's combination."""
+    T, H, E, k, I = 300, 512, 10, 4, 256  # noqa: E741
+    L = _layer(b, T, H, E, k, I, 16, 21)
+    w1q, w2q, xq, p = b.quantize_weights(L["w1"]), b.quantize_weights(L["w2"]), L["xq"], L["p"]
+    cap = L["cap"]
+    print_case("ckpt_training_step", T=T, H=H, E=E, k=k, I=I)
+
+    def step():
+        f = b.w4a4_grouped_expert_fwd_ckpt(xq, p, w1q, w2q, T, H, I, E, k, 16, save_o=True)
+        g = b.w4a4_expert_bwd_ckpt(L["dy"], L["x"], L["w1"], L["w2"], f, p, xq, T, H, I, E, k, 16)
+        dp = b.w4a4_unpermute_bwd(L["dy"], f["o"], xq, p, do=False)["dtopk_w"]
+        return dict(y=f["y"], dp=dp, **g)
+
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        eager = step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for n in range(3):
+        L["dy"].mul_(0.5 + n)
+        with torch.cuda.stream(stream):
+            stream.wait_stream(torch.cuda.default_stream())
+            eager = step()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(got[m], eager[m]) for m in eager)
+    f = b.w4a4_grouped_expert_fwd_ckpt(xq, p, w1q, w2q, T, H, I, E, k, 16, save_o=True)
+    o, row, dy = bf16_host(f["o"]), xq["row_map"].cpu().numpy(), bf16_host(L["dy"])
+    o[int(xq["offsets"][-1]):] = 0.0
+    v = np.random.default_rng(1).standard_normal((T, k))
+    p64 = p.double().cpu().numpy()
+    diff = np.sum(dy * (dispatch.gather_sum(o, row, p64 + v)[0] - dispatch.gather_sum(o, row, p64)[0]))
+    _, _, mag = dispatch.unpermute_bwd(dy, o, row, p64)
+    assert abs(np.sum(got["dp"].double().cpu().numpy() * v) - diff) <= 17 * 2.0 ** -24 * 1.01 * np.sum(mag * np.abs(v))
+
+
 def test_rows_behind_the_last_are_not_read(b):
     """The checkpoint's rows past the last group hold NaN codes here (as
     _layer leaves them), and a second call with other bytes there gives the same."""
