@@ -457,30 +457,31 @@ __device__ __forceinline__ void clear_pad_rows(const UnpermuteBwdArgs& a, int e)
     if (a.src_row[r] < 0) clear_row(a.d_o, r, a.chunks);
 }
 
-// One wave: do[r] = w[i] dy[t] and dp[i] = <dy[t], o[r]> of entry i = t k + j.
-// Lane l takes the chunks l, l + 64, ... in order (four in flight), each summed by
-// itself, the lanes join by halves: dp's bits depend on the row's length and type alone.
-template <typename T, bool NT>
+// LANES lanes: do[r] = w[i] dy[t] and dp[i] = <dy[t], o[r]> of entry i = t k + j.
+// Lane l takes the chunks l, l + LANES, ... in order (four in flight), each summed
+// by itself, the lanes join by halves: dp's bits depend on the row's length and
+// type alone.
+template <typename T, int LANES, bool NT>
 __device__ __forceinline__ void entry_grad(const UnpermuteBwdArgs& a, int64_t t, int64_t i, uint32_t r) {
   constexpr int N = Chunk<T>::N, kAhead = 4;
-  const int lane = threadIdx.x % kWave;
+  const int lane = threadIdx.x % LANES;
   const u32x4_t* dy = reinterpret_cast<const u32x4_t*>(static_cast<const uint8_t*>(a.dy) + t * a.dy_pitch);
   const u32x4_t* o = static_cast<const u32x4_t*>(a.o) + static_cast<int64_t>(r) * a.chunks;
   u32x4_t* d_o = static_cast<u32x4_t*>(a.d_o) + static_cast<int64_t>(r) * a.chunks;
   const float w = a.w[i];
   float sum = 0.0f;
-  for (int c0 = lane; c0 < a.chunks; c0 += kAhead * kWave) {
+  for (int c0 = lane; c0 < a.chunks; c0 += kAhead * LANES) {
     Chunk<T> g[kAhead], v[kAhead];
 #pragma unroll
     for (int n = 0; n < kAhead; ++n) {
-      const int c = c0 + n * kWave;
+      const int c = c0 + n * LANES;
       if (c >= a.chunks) continue;
       v[n].w = load16<NT>(o + c);
       g[n].w = dy[c];
     }
 #pragma unroll
     for (int n = 0; n < kAhead; ++n) {
-      const int c = c0 + n * kWave;
+      const int c = c0 + n * LANES;
       if (c >= a.chunks) continue;
       if (a.d_o != nullptr) store_scaled<T>(g[n], w, d_o + c);
       float part = g[n].get(0) * v[n].get(0);
@@ -490,12 +491,12 @@ __device__ __forceinline__ void entry_grad(const UnpermuteBwdArgs& a, int64_t t,
     }
   }
 #pragma unroll
-  for (int off = kWave / 2; off > 0; off >>= 1) sum += __shfl_xor(sum, off, kWave);
+  for (int off = LANES / 2; off > 0; off >>= 1) sum += __shfl_xor(sum, off, kWave);
   if (lane == 0) a.dw[i] = sum;
 }
 
-// A wave per entry; pad rows by workgroups of their own.
-template <typename T, bool NT>
+// LANES lanes per entry; pad rows by workgroups of their own.
+template <typename T, int LANES, bool NT>
 __global__ void __launch_bounds__(kThreads)
 unpermute_bwd_entries_kernel(UnpermuteBwdArgs a) {
   const int64_t block = a.first + blockIdx.x;
@@ -503,11 +504,13 @@ unpermute_bwd_entries_kernel(UnpermuteBwdArgs a) {
     clear_pad_rows(a, static_cast<int>(block - a.main_blocks));
     return;
   }
-  const int64_t i = block * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  int slot = threadIdx.x / LANES;
+  if constexpr (LANES == kWave) slot = __builtin_amdgcn_readfirstlane(slot);
+  const int64_t i = block * (kThreads / LANES) + slot;
   if (i >= a.T * a.k) return;
   const uint32_t r = static_cast<uint32_t>(a.row_map[i]);
-  if (r < used_rows(a)) entry_grad<T, NT>(a, i / a.k, i, r);
-  else if (threadIdx.x % kWave == 0) a.dw[i] = 0.0f;
+  if (r < used_rows(a)) entry_grad<T, LANES, NT>(a, i / a.k, i, r);
+  else if (threadIdx.x % LANES == 0) a.dw[i] = 0.0f;
 }
 
 // do alone: a workgroup per token, dy read once.
@@ -644,13 +647,25 @@ bool launch_unpermute_bwd(int64_t T, int H, int k, int E, int64_t rows, bool f32
     else go(T, pad_blocks, unpermute_bwd_scatter_kernel<uint16_t>);
     return launch_ok("unpermute_bwd");
   }
-  const int64_t entry_blocks = (T * k + kWaves - 1) / kWaves;
-  auto entries = [&](auto nt) {
-    if (f32) go(entry_blocks, pad_blocks, unpermute_bwd_entries_kernel<float, decltype(nt)::value>);
-    else go(entry_blocks, pad_blocks, unpermute_bwd_entries_kernel<uint16_t, decltype(nt)::value>);
+  // Four chunks a lane in flight where the row has as many: 16384 tokens of 128 37
+  // us with a wave to an entry, 14 with 16 lanes; 256 39 and 24, 512 62 and 53; 640
+  // 75 and with 32 lanes 66, 768 81 and 78, 1024 103 and 105.
+  auto entries = [&](auto elem, auto lanes, auto nt) {
+    constexpr int LANES = decltype(lanes)::value, kEntries = kThreads / LANES;
+    go((T * k + kEntries - 1) / kEntries, pad_blocks,
+       unpermute_bwd_entries_kernel<decltype(elem), LANES, decltype(nt)::value>);
   };
-  if (streams(T * k * row_bytes * (d_o != nullptr ? 2 : 1))) entries(std::true_type{});
-  else entries(std::false_type{});
+  auto shape = [&](auto elem, auto nt) {
+    if (a.chunks <= 64) entries(elem, std::integral_constant<int, 16>{}, nt);
+    else if (a.chunks < 128) entries(elem, std::integral_constant<int, 32>{}, nt);
+    else entries(elem, std::integral_constant<int, kWave>{}, nt);
+  };
+  auto types = [&](auto nt) {
+    if (f32) shape(float{}, nt);
+    else shape(uint16_t{}, nt);
+  };
+  if (streams(T * k * row_bytes * (d_o != nullptr ? 2 : 1))) types(std::true_type{});
+  else types(std::false_type{});
   return launch_ok("unpermute_bwd");
 }
 

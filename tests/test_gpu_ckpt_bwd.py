@@ -146,7 +146,7 @@ def test_training_step_of_a_layer(b):
     p64 = p.double().cpu().numpy()
     diff = np.sum(dy * (dispatch.gather_sum(o, row, p64 + v)[0] - dispatch.gather_sum(o, row, p64)[0]))
     _, _, mag = dispatch.unpermute_bwd(dy, o, row, p64)
-    assert abs(np.sum(got["dp"].double().cpu().numpy() * v) - diff) <= 17 * 2.0 ** -24 * 1.01 * np.sum(mag * np.abs(v))
+    assert abs(np.sum(got["dp"].double().cpu().numpy() * v) - diff) <= 18 * 2.0 ** -24 * 1.01 * np.sum(mag * np.abs(v))
 
 
 def test_rows_behind_the_last_are_not_read(b):

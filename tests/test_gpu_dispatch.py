@@ -7,9 +7,9 @@ float32, relative to the value):
   dx, y   at most 8 roundings of FP32, each at most u of the partial sums, which
           the magnitudes' sum bounds: 8 u sum|.|, times the final rounding.
   do      one product: u, and the rounding.
-  dp      a lane adds a 16-byte chunk's products one by one and then its chunks (64
-          lanes), 6 steps join the lanes: (products a chunk + chunks a lane + 6) u
-          sum|dy o|.
+  dp      a lane adds a 16-byte chunk's products one by one and then its chunks (16
+          lanes up to 64 chunks, 32 below 128, else 64), at most 6 steps join the
+          lanes: (products a chunk + chunks a lane + 6) u sum|dy o|.
 """
 import numpy as np
 import pytest
@@ -136,7 +136,7 @@ def test_unpermute_gradient(b, T, k, H, E, align, how, dtype):
     assert np.array_equal(got[n:], do[n:]) and not np.any(got[:n][src < 0])
     assert np.all(np.abs(got - do) <= (_step(dt) + U) * (1 + U) * np.abs(do) + TINY)
     chunks = H * o.element_size() // 16
-    steps = 16 // o.element_size() + -(-chunks // 64) + 6
+    steps = 16 // o.element_size() + -(-chunks // (16 if chunks <= 64 else 32 if chunks < 128 else 64)) + 6
     assert np.all(np.abs(_f64(r["dtopk_w"]) - dp) <= steps * U * (1 + 2.0 ** -10) * mag)
     alone = b.w4a4_unpermute_bwd(dy, o, perm, w, do=False)
     assert torch.equal(alone["dtopk_w"], r["dtopk_w"]) and "do" not in alone
@@ -429,7 +429,7 @@ def test_around_the_expert_calls(b):
     assert torch.equal(b.w4a4_permute_bwd(gr["dx"], perm), g["dx"])
     assert torch.equal(gr["dw1"], g["dw1"]) and torch.equal(gr["dw2"], g["dw2"])
     _, dp, mag = dispatch.unpermute_bwd(bf16_host(dy), bf16_host(fr["y"]), perm["row_map"].cpu().numpy(), _f64(p))
-    assert np.all(np.abs(_f64(back["dtopk_w"]) - dp) <= 15 * U * 1.01 * mag)
+    assert np.all(np.abs(_f64(back["dtopk_w"]) - dp) <= 18 * U * 1.01 * mag)
 
 
 def test_experts_of_two_ranks(b):
