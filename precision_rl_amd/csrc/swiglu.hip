@@ -143,8 +143,10 @@ swiglu_bwd_kernel(SwigluArgs a) {
     unpack8(d, da);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      dg[i] = da[i] * up[i] * s[i] * (1.0f + gate[i] * (1.0f - s[i]));
-      du[i] = da[i] * gate[i] * s[i];
+      // products from the bounded factor outwards: da * up or da * gate alone can
+      // pass the range where the result is 0
+      dg[i] = da[i] * (up[i] * (s[i] * (1.0f + gate[i] * (1.0f - s[i]))));
+      du[i] = da[i] * (gate[i] * s[i]);
     }
     u32x4_t* dh = reinterpret_cast<u32x4_t*>(a.dh) + hat;
     __builtin_nontemporal_store(pack8(dg), dh);

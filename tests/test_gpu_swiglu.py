@@ -193,6 +193,20 @@ def test_special_values(b):
     _check_dh(g["dh"], bf16_host(da[:1]), bf16_host(h[:1]))
 
 
+def test_factors_whose_product_passes_the_range(b):
+    """da up and da gate beyond 2^128 where the sigmoid is 0 or the result moderate."""
+    I = 32  # noqa: E741
+    h = torch.zeros(1, 2 * I, dtype=torch.bfloat16, device="cuda")
+    h[0, :4] = torch.tensor([-1000.0, -1.0e30, -2.0, 2.0])
+    h[0, I:I + 4] = torch.tensor([1.0e30, 1.0e30, 1.0e30, 1.0e-30])
+    da = torch.zeros(1, I, dtype=torch.bfloat16, device="cuda")
+    da[0, :4] = torch.tensor([1.0e30, 1.0e30, 1.0e-20, 1.0e30])
+    print_case("swiglu_range", I=I)
+    dh = b.w4a4_swiglu_bwd(da, h)["dh"]
+    assert bool(torch.isfinite(dh).all()) and not dh[0, :2].any() and not dh[0, I:I + 2].any()
+    _check_dh(dh[:, [2, 3, I + 2, I + 3]], bf16_host(da[:, 2:4]), bf16_host(h[:, [2, 3, I + 2, I + 3]]))
+
+
 def test_smallest_scales(b):
     """Blocks near the bottom of the format: scale bytes 0 and 1, subnormal bf16."""
     I = 32  # noqa: E741
