@@ -634,7 +634,7 @@ def summarize(kern, ms, steps, fl, by, concurrent=None):
     return per_kernel, roof
 
 
-def moe_buffers(torch, dev, b, T, H, E, k, I, A, mx, mx8):
+def moe_buffers(torch, dev, b, T, H, E, k, I, A, mx, mx8, keep8=False):
     """Preallocated outputs and workspaces of one quantize+permute + forward
     (+ backward) of a MoE layer."""
     cap = b.rows_capacity(T, k, E, A)
@@ -645,26 +645,43 @@ def moe_buffers(torch, dev, b, T, H, E, k, I, A, mx, mx8):
               src_row=torch.empty(cap, dtype=torch.int32, device=dev))
     if not mx:
         xq["outer"] = torch.empty(cap, dtype=torch.float32, device=dev)
+    if keep8:
+        saved = dict(h_codes=torch.empty(cap, 2 * I, dtype=torch.uint8, device=dev),
+                     h_scales=torch.empty(cap, 2 * I // 32, dtype=torch.uint8, device=dev))
+    else:
+        saved = dict(h=torch.empty(cap, 2 * I, dtype=torch.bfloat16, device=dev),
+                     a=torch.empty(cap, I, dtype=torch.bfloat16, device=dev))
+    bwd = b.WS_MX8_BACKWARD if mx8 else b.WS_BACKWARD_CKPT if keep8 else b.WS_BACKWARD
     return dict(
         xq=xq,
         ws_qp=torch.empty(b.workspace_size(b.WS_QUANTIZE_PERMUTE, T, H, I, E, k, A) + 256,
                           dtype=torch.uint8, device=dev),
         ws_f=torch.empty(b.workspace_size(b.WS_FORWARD, T, H, I, E, k, A), dtype=torch.uint8, device=dev),
-        ws_b=torch.empty(b.workspace_size(b.WS_MX8_BACKWARD if mx8 else b.WS_BACKWARD, T, H, I, E, k, A),
-                         dtype=torch.uint8, device=dev),
+        ws_b=torch.empty(b.workspace_size(bwd, T, H, I, E, k, A), dtype=torch.uint8, device=dev),
         y=torch.empty(T, H, dtype=torch.bfloat16, device=dev),
-        saved=dict(h=torch.empty(cap, 2 * I, dtype=torch.bfloat16, device=dev),
-                   a=torch.empty(cap, I, dtype=torch.bfloat16, device=dev)),
+        saved=saved,
         grads=dict(dx=torch.empty(T, H, dtype=torch.bfloat16, device=dev),
                    dw1=torch.empty(E, 2 * I, H, dtype=torch.bfloat16, device=dev),
                    dw2=torch.empty(E, H, I, dtype=torch.bfloat16, device=dev)))
 
 
 def moe_step(b, bufs, x, idx, p, w1q, w2q, w1, w2, dy, T, H, E, k, I, A, mx=False, mx8=False,
-             backward=True):
+             backward=True, keep8=False):
     """One pass of the hot path: quantize+permute, the grouped expert forward
-    (saving h and a) and, with `backward`, the straight-through backward."""
+    (saving h and a, or with `keep8` h in MXFP8) and, with `backward`, the
+    straight-through backward."""
     xq, saved, grads = bufs["xq"], bufs["saved"], bufs["grads"]
+    if keep8:
+        out = dict(saved, y=bufs["y"])
+
+        def step():
+            if mx:
+                b.w4a4_mx_quantize_permute(x, idx, E, A, out=xq, workspace=bufs["ws_qp"])
+            else:
+                b.w4a4_quantize_permute(x, idx, E, A, out=xq, workspace=bufs["ws_qp"])
+            b.w4a4_grouped_expert_fwd_ckpt(xq, p, w1q, w2q, T, H, I, E, k, A, out=out, workspace=bufs["ws_f"])
+            b.w4a4_expert_bwd_ckpt(dy, x, w1, w2, saved, p, xq, T, H, I, E, k, A, out=grads, workspace=bufs["ws_b"])
+        return step
 
     def step():
         if mx:
@@ -779,6 +796,9 @@ def main():
                     help="learner: the straight-through backward's GEMM operands -- bf16 (the "
                          "default) or mxfp8 (E4M3 + E8M0 per 32 along each GEMM's reduction axis, "
                          "scaled FP8 MFMA; routes with row_align 128)")
+    ap.add_argument("--keep", choices=["bf16", "mxfp8"], default="bf16",
+                    help="learner: what the forward keeps for the bf16 backward -- h and a in bf16 "
+                         "(the default) or h in MXFP8, from which the backward makes both")
     ap.add_argument("--recipe", choices=["nvfp4", "mxfp4", "mxfp8"], default="nvfp4",
                     help="the forward's format -- nvfp4 (E4M3 per 16 + FP32 outer "
                          "scales, exact f16 decode, the default) or mxfp4 (E8M0 per 32, scaled "
@@ -787,6 +807,9 @@ def main():
     args = ap.parse_args()
     if args.recipe == "mxfp8" and args.workload != "linear":
         ap.error("--recipe mxfp8 is a recipe of --workload linear")
+    keep8 = args.keep == "mxfp8"
+    if keep8 and (args.workload != "learner" or args.bwd != "bf16"):
+        ap.error("--keep mxfp8 is for --workload learner with --bwd bf16")
     if args.gpus != 1:
         print(f"bench.py: the benchmark runs on one GPU only (asked for --gpus {args.gpus}); "
               "the library's expert path is single-GPU (sharding is described in the design notes).",
@@ -819,8 +842,8 @@ def main():
     else:
         w1q, w2q = b.quantize_weights(w1), b.quantize_weights(w2)         # offline, untimed
 
-    bufs = moe_buffers(torch, dev, b, T, H, E, k, I, A, mx, mx8)
-    step = moe_step(b, bufs, x, idx, p, w1q, w2q, w1, w2, dy, T, H, E, k, I, A, mx=mx, mx8=mx8)
+    bufs = moe_buffers(torch, dev, b, T, H, E, k, I, A, mx, mx8, keep8)
+    step = moe_step(b, bufs, x, idx, p, w1q, w2q, w1, w2, dy, T, H, E, k, I, A, mx=mx, mx8=mx8, keep8=keep8)
     calibration_copy(torch, dev)
     flush = Flusher(torch, dev)
 
@@ -848,7 +871,8 @@ def main():
         "data": "synthetic (seeded; random-init weights of the layer's shape)",
         "config": {"workload": f"{WORKLOAD}: quantize+permute + grouped expert fwd + "
                                + ("MXFP8" if mx8 else "BF16") + " STE bwd"
-                               + (" (MXFP4 recipe: E2M1 + E8M0 per 32)" if mx else ""),
+                               + (" (MXFP4 recipe: E2M1 + E8M0 per 32)" if mx else "")
+                               + (", h kept in MXFP8" if keep8 else ""),
                    "T": T, "H": H, "E": E, "top_k": k, "I": I, "row_align": A,
                    "routing": w.routing},
         "timing": dict(time_fields(st, args.steps), flush_bytes=FLUSH_BYTES,
@@ -861,7 +885,7 @@ def main():
         "gemm_frac_mfma": gemm_fracs(per_kernel),
         "kernels": per_kernel,
     }
-    if not args.no_secondary and not mx and not mx8:
+    if not args.no_secondary and not mx and not mx8 and not keep8:
         out["configs"] = secondary_configs(b, torch, dev, args, flush, (w1q, w2q, w1, w2))
     if not args.no_cpu_baseline:
         print("[bench] timing the FP64 oracle on the host", file=sys.stderr, flush=True)
