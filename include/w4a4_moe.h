@@ -29,9 +29,10 @@
  *    do not depend on the other tokens of the batch (per-token scale domain).
  *  - Calls are thread-safe; concurrent calls on different streams need
  *    different workspaces.
- *  - w4a4_expert_bwd runs two of its kernels (the wgrad tile schedule and the
- *    copy of x to the expert rows) on a second stream of the current device
- *    (one per device, created on first use, default priority), forked from
+ *  - w4a4_expert_bwd and w4a4_expert_bwd_ckpt run two of their kernels (the
+ *    wgrad tile schedule and the copy of x to the expert rows) on a second
+ *    stream of the current device (one per device, created on first use,
+ *    default priority), forked from
  *    `stream` and joined back into it before the call's last kernels: work
  *    enqueued on `stream` after the call sees every output.  Each host
  *    thread forks and joins with events of its own, so concurrent calls from

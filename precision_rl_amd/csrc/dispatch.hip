@@ -31,8 +31,6 @@
 namespace w4a4 {
 namespace {
 
-typedef float floatx4_t __attribute__((ext_vector_type(4)));
-
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
 constexpr int kMaxK = 8;
@@ -202,20 +200,7 @@ struct PermuteArgs {
   int32_t *offsets, *row_map, *src_row;
   const int32_t *counts, *expert_count;
   int64_t token_blocks, first;         // workgroups of tokens (those of pad rows follow); this launch's first
-  bool stream;                         // x past the caches
 };
-
-// NT: past the caches.  A choice at run time around each load keeps the loads of
-// a lane from being in flight together (the combination below took 110 us with
-// it, 102 without): kernels with several are built both ways.
-template <bool NT>
-__device__ __forceinline__ u32x4_t load16(const u32x4_t* p) {
-  if constexpr (NT) return __builtin_nontemporal_load(p);
-  else return *p;
-}
-__device__ __forceinline__ u32x4_t load16(const u32x4_t* p, bool stream) {
-  return stream ? load16<true>(p) : load16<false>(p);
-}
 
 // Zeros in the pad rows of an expert whose group's pad rows are [r0, r1).
 template <int THREADS>
@@ -232,7 +217,7 @@ __device__ __forceinline__ void clear_pad_rows(const PermuteArgs& a, int r0, int
 __device__ __forceinline__ u32x4_t first_chunk(const PermuteArgs& a, int64_t t, int lane) {
   u32x4_t v{0u, 0u, 0u, 0u};
   if (a.xp != nullptr && t < a.T && lane < a.chunks)
-    v = load16(reinterpret_cast<const u32x4_t*>(a.x + t * a.x_pitch) + lane, a.stream);
+    v = reinterpret_cast<const u32x4_t*>(a.x + t * a.x_pitch)[lane];
   return v;
 }
 template <int TEAM>
@@ -240,7 +225,7 @@ __device__ __forceinline__ void copy_token(const PermuteArgs& a, int64_t t, int 
   const u32x4_t* src = reinterpret_cast<const u32x4_t*>(a.x + t * a.x_pitch);
   u32x4_t* dst = reinterpret_cast<u32x4_t*>(a.xp);
   for (int c = lane; c < a.chunks; c += TEAM) {
-    if (c != lane) v = load16(src + c, a.stream);
+    if (c != lane) v = src[c];
     for (int j = 0; j < a.k; ++j) {
       const int r = rows[j];
       if (r >= 0) __builtin_nontemporal_store(v, dst + static_cast<int64_t>(r) * a.chunks + c);
@@ -360,6 +345,18 @@ clear_offsets_kernel(int32_t* offsets, int n) {
 }
 
 // ------------------------------------------------------------ back to tokens
+// NT: expert rows loaded past the caches, where streams() says so of their bytes:
+// 16384 tokens of 2048 with 8 experts each combined in 102 us against 110, 2048 of
+// them in 14.4 against 13.1; the gradients 208 against 221, 28 against 24.  A
+// choice at run time around each load keeps a lane's loads from being in flight
+// together (110 us for 102), so both kernels are built both ways.  Tokens' rows
+// are loaded through the caches: past them the sort takes as long (110 us).
+template <bool NT>
+__device__ __forceinline__ u32x4_t load16(const u32x4_t* p) {
+  if constexpr (NT) return __builtin_nontemporal_load(p);
+  else return *p;
+}
+
 struct GatherArgs {
   int64_t T;
   int chunks, k;
@@ -380,7 +377,8 @@ __global__ void __launch_bounds__(kThreads)
 gather_rows_kernel(GatherArgs a) {
   constexpr int N = Chunk<T>::N;
   const int64_t base = (a.first + blockIdx.x) * kThreads, t0 = base / a.chunks;
-  const uint32_t i = static_cast<uint32_t>(base - t0 * a.chunks) + threadIdx.x;   // below chunks + 256: magic divides exactly
+  // below chunks + 256, where magic divides exactly
+  const uint32_t i = static_cast<uint32_t>(base - t0 * a.chunks) + threadIdx.x;
   const uint32_t q = a.chunks > 1 ? __umulhi(i, a.magic) : i;
   const int64_t t = t0 + q;
   const int c = static_cast<int>(i - q * a.chunks);
@@ -419,14 +417,13 @@ struct UnpermuteBwdArgs {
   uint32_t rows;
   const void* dy;
   int64_t dy_pitch;           // bytes
-  const void* o;              // null: no dp
+  const void* o;
   const int32_t* row_map;
   const float* w;
   const int32_t *offsets, *src_row;   // offsets may be null where no group can be padded
   void* d_o;                  // null: dp alone
-  float* dw;
+  float* dw;                  // null: do alone
   int64_t main_blocks, first; // workgroups of entries or tokens (those of pad rows follow); this launch's first
-  bool stream;                // do alone: dy past the caches
 };
 
 // Rows in use: entries of row_map at or past this are not dispatched.
@@ -452,7 +449,8 @@ __device__ __forceinline__ void clear_row(void* rows, int64_t r, int chunks) {
 
 // Pad rows of expert e: up to 127 rows before its group's end with src_row -1.
 __device__ __forceinline__ void clear_pad_rows(const UnpermuteBwdArgs& a, int e) {
-  const int64_t lo = max(a.offsets[e], 0), hi = min(static_cast<int64_t>(a.offsets[e + 1]), static_cast<int64_t>(a.rows));
+  const int64_t lo = max(a.offsets[e], 0);
+  const int64_t hi = min(static_cast<int64_t>(a.offsets[e + 1]), static_cast<int64_t>(a.rows));
   for (int64_t r = max(lo, hi - 127) + threadIdx.x / kWave; r < hi; r += kWaves)
     if (a.src_row[r] < 0) clear_row(a.d_o, r, a.chunks);
 }
@@ -526,7 +524,7 @@ unpermute_bwd_scatter_kernel(UnpermuteBwdArgs a) {
   const u32x4_t* dy = reinterpret_cast<const u32x4_t*>(static_cast<const uint8_t*>(a.dy) + t * a.dy_pitch);
   for (int c = threadIdx.x; c < a.chunks; c += kThreads) {
     Chunk<T> g;
-    g.w = load16(dy + c, a.stream);
+    g.w = dy[c];
     for (int j = 0; j < a.k; ++j) {
       const uint32_t r = static_cast<uint32_t>(a.row_map[t * a.k + j]);
       if (r < used)
@@ -534,10 +532,6 @@ unpermute_bwd_scatter_kernel(UnpermuteBwdArgs a) {
     }
   }
 }
-
-// Whether loads of so many bytes go past the 256 MiB memory-side cache, which
-// cannot hold them all from their producer.
-bool streams(double bytes) { return bytes > 0.75 * 256 * 1024 * 1024; }
 
 template <class F>
 void with_slots(int k, F f) {
@@ -561,8 +555,7 @@ bool launch_permute(int64_t T, int row_bytes, int k, int E, int row_align, const
     return launch_ok("permute_rows");
   }
   PermuteArgs a{T, row_bytes / 16, k, E, row_align, static_cast<const uint8_t*>(x), x_pitch, topk_idx,
-                static_cast<uint8_t*>(xp), offsets, row_map, src_row, nullptr, nullptr, T, 0,
-                streams(static_cast<double>(T) * row_bytes)};
+                static_cast<uint8_t*>(xp), offsets, row_map, src_row, nullptr, nullptr, T, 0};
   const int pad_blocks = row_align > 1 ? E : 0;
   if (one_launch(T, k)) {
     auto few = [&](auto threads, auto tokens) {
@@ -596,7 +589,8 @@ bool launch_permute(int64_t T, int row_bytes, int k, int E, int row_align, const
                     a);
     });
   };
-  // lanes per token
+  // Lanes per token.  (16384 tokens in bf16 take 17 us with rows of 128, 36 with
+  // 512, 86 with 1536.)
   if (a.chunks <= 16) rows(std::integral_constant<int, 16>{});
   else if (a.chunks <= 128) rows(std::integral_constant<int, kWave>{});
   else rows(std::integral_constant<int, kThreads>{});
@@ -630,7 +624,7 @@ bool launch_unpermute_bwd(int64_t T, int H, int k, int E, int64_t rows, bool f32
                           const int32_t* src_row, void* d_o, float* dw, hipStream_t s) {
   if (T == 0) return true;
   UnpermuteBwdArgs a{T, H / (f32 ? 4 : 8), k, E, static_cast<uint32_t>(rows), dy, dy_pitch, o, row_map, w,
-                     E > 0 ? offsets : nullptr, src_row, d_o, dw, 0, 0, false};
+                     E > 0 ? offsets : nullptr, src_row, d_o, dw, 0, 0};
   const double row_bytes = 16.0 * a.chunks;
   auto go = [&](int64_t main_blocks, int64_t others, auto kernel) {
     a.main_blocks = main_blocks;
@@ -642,7 +636,6 @@ bool launch_unpermute_bwd(int64_t T, int H, int k, int E, int64_t rows, bool f32
   // as many rows as slots: no group has been padded
   const int pad_blocks = d_o != nullptr && rows > T * k ? E : 0;
   if (dw == nullptr) {
-    a.stream = streams(T * row_bytes);
     if (f32) go(T, pad_blocks, unpermute_bwd_scatter_kernel<float>);
     else go(T, pad_blocks, unpermute_bwd_scatter_kernel<uint16_t>);
     return launch_ok("unpermute_bwd");

@@ -48,6 +48,14 @@ inline bool set_lds(OncePerDevice& done, Kern kernel, int bytes) {
 // Compute units of the current device (queried once).
 int device_cu_count();
 
+// Whether a call's loads are non-temporal: where it moves more than three
+// quarters of the 256 MiB memory-side cache, its inputs cannot all still lie
+// there, and loads that leave the cache alone are faster (the pre-norm's 16384
+// rows of 2048, forward with FP8 codes, 236 MB: 46.7 us against 49.0, backward,
+// 268 MB: 50.8 against 53.6); below, they would miss what the producer left
+// (2000 rows of 8192, 115 MB: 28 against 22).
+inline bool streams(double bytes) { return bytes > 0.75 * 256 * 1024 * 1024; }
+
 // ------------------------------------------------------------ routing / quant
 constexpr int kRouteChunk = 256;      // tokens per routing chunk (one workgroup)
 constexpr int kMaxRouteK = 8;         // largest k the routing kernels take

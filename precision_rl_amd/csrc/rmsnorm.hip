@@ -43,14 +43,6 @@ constexpr int kFewRows = 512;
 // row at every T).
 constexpr int kSpreadRows = 2048, kSpreadBwdRows = 256;
 
-// Whether a call's loads are non-temporal: where it moves more than three
-// quarters of the 256 MiB memory-side cache, its inputs cannot all still lie
-// there, and loads that leave the cache alone are faster (16384 rows of 2048,
-// forward with FP8 codes, 236 MB: 46.7 us against 49.0, backward, 268 MB: 50.8
-// against 53.6); below, they would miss what the producer left (2000 rows of
-// 8192, 115 MB: 28 against 22).
-bool streams(double bytes) { return bytes > 0.75 * 256 * 1024 * 1024; }
-
 // 8 consecutive elements as floats.  Stores are non-temporal (no output is
 // read again by its call): 16384 rows of 2048 with all outputs 66 to 63 us,
 // 2000 rows of 8192 38 to 25.

@@ -12,7 +12,9 @@
 //
 // Everything is element by element but the blocks' maxima, which a quad of
 // lanes finds among itself: HBM binds the calls of many rows, latency those of
-// few.
+// few.  131072 rows of 768 take 133 us with the checkpoint (6.1 TB/s; a linear
+// copy reaches 6.5), 94 without, 160 backward (6.3); 5001 rows of 2048 16
+// backward; 8 rows 2.1 on the device.
 
 #include <algorithm>
 #include <type_traits>
@@ -51,7 +53,8 @@ __device__ __forceinline__ bool place(const SwigluArgs& a, Place& p) {
   const int chunks = a.I / 8;
   const int64_t T = a.rows != nullptr ? min(a.T, static_cast<int64_t>(max(*a.rows, 0))) : a.T;
   const int64_t base = (a.first + blockIdx.x) * kThreads, row0 = base / chunks;
-  const uint32_t i = static_cast<uint32_t>(base - row0 * chunks) + threadIdx.x;   // below chunks + 256: magic divides exactly
+  // below chunks + 256, where magic divides exactly
+  const uint32_t i = static_cast<uint32_t>(base - row0 * chunks) + threadIdx.x;
   const uint32_t q = chunks > 1 ? __umulhi(i, a.magic) : i;
   p.row = row0 + q;
   p.col = static_cast<int>(i - q * chunks);
@@ -76,9 +79,10 @@ __device__ __forceinline__ void keep8(const SwigluArgs& a, const u32x4_t& v, int
   mx_store8<kMxFp8, KEEP == kKeepLines>(a.h_codes, a.h_scales, chunk, code, byte);
 }
 
-// NT: loads past the caches.  It and the outputs of the backward pass are chosen
-// outside the kernels: branches around single loads and stores took 142 us where
-// this takes 133 (131072 rows of 768 with the checkpoint), 168 for 160 backward.
+// NT: loads past the caches (131072 rows of 768 with the checkpoint 134 us against
+// 140, 8192 11.6 against 10.2; backward 160 against 165, 12.4 against 10.8).  It
+// and the outputs of the backward pass are chosen outside the kernels: branches
+// around single loads and stores took 142 us for 133, and 168 for 160 backward.
 template <int FMT, Keep KEEP, bool NT>
 __global__ void __launch_bounds__(kThreads)
 swiglu_fwd_kernel(SwigluArgs a) {
@@ -120,7 +124,8 @@ swiglu_bwd_kernel(SwigluArgs a) {
   float gate[8], up[8], s[8];
   if constexpr (CKPT) {
     const u32x2_t* c = reinterpret_cast<const u32x2_t*>(a.h_codes) + hat;
-    const u32x2_t g = NT ? __builtin_nontemporal_load(c) : *c, v = NT ? __builtin_nontemporal_load(c + chunks) : c[chunks];
+    const u32x2_t g = NT ? __builtin_nontemporal_load(c) : *c;
+    const u32x2_t v = NT ? __builtin_nontemporal_load(c + chunks) : c[chunks];
     const uint32_t gs = a.h_scales[hat >> 2], vs = a.h_scales[(hat + chunks) >> 2];
     mx_decode8(g, gs, gate);
     mx_decode8(v, vs, up);
@@ -153,10 +158,6 @@ swiglu_bwd_kernel(SwigluArgs a) {
     __builtin_nontemporal_store(pack8(du), dh + chunks);
   }
 }
-
-// As the pre-norm: a call that moves more than three quarters of the 256 MiB
-// memory-side cache loads past it.
-bool streams(double bytes) { return bytes > 0.75 * 256 * 1024 * 1024; }
 
 template <class F>
 bool launch_chunks(SwigluArgs a, const char* name, hipStream_t s, F kernel) {
