@@ -350,6 +350,61 @@ def test_more_tokens_than_a_launch_holds(b):
         assert torch.equal(r["xp"][int(r["row_map"][t, 0])], x[t])
 
 
+@pytest.mark.parametrize("dtype,T,H,align", [("bf16", 8200, 2056, 16), ("f32", 5000, 2048, 1)])
+def test_gradients_of_many_wide_rows(b, dtype, T, H, align):
+    """Beyond 256 MiB of rows the two gradients come in passes of their own: the bits of
+    each alone and of the same tokens in a small batch; pads zero, rows behind them left."""
+    k, E, dt = 8, 24, TYPES[dtype]
+    print_case("unpermute_bwd_apart", T=T, H=H, align=align, dtype=dtype)
+    g = torch.Generator(device="cuda").manual_seed(12)
+    ids = torch.randint(-2, E, (T, k), generator=g, device="cuda", dtype=torch.int32)
+    x = torch.randn(T, H, generator=g, device="cuda").to(dt)
+    w = torch.randn(T, k, generator=g, device="cuda")
+    perm = b.w4a4_permute_fwd(x, ids, E, align)
+    o = torch.randn(perm["xp"].shape, generator=g, device="cuda").to(dt)
+    out = dict(do=torch.full_like(o, 7.0), dtopk_w=torch.full((T, k), 7.0, device="cuda"))
+    r = b.w4a4_unpermute_bwd(x, o, perm, w, out=out)
+    n = int(perm["offsets"][-1])
+    assert bool((r["do"][n:] == 7).all())
+    src, row = perm["src_row"][:n], perm["row_map"].long()
+    assert not r["do"][:n][src < 0].any()
+    live = row >= 0
+    assert torch.equal(r["do"][row[live]], (w[..., None] * x[:, None, :].float())[live].to(dt))
+    assert not r["dtopk_w"][~live].any()
+    for t0 in (0, 4000, T - 60):
+        part = b.w4a4_permute_fwd(x[t0:t0 + 60], ids[t0:t0 + 60].contiguous(), E)
+        op = torch.zeros_like(part["xp"])
+        op[part["row_map"].long()[live[t0:t0 + 60]]] = o[row[t0:t0 + 60][live[t0:t0 + 60]]]
+        p = b.w4a4_unpermute_bwd(x[t0:t0 + 60], op, part, w[t0:t0 + 60].contiguous())
+        assert torch.equal(p["dtopk_w"], r["dtopk_w"][t0:t0 + 60])
+
+
+def test_two_graphs_share_a_workspace(b):
+    """Two captured calls on one workspace, replayed in turn with eager work between: each replay ranks anew."""
+    T, k, H, E = 6100, 8, 64, 40
+    print_case("dispatch_two_graphs", T=T, k=k, H=H, E=E)
+    ws = torch.full((b.workspace_size(b.WS_PERMUTE, T, 0, 0, E, k),), 255, dtype=torch.uint8, device="cuda")
+    assert ws.numel() > 0
+    inputs, graphs = [], []
+    for n in range(2):
+        rng = np.random.default_rng(70 + n)
+        x, ids = _dev(rng.standard_normal((T, H)), torch.bfloat16), torch.from_numpy(_ids(T, k, E, "any", rng)).cuda()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = b.w4a4_permute_fwd(x, ids, E, 32, workspace=ws)
+        inputs.append((x, ids))
+        graphs.append((graph, got))
+    for _ in range(3):
+        for (x, ids), (graph, got) in zip(inputs, graphs):
+            graph.replay()
+            torch.cuda.synchronize()
+            want = b.w4a4_permute_fwd(x, ids, E, 32)
+            n = int(want["offsets"][-1])
+            assert torch.equal(got["offsets"], want["offsets"]) and torch.equal(got["row_map"], want["row_map"])
+            assert torch.equal(got["src_row"][:n], want["src_row"][:n]) and torch.equal(got["xp"][:n], want["xp"][:n])
+            ids.copy_(torch.roll(ids, 1, 0))
+
+
 def test_streams_and_captured_graph(b):
     """A training step's four calls in one captured graph with a workspace of its
     own, replayed with new inputs between eager calls on another stream."""
