@@ -16,11 +16,11 @@
 // read or written once, and a token's row is read once for its k destinations.
 // Linear copies of 1 GiB reach 6.5 TB/s on this card, rows of 4 KB in the order
 // of the tokens 5.5 to 5.9: 16384 tokens of 2048 in bf16 with 8 of 128 experts
-// each take 110 us sorted (101 the copy, 9 the maps), 102 combined, 206 for the
-// combination's gradients.  Two kernels that went by expert rows instead, so that
-// those are streamed and the tokens' come from the memory-side cache, took 140
-// for 101 (the copy) and 220 for 206.  One token takes 3.5 us sorted, 48 2.9
-// combined, 61 3.6 for the gradients.
+// each take 110 us sorted (101 the copy, 9 the maps), 102 combined, 202 for the
+// combination's gradients (100 dp, 101 do).  Two kernels that went by expert rows
+// instead, so that those are streamed and the tokens' come from the memory-side
+// cache, took 140 for 101 (the copy) and 220 for 207 (both gradients in one).
+// One token takes 3.4 us sorted, 48 3.3 combined, 61 4.2 for the gradients.
 
 #include <type_traits>
 
@@ -95,9 +95,10 @@ __device__ __forceinline__ bool in_range(int e, int E) { return static_cast<uint
 // Per chunk of 1024 entries, one thread each: an entry's rank within the chunk
 // among those of its expert (ascending t * k + j, also where a token names an
 // expert twice), parked in row_map, and the chunk's counts.  The waves' counts
-// per expert meet in LDS.  Count and scan take 4.3 and 4.7 us for 131072 entries
-// of 128 experts; adding the chunks' counts up in every workgroup of the copy
-// instead of a scan saves nothing there and costs 14 us with rows of 256 bytes.
+// per expert meet in LDS.  Count and scan take 4.3 to 4.9 us each for 131072
+// entries of 128 experts; adding the chunks' counts up in every workgroup of the
+// copy instead of a scan saves nothing there and costs 14 us with rows of 256
+// bytes.
 __global__ void __launch_bounds__(kRankChunk)
 permute_count_kernel(int64_t n, int E, const int32_t* __restrict__ idx, int32_t* __restrict__ row_map,
                      int32_t* __restrict__ counts) {
@@ -638,7 +639,7 @@ bool launch_unpermute_bwd(int64_t T, int H, int k, int E, int64_t rows, bool f32
   // Both wanted of many wide rows: dp first, then do, so that reads and writes of
   // rows in token order do not alternate; dy is read twice, mostly from the
   // memory-side cache.  16384 tokens of 2048 202 us against 207 in one pass, 32768
-  // 403 against 429, 16384 of 4096 394 against 437; 8192 of 2048 106 against 105, 4096
+  // 400 against 429, 16384 of 4096 393 against 437; 8192 of 2048 106 against 105, 4096
   // 58 against 54, 16384 of 1024 113 against 104.
   const bool apart = d_o != nullptr && dw != nullptr && a.chunks >= 256 && T * k * row_bytes >= 256.0 * 1024 * 1024;
   auto scatter = [&] {
