@@ -22,6 +22,7 @@
 // cache, took 140 for 101 (the copy) and 220 for 207 (both gradients in one).
 // One token takes 3.4 us sorted, 48 3.3 combined, 61 4.2 for the gradients.
 
+#include <algorithm>
 #include <type_traits>
 
 #include "device_common.h"
@@ -201,16 +202,68 @@ struct PermuteArgs {
   int32_t *offsets, *row_map, *src_row;
   const int32_t *counts, *expert_count;
   int64_t token_blocks, first;         // workgroups of tokens (those of pad rows follow); this launch's first
+  int pad_parts;                       // workgroups of pad rows per expert
 };
 
-// Zeros in the pad rows of an expert whose group's pad rows are [r0, r1).
+// Workgroups that clear the pad rows of an expert, of which there may be `rows`:
+// 64 KiB to each, and two a compute unit for all experts.  A workgroup an expert
+// took 14.4 us against 5.7 for the combination's gradients of 52 tokens of 7 KB in
+// groups of 128 for 16 experts, 19.2 against 14.4 for 512 of 4 KB and 128 experts.
+int pad_parts(int64_t rows, int chunks, int E) {
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((rows * chunks + 4095) / 4096, 512 / E)));
+}
+
+// A part's share of the zeros in the pad rows [r0, r1) of an expert.
 template <int THREADS>
-__device__ __forceinline__ void clear_pad_rows(const PermuteArgs& a, int r0, int r1) {
-  for (int r = r0 + static_cast<int>(threadIdx.x); r < r1; r += THREADS) a.src_row[r] = -1;
+__device__ __forceinline__ void clear_pad_rows(const PermuteArgs& a, int r0, int r1, int part) {
+  if (part == 0)
+    for (int r = r0 + static_cast<int>(threadIdx.x); r < r1; r += THREADS) a.src_row[r] = -1;
   if (a.xp == nullptr) return;
-  for (int r = r0 + static_cast<int>(threadIdx.x) / kWave; r < r1; r += THREADS / kWave) {
+  constexpr int W = THREADS / kWave;
+  for (int r = r0 + part * W + static_cast<int>(threadIdx.x) / kWave; r < r1; r += a.pad_parts * W) {
     u32x4_t* row = reinterpret_cast<u32x4_t*>(a.xp) + static_cast<int64_t>(r) * a.chunks;
     for (int c = threadIdx.x % kWave; c < a.chunks; c += kWave) row[c] = u32x4_t{0u, 0u, 0u, 0u};
+  }
+}
+
+// Rows of a length that 64 bytes do not divide start anywhere in a line, and a
+// wave's 64 chunks would write parts of the lines at both of its ends.  Where many
+// are written, every destination gets its chunks in lanes counted from a line's
+// start, so that only a row's own ends are written in parts.  A lane's chunk then
+// differs from destination to destination: each loads its own, all before the
+// first is stored (from the caches after the first).  16384 tokens of 2056 with 5
+// experts each 88 us against 103 (of 2048: 71), 6760 of 6008 94 against 121; not
+// worth it with one destination (16384 of 2056 34 against 31), short rows (16384
+// of 264 with 5 23.6 against 22.8), what the caches hold (2000 of 2056 with 5 17.0
+// against 16.2) and in the one launch for few tokens (2500 of 4104 40 against 36).
+bool by_lines(int64_t T, int k, int chunks) {
+  return chunks % 4 != 0 && chunks >= 64 && k > 1 && T * k * chunks >= int64_t{1} << 22;
+}
+__device__ __forceinline__ int line_offset(const u32x4_t* p) {
+  return static_cast<int>(reinterpret_cast<uintptr_t>(p) >> 4) & 7;
+}
+
+// For each destination row_of(j), j < k, that is one: store(j, p, chunk c of src)
+// for all c, TEAM lanes.
+template <int TEAM, class Row, class Store>
+__device__ __forceinline__ void to_lines(const u32x4_t* src, u32x4_t* dst, int chunks, int k, int lane, Row row_of,
+                                         Store store) {
+  u32x4_t* to[kMaxK];
+  int at[kMaxK];
+#pragma unroll
+  for (int j = 0; j < kMaxK; ++j) {
+    const int64_t r = j < k ? row_of(j) : -1;
+    to[j] = dst + (r < 0 ? 0 : r) * chunks;
+    at[j] = r < 0 ? 1 << 30 : lane - line_offset(to[j]);
+  }
+  for (int c0 = 0; c0 < chunks + 7; c0 += TEAM) {
+    u32x4_t v[kMaxK];
+#pragma unroll
+    for (int j = 0; j < kMaxK; ++j)
+      if (static_cast<uint32_t>(at[j] + c0) < static_cast<uint32_t>(chunks)) v[j] = src[at[j] + c0];
+#pragma unroll
+    for (int j = 0; j < kMaxK; ++j)
+      if (static_cast<uint32_t>(at[j] + c0) < static_cast<uint32_t>(chunks)) store(j, to[j] + at[j] + c0, v[j]);
   }
 }
 
@@ -221,10 +274,15 @@ __device__ __forceinline__ u32x4_t first_chunk(const PermuteArgs& a, int64_t t, 
     v = reinterpret_cast<const u32x4_t*>(a.x + t * a.x_pitch)[lane];
   return v;
 }
-template <int TEAM>
+template <int TEAM, bool LINES>
 __device__ __forceinline__ void copy_token(const PermuteArgs& a, int64_t t, int lane, u32x4_t v, const int32_t* rows) {
   const u32x4_t* src = reinterpret_cast<const u32x4_t*>(a.x + t * a.x_pitch);
   u32x4_t* dst = reinterpret_cast<u32x4_t*>(a.xp);
+  if constexpr (LINES) {
+    to_lines<TEAM>(src, dst, a.chunks, a.k, lane, [&](int j) { return rows[j]; },
+                   [](int, u32x4_t* p, const u32x4_t& w) { __builtin_nontemporal_store(w, p); });
+    return;
+  }
   for (int c = lane; c < a.chunks; c += TEAM) {
     if (c != lane) v = src[c];
     for (int j = 0; j < a.k; ++j) {
@@ -280,8 +338,8 @@ permute_few_kernel(PermuteArgs a) {
   if (blockIdx.x == 0)
     for (int e = tid; e <= a.E; e += THREADS) a.offsets[e] = s_off[e];
   if (pads) {
-    const int e = static_cast<int>(blockIdx.x - a.token_blocks);
-    clear_pad_rows<THREADS>(a, s_off[e] + s_before[e] + s_after[e], s_off[e + 1]);
+    const int b = static_cast<int>(blockIdx.x - a.token_blocks), e = b / a.pad_parts;
+    clear_pad_rows<THREADS>(a, s_off[e] + s_before[e] + s_after[e], s_off[e + 1], b % a.pad_parts);
     return;
   }
   if (wave == 0) {
@@ -306,12 +364,12 @@ permute_few_kernel(PermuteArgs a) {
   for (int g = 0; g < G / kTeams; ++g) {
     const int own = g * kTeams + team;
     const int64_t t = t0 + own;
-    if (t < a.T) copy_token<kThreads>(a, t, tl, g == 0 ? v : first_chunk(a, t, tl), s_row + own * a.k);
+    if (t < a.T) copy_token<kThreads, false>(a, t, tl, g == 0 ? v : first_chunk(a, t, tl), s_row + own * a.k);
   }
 }
 
 // After the counts and their scan: TEAM lanes per token.
-template <int TEAM>
+template <int TEAM, bool LINES>
 __global__ void __launch_bounds__(kThreads)
 permute_rows_kernel(PermuteArgs a) {
   constexpr int kTeams = kThreads / TEAM;
@@ -319,8 +377,8 @@ permute_rows_kernel(PermuteArgs a) {
   const int tid = threadIdx.x, lane = tid % TEAM;
   const int64_t block = a.first + blockIdx.x;
   if (block >= a.token_blocks) {
-    const int e = static_cast<int>(block - a.token_blocks);
-    clear_pad_rows<kThreads>(a, a.offsets[e] + a.expert_count[e], a.offsets[e + 1]);
+    const int b = static_cast<int>(block - a.token_blocks), e = b / a.pad_parts;
+    clear_pad_rows<kThreads>(a, a.offsets[e] + a.expert_count[e], a.offsets[e + 1], b % a.pad_parts);
     return;
   }
   const int64_t t0 = block * kTeams, t = t0 + tid / TEAM;
@@ -337,7 +395,7 @@ permute_rows_kernel(PermuteArgs a) {
     s_row[tid] = row;
   }
   __syncthreads();
-  if (t < a.T && a.xp != nullptr) copy_token<TEAM>(a, t, lane, v, s_row + tid / TEAM * a.k);
+  if (t < a.T && a.xp != nullptr) copy_token<TEAM, LINES>(a, t, lane, v, s_row + tid / TEAM * a.k);
 }
 
 __global__ void __launch_bounds__(kThreads)
@@ -425,6 +483,7 @@ struct UnpermuteBwdArgs {
   void* d_o;                  // null: dp alone
   float* dw;                  // null: do alone
   int64_t main_blocks, first; // workgroups of entries or tokens (those of pad rows follow); this launch's first
+  int pad_parts;              // workgroups of pad rows per expert
 };
 
 // Rows in use: entries of row_map at or past this are not dispatched.
@@ -448,11 +507,13 @@ __device__ __forceinline__ void clear_row(void* rows, int64_t r, int chunks) {
   for (int c = threadIdx.x % kWave; c < chunks; c += kWave) row[c] = u32x4_t{0u, 0u, 0u, 0u};
 }
 
-// Pad rows of expert e: up to 127 rows before its group's end with src_row -1.
-__device__ __forceinline__ void clear_pad_rows(const UnpermuteBwdArgs& a, int e) {
+// A part's share of the pad rows of an expert: up to 127 rows before its group's
+// end with src_row -1.
+__device__ __forceinline__ void clear_pad_rows(const UnpermuteBwdArgs& a, int b) {
+  const int e = b / a.pad_parts, part = b % a.pad_parts;
   const int64_t lo = max(a.offsets[e], 0);
   const int64_t hi = min(static_cast<int64_t>(a.offsets[e + 1]), static_cast<int64_t>(a.rows));
-  for (int64_t r = max(lo, hi - 127) + threadIdx.x / kWave; r < hi; r += kWaves)
+  for (int64_t r = max(lo, hi - 127) + part * kWaves + threadIdx.x / kWave; r < hi; r += a.pad_parts * kWaves)
     if (a.src_row[r] < 0) clear_row(a.d_o, r, a.chunks);
 }
 
@@ -512,8 +573,8 @@ unpermute_bwd_entries_kernel(UnpermuteBwdArgs a) {
   else if (threadIdx.x % LANES == 0) a.dw[i] = 0.0f;
 }
 
-// do alone: a workgroup per token, dy read once.
-template <typename T>
+// do alone: a workgroup per token, dy read once from memory.
+template <typename T, bool LINES>
 __global__ void __launch_bounds__(kThreads)
 unpermute_bwd_scatter_kernel(UnpermuteBwdArgs a) {
   const int64_t t = a.first + blockIdx.x;
@@ -523,6 +584,16 @@ unpermute_bwd_scatter_kernel(UnpermuteBwdArgs a) {
   }
   const uint32_t used = used_rows(a);
   const u32x4_t* dy = reinterpret_cast<const u32x4_t*>(static_cast<const uint8_t*>(a.dy) + t * a.dy_pitch);
+  if constexpr (LINES) {
+    to_lines<kThreads>(
+        dy, static_cast<u32x4_t*>(a.d_o), a.chunks, a.k, threadIdx.x,
+        [&](int j) {
+          const uint32_t r = static_cast<uint32_t>(a.row_map[t * a.k + j]);
+          return r < used ? static_cast<int64_t>(r) : -1;
+        },
+        [&](int j, u32x4_t* p, const u32x4_t& w) { store_scaled<T>(Chunk<T>{w}, a.w[t * a.k + j], p); });
+    return;
+  }
   for (int c = threadIdx.x; c < a.chunks; c += kThreads) {
     Chunk<T> g;
     g.w = dy[c];
@@ -556,8 +627,9 @@ bool launch_permute(int64_t T, int row_bytes, int k, int E, int row_align, const
     return launch_ok("permute_rows");
   }
   PermuteArgs a{T, row_bytes / 16, k, E, row_align, static_cast<const uint8_t*>(x), x_pitch, topk_idx,
-                static_cast<uint8_t*>(xp), offsets, row_map, src_row, nullptr, nullptr, T, 0};
-  const int pad_blocks = row_align > 1 ? E : 0;
+                static_cast<uint8_t*>(xp), offsets, row_map, src_row, nullptr, nullptr, T, 0,
+                pad_parts(row_align - 1, xp != nullptr ? row_bytes / 16 : 0, E)};
+  const int pad_blocks = row_align > 1 ? E * a.pad_parts : 0;
   if (one_launch(T, k)) {
     auto few = [&](auto threads, auto tokens) {
       constexpr int THREADS = decltype(threads)::value, G = decltype(tokens)::value;
@@ -581,13 +653,14 @@ bool launch_permute(int64_t T, int row_bytes, int k, int E, int row_align, const
   launch_kernel("permute_scan", permute_scan_kernel, dim3(1), dim3(kScanThreads), 0, s, counts,
                 static_cast<int>(chunks), E, cols, row_align, offsets, counts + chunks * E);
   if (!launch_ok("permute_scan")) return false;
+  const bool lines = by_lines(T, k, a.chunks);
   auto rows = [&](auto team) {
     constexpr int TEAM = decltype(team)::value, kTeams = kThreads / TEAM;
     a.token_blocks = (T + kTeams - 1) / kTeams;
     launch_parts(a.token_blocks + pad_blocks, kThreads, [&](int64_t first, int64_t count) {
       a.first = first;
-      launch_kernel("permute_rows", permute_rows_kernel<TEAM>, dim3(static_cast<unsigned>(count)), dim3(kThreads), 0, s,
-                    a);
+      launch_kernel("permute_rows", lines ? permute_rows_kernel<TEAM, (TEAM >= kWave)> : permute_rows_kernel<TEAM, false>,
+                    dim3(static_cast<unsigned>(count)), dim3(kThreads), 0, s, a);
     });
   };
   // Lanes per token.  (16384 tokens in bf16 take 17 us with rows of 128, 36 with
@@ -625,7 +698,7 @@ bool launch_unpermute_bwd(int64_t T, int H, int k, int E, int64_t rows, bool f32
                           const int32_t* src_row, void* d_o, float* dw, hipStream_t s) {
   if (T == 0) return true;
   UnpermuteBwdArgs a{T, H / (f32 ? 4 : 8), k, E, static_cast<uint32_t>(rows), dy, dy_pitch, o, row_map, w,
-                     E > 0 ? offsets : nullptr, src_row, d_o, dw, 0, 0};
+                     E > 0 ? offsets : nullptr, src_row, d_o, dw, 0, 0, 1};
   const double row_bytes = 16.0 * a.chunks;
   auto go = [&](int64_t main_blocks, int64_t others, auto kernel) {
     a.main_blocks = main_blocks;
@@ -635,7 +708,11 @@ bool launch_unpermute_bwd(int64_t T, int H, int k, int E, int64_t rows, bool f32
     });
   };
   // as many rows as slots: no group has been padded
-  const int pad_blocks = d_o != nullptr && rows > T * k ? E : 0;
+  int pad_blocks = 0;
+  if (d_o != nullptr && rows > T * k) {
+    a.pad_parts = pad_parts(std::min<int64_t>(127, (rows - T * k + E - 1) / E), a.chunks, E);
+    pad_blocks = E * a.pad_parts;
+  }
   // Both wanted of many wide rows: dp first, then do, so that reads and writes of
   // rows in token order do not alternate; dy is read twice, mostly from the
   // memory-side cache.  16384 tokens of 2048 202 us against 207 in one pass, 32768
@@ -643,8 +720,13 @@ bool launch_unpermute_bwd(int64_t T, int H, int k, int E, int64_t rows, bool f32
   // 58 against 54, 16384 of 1024 113 against 104.
   const bool apart = d_o != nullptr && dw != nullptr && a.chunks >= 256 && T * k * row_bytes >= 256.0 * 1024 * 1024;
   auto scatter = [&] {
-    if (f32) go(T, pad_blocks, unpermute_bwd_scatter_kernel<float>);
-    else go(T, pad_blocks, unpermute_bwd_scatter_kernel<uint16_t>);
+    const bool lines = by_lines(T, k, a.chunks);
+    auto type = [&](auto elem) {
+      using Elem = decltype(elem);
+      go(T, pad_blocks, lines ? unpermute_bwd_scatter_kernel<Elem, true> : unpermute_bwd_scatter_kernel<Elem, false>);
+    };
+    if (f32) type(float{});
+    else type(uint16_t{});
     return launch_ok("unpermute_bwd");
   };
   if (dw == nullptr) return scatter();

@@ -379,6 +379,55 @@ def test_gradients_of_many_wide_rows(b, dtype, T, H, align):
         assert torch.equal(p["dtopk_w"], r["dtopk_w"][t0:t0 + 60])
 
 
+@pytest.mark.parametrize("dtype,T,H,k,align", [("bf16", 2100, 2056, 8, 16), ("f32", 2100, 1032, 8, 1),
+                                               ("bf16", 8100, 520, 8, 32), ("bf16", 6000, 2808, 2, 1),
+                                               ("f32", 2700, 1032, 7, 128)])
+def test_many_rows_that_share_lines(b, dtype, T, H, k, align):
+    """From 64 MiB of rows that 64 bytes do not divide each is written by the lines of its place: to buffers that
+    start inside a line, from a column slice; rows behind the last group and beside the buffers are left."""
+    E, dt = 19, TYPES[dtype]
+    print_case("dispatch_lines", T=T, H=H, k=k, align=align, dtype=dtype)
+    g = torch.Generator(device="cuda").manual_seed(T + H)
+    ids = torch.randint(-1, E, (T, k), generator=g, device="cuda", dtype=torch.int32)
+    x = torch.randn(T, H + 16, generator=g, device="cuda").to(dt)[:, 8:8 + H]
+    w = torch.randn(T, k, generator=g, device="cuda")
+    cap, skip = b.rows_capacity(T, k, E, align), 16 // x.element_size()
+    flat = torch.full((2, cap * H + 2 * skip), 7.0, dtype=dt, device="cuda")
+    xp, do = (flat[i, skip:-skip].view(cap, H) for i in range(2))
+    perm = b.w4a4_permute_fwd(x, ids, E, align, out=dict(xp=xp))
+    b.w4a4_unpermute_bwd(x, None, perm, w, dtopk_w=False, out=dict(do=do))
+    n, row, live = int(perm["offsets"][-1]), perm["row_map"].long(), perm["row_map"] >= 0
+    assert torch.equal(live, ids >= 0) and torch.equal(perm["src_row"].long()[row[live]], live.nonzero()[:, 0])
+    assert torch.equal(xp[row[live]], x[live.nonzero()[:, 0]])
+    assert torch.equal(do[row[live]], (w[..., None] * x[:, None, :].float())[live].to(dt))
+    pad = perm["src_row"][:n] < 0
+    assert int(pad.sum()) == n - int(live.sum())
+    for out in (xp, do):
+        assert not out[:n][pad].any() and bool((out[n:] == 7).all())
+    assert bool((flat[:, :skip] == 7).all()) and bool((flat[:, -skip:] == 7).all())
+
+
+@pytest.mark.parametrize("T,H,k,E", [(1, 8200, 1, 1), (9, 65536, 2, 3), (300, 4104, 2, 2), (5, 1032, 8, 600)])
+def test_wide_pads_of_few_experts(b, T, H, k, E):
+    """Pad rows that several workgroups clear for an expert."""
+    print_case("dispatch_pads", T=T, H=H, k=k, E=E)
+    g = torch.Generator(device="cuda").manual_seed(T + H)
+    ids = torch.randint(0, E, (T, k), generator=g, device="cuda", dtype=torch.int32)
+    x = torch.randn(T, H, generator=g, device="cuda").bfloat16()
+    w = torch.randn(T, k, generator=g, device="cuda")
+    cap = b.rows_capacity(T, k, E, 128)
+    full = lambda: torch.full((cap, H), 7.0, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    perm = b.w4a4_permute_fwd(x, ids, E, 128, out=dict(xp=full()))
+    r = b.w4a4_unpermute_bwd(x, perm["xp"], perm, w, out=dict(do=full()))
+    alone = b.w4a4_unpermute_bwd(x, None, perm, w, dtopk_w=False, out=dict(do=full()))
+    n = int(perm["offsets"][-1])
+    pad = perm["src_row"][:n] < 0
+    assert int(pad.sum()) == n - T * k
+    for out in (perm["xp"], r["do"], alone["do"]):
+        assert not out[:n][pad].any() and bool((out[n:] == 7).all()) and bool((out[:n][~pad] != 7).any())
+    assert torch.equal(r["do"], alone["do"])
+
+
 def test_two_graphs_share_a_workspace(b):
     """Two captured calls on one workspace, replayed in turn with eager work between: each replay ranks anew."""
     T, k, H, E = 6100, 8, 64, 40
