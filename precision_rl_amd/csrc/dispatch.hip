@@ -203,14 +203,31 @@ struct PermuteArgs {
   const int32_t *counts, *expert_count;
   int64_t token_blocks, first;         // workgroups of tokens (those of pad rows follow); this launch's first
   int pad_parts;                       // workgroups of pad rows per expert
+  bool pads_past;                      // pad rows are stored past the caches
 };
 
 // Workgroups that clear the pad rows of an expert, of which there may be `rows`:
-// 64 KiB to each, and two a compute unit for all experts.  A workgroup an expert
-// took 14.4 us against 5.7 for the combination's gradients of 52 tokens of 7 KB in
-// groups of 128 for 16 experts, 19.2 against 14.4 for 512 of 4 KB and 128 experts.
-int pad_parts(int64_t rows, int chunks, int E) {
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((rows * chunks + 4095) / 4096, 512 / E)));
+// 64 KiB to each, `most` for all experts (two of 256 threads a compute unit; fewer
+// of those that count all entries first: 512 tokens of 4 KB in groups of 128 for
+// 128 experts 14.3 us with 128, 15.4 with 512).  A workgroup an expert took 14.4
+// us against 5.7 for the combination's gradients of 52 tokens of 7 KB in groups of
+// 128 for 16 experts, 19.0 against 14.4 for 512 of 4 KB and 128 experts.
+int pad_parts(int64_t rows, int chunks, int E, int most = 512) {
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((rows * chunks + 4095) / 4096, most / E)));
+}
+
+// A wave's zeros in row r, past the caches where the rows that the call may write,
+// pads among them, are more than they hold: 1478 tokens of 14 KB sorted in groups
+// of 64 for 171 experts 42 us against 53, 16384 of 4 KB in groups of 128 for 128
+// 117 against 128; 64 of 8 KB 18.4 against 16.6.
+__device__ __forceinline__ void clear_row(void* rows, int64_t r, int chunks, bool past) {
+  u32x4_t* row = static_cast<u32x4_t*>(rows) + r * chunks;
+  const u32x4_t zero{0u, 0u, 0u, 0u};
+  if (past) {
+    for (int c = threadIdx.x % kWave; c < chunks; c += kWave) __builtin_nontemporal_store(zero, row + c);
+  } else {
+    for (int c = threadIdx.x % kWave; c < chunks; c += kWave) row[c] = zero;
+  }
 }
 
 // A part's share of the zeros in the pad rows [r0, r1) of an expert.
@@ -220,10 +237,8 @@ __device__ __forceinline__ void clear_pad_rows(const PermuteArgs& a, int r0, int
     for (int r = r0 + static_cast<int>(threadIdx.x); r < r1; r += THREADS) a.src_row[r] = -1;
   if (a.xp == nullptr) return;
   constexpr int W = THREADS / kWave;
-  for (int r = r0 + part * W + static_cast<int>(threadIdx.x) / kWave; r < r1; r += a.pad_parts * W) {
-    u32x4_t* row = reinterpret_cast<u32x4_t*>(a.xp) + static_cast<int64_t>(r) * a.chunks;
-    for (int c = threadIdx.x % kWave; c < a.chunks; c += kWave) row[c] = u32x4_t{0u, 0u, 0u, 0u};
-  }
+  for (int r = r0 + part * W + static_cast<int>(threadIdx.x) / kWave; r < r1; r += a.pad_parts * W)
+    clear_row(a.xp, r, a.chunks, a.pads_past);
 }
 
 // Rows of a length that 64 bytes do not divide start anywhere in a line, and a
@@ -484,6 +499,7 @@ struct UnpermuteBwdArgs {
   float* dw;                  // null: do alone
   int64_t main_blocks, first; // workgroups of entries or tokens (those of pad rows follow); this launch's first
   int pad_parts;              // workgroups of pad rows per expert
+  bool pads_past;             // pad rows are stored past the caches
 };
 
 // Rows in use: entries of row_map at or past this are not dispatched.
@@ -502,11 +518,6 @@ __device__ __forceinline__ void store_scaled(const Chunk<T>& g, float w, u32x4_t
   __builtin_nontemporal_store(q.w, to);
 }
 
-__device__ __forceinline__ void clear_row(void* rows, int64_t r, int chunks) {
-  u32x4_t* row = static_cast<u32x4_t*>(rows) + r * chunks;
-  for (int c = threadIdx.x % kWave; c < chunks; c += kWave) row[c] = u32x4_t{0u, 0u, 0u, 0u};
-}
-
 // A part's share of the pad rows of an expert: up to 127 rows before its group's
 // end with src_row -1.
 __device__ __forceinline__ void clear_pad_rows(const UnpermuteBwdArgs& a, int b) {
@@ -514,7 +525,7 @@ __device__ __forceinline__ void clear_pad_rows(const UnpermuteBwdArgs& a, int b)
   const int64_t lo = max(a.offsets[e], 0);
   const int64_t hi = min(static_cast<int64_t>(a.offsets[e + 1]), static_cast<int64_t>(a.rows));
   for (int64_t r = max(lo, hi - 127) + part * kWaves + threadIdx.x / kWave; r < hi; r += a.pad_parts * kWaves)
-    if (a.src_row[r] < 0) clear_row(a.d_o, r, a.chunks);
+    if (a.src_row[r] < 0) clear_row(a.d_o, r, a.chunks, a.pads_past);
 }
 
 // LANES lanes: do[r] = w[i] dy[t] and dp[i] = <dy[t], o[r]> of entry i = t k + j.
@@ -628,7 +639,9 @@ bool launch_permute(int64_t T, int row_bytes, int k, int E, int row_align, const
   }
   PermuteArgs a{T, row_bytes / 16, k, E, row_align, static_cast<const uint8_t*>(x), x_pitch, topk_idx,
                 static_cast<uint8_t*>(xp), offsets, row_map, src_row, nullptr, nullptr, T, 0,
-                pad_parts(row_align - 1, xp != nullptr ? row_bytes / 16 : 0, E)};
+                pad_parts(row_align - 1, xp != nullptr ? row_bytes / 16 : 0, E,
+                          one_launch(T, k) && T > kOneTokenAWorkgroup ? 128 : 512),
+                streams((static_cast<double>(T) * k + static_cast<double>(E) * (row_align - 1)) * row_bytes)};
   const int pad_blocks = row_align > 1 ? E * a.pad_parts : 0;
   if (one_launch(T, k)) {
     auto few = [&](auto threads, auto tokens) {
@@ -698,7 +711,7 @@ bool launch_unpermute_bwd(int64_t T, int H, int k, int E, int64_t rows, bool f32
                           const int32_t* src_row, void* d_o, float* dw, hipStream_t s) {
   if (T == 0) return true;
   UnpermuteBwdArgs a{T, H / (f32 ? 4 : 8), k, E, static_cast<uint32_t>(rows), dy, dy_pitch, o, row_map, w,
-                     E > 0 ? offsets : nullptr, src_row, d_o, dw, 0, 0, 1};
+                     E > 0 ? offsets : nullptr, src_row, d_o, dw, 0, 0, 1, false};
   const double row_bytes = 16.0 * a.chunks;
   auto go = [&](int64_t main_blocks, int64_t others, auto kernel) {
     a.main_blocks = main_blocks;
@@ -712,6 +725,7 @@ bool launch_unpermute_bwd(int64_t T, int H, int k, int E, int64_t rows, bool f32
   if (d_o != nullptr && rows > T * k) {
     a.pad_parts = pad_parts(std::min<int64_t>(127, (rows - T * k + E - 1) / E), a.chunks, E);
     pad_blocks = E * a.pad_parts;
+    a.pads_past = streams(rows * row_bytes);
   }
   // Both wanted of many wide rows: dp first, then do, so that reads and writes of
   // rows in token order do not alternate; dy is read twice, mostly from the
