@@ -28,6 +28,7 @@
 #include "device_common.h"
 #include "internal.h"
 #include "launch_parts.h"
+#include "row_walk.h"
 
 namespace w4a4 {
 namespace {
@@ -233,12 +234,12 @@ __device__ __forceinline__ void clear_row(void* rows, int64_t r, int chunks, boo
 // A part's share of the zeros in the pad rows [r0, r1) of an expert.
 template <int THREADS>
 __device__ __forceinline__ void clear_pad_rows(const PermuteArgs& a, int r0, int r1, int part) {
-  if (part == 0)
-    for (int r = r0 + static_cast<int>(threadIdx.x); r < r1; r += THREADS) a.src_row[r] = -1;
+  const int tid = static_cast<int>(threadIdx.x);
+  if (part == 0) walk_rows(r0, r1, tid, THREADS, [&](int64_t r) { a.src_row[r] = -1; });
   if (a.xp == nullptr) return;
   constexpr int W = THREADS / kWave;
-  for (int r = r0 + part * W + static_cast<int>(threadIdx.x) / kWave; r < r1; r += a.pad_parts * W)
-    clear_row(a.xp, r, a.chunks, a.pads_past);
+  walk_rows(r0, r1, part * W + tid / kWave, a.pad_parts * W,
+            [&](int64_t r) { clear_row(a.xp, r, a.chunks, a.pads_past); });
 }
 
 // Rows of a length that 64 bytes do not divide start anywhere in a line, and a
