@@ -677,9 +677,11 @@ w4a4_status w4a4_unpermute_fwd(
  *   dy         [T, H].   o [rows, H]: the forward's (NULL without dtopk_w).
  *   d_o        [rows, H] out or NULL; rows at or past expert_offsets[E] are not
  *              written.   dtopk_w [T, k] float out or NULL.
- *   expert_offsets [E+1], src_row: of the permute (to find the pad rows where
- *              d_o is wanted and rows > T * k; else they may be NULL).  Entries
- *              of row_map at or past expert_offsets[E] are not dispatched either.
+ *   expert_offsets [E+1], src_row [rows]: of the permute, to find the pad rows
+ *              where d_o is wanted.  Needed where rows > T * k; with fewer rows
+ *              either may be NULL, but only where no group is padded (slots that
+ *              are not dispatched let padded groups fit).  Entries of row_map at
+ *              or past expert_offsets[E] are not dispatched either.
  */
 w4a4_status w4a4_unpermute_bwd(
     int64_t T, int H, int k, int E, int64_t rows, int dtype, const void* dy, int64_t dy_stride,

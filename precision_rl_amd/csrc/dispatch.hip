@@ -495,7 +495,7 @@ struct UnpermuteBwdArgs {
   const void* o;
   const int32_t* row_map;
   const float* w;
-  const int32_t *offsets, *src_row;   // offsets may be null where no group can be padded
+  const int32_t *offsets, *src_row;   // either may be null where no group is padded
   void* d_o;                  // null: dp alone
   float* dw;                  // null: do alone
   int64_t main_blocks, first; // workgroups of entries or tokens (those of pad rows follow); this launch's first
@@ -520,13 +520,16 @@ __device__ __forceinline__ void store_scaled(const Chunk<T>& g, float w, u32x4_t
 }
 
 // A part's share of the pad rows of an expert: up to 127 rows before its group's
-// end with src_row -1.
+// end (or the buffer's) with src_row -1, none where the last row is a slot's.
 __device__ __forceinline__ void clear_pad_rows(const UnpermuteBwdArgs& a, int b) {
   const int e = b / a.pad_parts, part = b % a.pad_parts;
   const int64_t lo = max(a.offsets[e], 0);
   const int64_t hi = min(static_cast<int64_t>(a.offsets[e + 1]), static_cast<int64_t>(a.rows));
-  for (int64_t r = max(lo, hi - 127) + part * kWaves + threadIdx.x / kWave; r < hi; r += a.pad_parts * kWaves)
-    if (a.src_row[r] < 0) clear_row(a.d_o, r, a.chunks, a.pads_past);
+  if (lo >= hi || a.src_row[hi - 1] >= 0) return;
+  walk_rows(max(lo, hi - 127), hi, part * kWaves + static_cast<int>(threadIdx.x) / kWave, a.pad_parts * kWaves,
+            [&](int64_t r) {
+              if (a.src_row[r] < 0) clear_row(a.d_o, r, a.chunks, a.pads_past);
+            });
 }
 
 // LANES lanes: do[r] = w[i] dy[t] and dp[i] = <dy[t], o[r]> of entry i = t k + j.
@@ -721,10 +724,12 @@ bool launch_unpermute_bwd(int64_t T, int H, int k, int E, int64_t rows, bool f32
       launch_kernel("unpermute_bwd", kernel, dim3(static_cast<unsigned>(count)), dim3(kThreads), 0, s, a);
     });
   };
-  // as many rows as slots: no group has been padded
+  // Whatever the number of rows: where slots are not dispatched, padded groups may
+  // fit a buffer of fewer rows than slots.  An expert's share of the rows beyond
+  // the slots, or there of all rows, sets the number of workgroups alone.
   int pad_blocks = 0;
-  if (d_o != nullptr && rows > T * k) {
-    a.pad_parts = pad_parts(std::min<int64_t>(127, (rows - T * k + E - 1) / E), a.chunks, E);
+  if (d_o != nullptr && E > 0 && offsets != nullptr && src_row != nullptr) {
+    a.pad_parts = pad_parts(std::min<int64_t>(127, ((rows > T * k ? rows - T * k : rows) + E - 1) / E), a.chunks, E);
     pad_blocks = E * a.pad_parts;
     a.pads_past = streams(rows * row_bytes);
   }

@@ -278,7 +278,7 @@ bool launch_gather_rows(int64_t T, int H, int k, int64_t rows, bool f32, const v
                         const float* w, void* out, int64_t out_pitch, const char* name, hipStream_t s);
 // d_o[row_map[t,j]] = rnd(w[t,j] dy[t]) (d_o null: not wanted) and dw[t,j] =
 // <dy[t], o[row_map[t,j]]> (dw null: not wanted); pad rows of d_o, told by
-// offsets and src_row, cleared where rows > T k.
+// offsets and src_row, cleared where both are given.
 bool launch_unpermute_bwd(int64_t T, int H, int k, int E, int64_t rows, bool f32, const void* dy, int64_t dy_pitch,
                           const void* o, const int32_t* row_map, const float* w, const int32_t* offsets,
                           const int32_t* src_row, void* d_o, float* dw, hipStream_t s);
