@@ -42,6 +42,14 @@ __device__ __forceinline__ float sigmoid_fast(float x) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-x * 1.44269504088896341f));
 }
 
+// Gradients of a = gate s up, s = sigmoid(gate), for da.  Products from the bounded
+// factor outwards: da up or da gate alone can pass the range where the result is
+// 0 or moderate, and infinity times 0 is NaN.
+__device__ __forceinline__ void swiglu_grad(float da, float gate, float up, float s, float& dgate, float& dup) {
+  dgate = da * (up * (s * (1.0f + gate * (1.0f - s))));
+  dup = da * (gate * s);
+}
+
 __device__ __forceinline__ float wave_max(float v) {
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor(v, off, kWave));

@@ -463,8 +463,7 @@ dgrad_kernel(DgradArgs args) {
             const float gt = gate[2 * d + p];
             const float up = upv[2 * d + p];
             const float sg = sigmoid_fast(gt);
-            rg[p] = da * up * sg * (1.0f + gt * (1.0f - sg));
-            ru[p] = da * gt * sg;
+            swiglu_grad(da, gt, up, sg, rg[p], ru[p]);
             if constexpr (kCkpt) ra[p] = gt * sg * up;
           }
           dg[d] = pack_bf16x2(rg[0], rg[1]);

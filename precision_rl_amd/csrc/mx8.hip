@@ -213,9 +213,7 @@ q8_dual_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ h, i
           const float a = bf16_to_f32(static_cast<uint16_t>(da[d] >> (16 * p)));
           const float gt = bf16_to_f32(static_cast<uint16_t>(hg[d] >> (16 * p)));
           const float up = bf16_to_f32(static_cast<uint16_t>(hu[d] >> (16 * p)));
-          const float sg = sigmoid_fast(gt);
-          g2[p] = a * up * sg * (1.0f + gt * (1.0f - sg));
-          u2[p] = a * gt * sg;
+          swiglu_grad(a, gt, up, sigmoid_fast(gt), g2[p], u2[p]);
         }
         vg[d] = pack_bf16x2(g2[0], g2[1]);
         vu[d] = pack_bf16x2(u2[0], u2[1]);

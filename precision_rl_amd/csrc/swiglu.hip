@@ -147,12 +147,7 @@ swiglu_bwd_kernel(SwigluArgs a) {
     float da[8], dg[8], du[8];
     unpack8(d, da);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      // products from the bounded factor outwards: da * up or da * gate alone can
-      // pass the range where the result is 0
-      dg[i] = da[i] * (up[i] * (s[i] * (1.0f + gate[i] * (1.0f - s[i]))));
-      du[i] = da[i] * (gate[i] * s[i]);
-    }
+    for (int i = 0; i < 8; ++i) swiglu_grad(da[i], gate[i], up[i], s[i], dg[i], du[i]);
     u32x4_t* dh = reinterpret_cast<u32x4_t*>(a.dh) + hat;
     __builtin_nontemporal_store(pack8(dg), dh);
     __builtin_nontemporal_store(pack8(du), dh + chunks);
