@@ -630,7 +630,7 @@ w4a4_status w4a4_mx_linear_fwd(
  *   (one row each, in slot order); E may be smaller than k.
  *   `dtype` (w4a4_dtype) is the element type of rows and tokens alike.  H % 8 ==
  *   0, H <= 65536, k <= 8, E <= 1024 (else W4A4_ERR_UNSUPPORTED); T >= 0 of any
- *   size with at most 2^31 - 1 rows (tensors of T = 0 tokens may be NULL).
+ *   size with at most 2^31 - 1 rows (tensors of no tokens or no rows may be NULL).
  *   Token tensors (x, y, dx, dy) have rows *_stride elements apart (>= H, a
  *   multiple of 8).  row_map, topk_w, dtopk_w, src_row and the offsets are
  *   aligned to their element, everything else to 16 bytes.  No output may share

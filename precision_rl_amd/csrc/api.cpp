@@ -1171,7 +1171,10 @@ w4a4_status w4a4_unpermute_bwd(int64_t T, int H, int k, int E, int64_t rows, int
   if (st != W4A4_OK || (st = check_buffer_rows(rows)) != W4A4_OK) return st;
   if ((st = check_stride("dy_stride", dy_stride, H)) != W4A4_OK) return st;
   if (T == 0) return W4A4_OK;
-  if (d_o == nullptr && dtopk_w == nullptr) return fail(W4A4_ERR_INVALID_ARG, "neither d_o nor dtopk_w is wanted");
+  if (d_o == nullptr && dtopk_w == nullptr) {
+    if (rows == 0) return W4A4_OK;   // d_o of no rows
+    return fail(W4A4_ERR_INVALID_ARG, "neither d_o nor dtopk_w is wanted");
+  }
   REQUIRE_PTR(dy);
   OPTIONAL_PTR(d_o);
   if (dtopk_w != nullptr && rows > 0) REQUIRE_PTR(o);
