@@ -498,6 +498,7 @@ struct UnpermuteBwdArgs {
   const int32_t *offsets, *src_row;   // either may be null where no group is padded
   void* d_o;                  // null: dp alone
   float* dw;                  // null: do alone
+  uint32_t apart;             // rows in use from which do is made by tokens and not beside dp
   int64_t main_blocks, first; // workgroups of entries or tokens (those of pad rows follow); this launch's first
   int pad_parts;              // workgroups of pad rows per expert
   bool pads_past;             // pad rows are stored past the caches
@@ -537,7 +538,7 @@ __device__ __forceinline__ void clear_pad_rows(const UnpermuteBwdArgs& a, int b)
 // by itself, the lanes join by halves: dp's bits depend on the row's length and
 // type alone.
 template <typename T, int LANES, bool NT>
-__device__ __forceinline__ void entry_grad(const UnpermuteBwdArgs& a, int64_t t, int64_t i, uint32_t r) {
+__device__ __forceinline__ void entry_grad(const UnpermuteBwdArgs& a, int64_t t, int64_t i, uint32_t r, bool store) {
   constexpr int N = Chunk<T>::N, kAhead = 4;
   const int lane = threadIdx.x % LANES;
   const u32x4_t* dy = reinterpret_cast<const u32x4_t*>(static_cast<const uint8_t*>(a.dy) + t * a.dy_pitch);
@@ -558,7 +559,7 @@ __device__ __forceinline__ void entry_grad(const UnpermuteBwdArgs& a, int64_t t,
     for (int n = 0; n < kAhead; ++n) {
       const int c = c0 + n * LANES;
       if (c >= a.chunks) continue;
-      if (a.d_o != nullptr) store_scaled<T>(g[n], w, d_o + c);
+      if (store) store_scaled<T>(g[n], w, d_o + c);
       float part = g[n].get(0) * v[n].get(0);
 #pragma unroll
       for (int q = 1; q < N; ++q) part = fmaf(g[n].get(q), v[n].get(q), part);
@@ -583,12 +584,12 @@ unpermute_bwd_entries_kernel(UnpermuteBwdArgs a) {
   if constexpr (LANES == kWave) slot = __builtin_amdgcn_readfirstlane(slot);
   const int64_t i = block * (kThreads / LANES) + slot;
   if (i >= a.T * a.k) return;
-  const uint32_t r = static_cast<uint32_t>(a.row_map[i]);
-  if (r < used_rows(a)) entry_grad<T, LANES, NT>(a, i / a.k, i, r);
+  const uint32_t r = static_cast<uint32_t>(a.row_map[i]), used = used_rows(a);
+  if (r < used) entry_grad<T, LANES, NT>(a, i / a.k, i, r, a.d_o != nullptr && used < a.apart);
   else if (threadIdx.x % LANES == 0) a.dw[i] = 0.0f;
 }
 
-// do alone: a workgroup per token, dy read once from memory.
+// do by itself: a workgroup per token, dy read once from memory.
 template <typename T, bool LINES>
 __global__ void __launch_bounds__(kThreads)
 unpermute_bwd_scatter_kernel(UnpermuteBwdArgs a) {
@@ -598,6 +599,7 @@ unpermute_bwd_scatter_kernel(UnpermuteBwdArgs a) {
     return;
   }
   const uint32_t used = used_rows(a);
+  if (used < a.apart) return;
   const u32x4_t* dy = reinterpret_cast<const u32x4_t*>(static_cast<const uint8_t*>(a.dy) + t * a.dy_pitch);
   if constexpr (LINES) {
     to_lines<kThreads>(
@@ -715,7 +717,7 @@ bool launch_unpermute_bwd(int64_t T, int H, int k, int E, int64_t rows, bool f32
                           const int32_t* src_row, void* d_o, float* dw, hipStream_t s) {
   if (T == 0) return true;
   UnpermuteBwdArgs a{T, H / (f32 ? 4 : 8), k, E, static_cast<uint32_t>(rows), dy, dy_pitch, o, row_map, w,
-                     E > 0 ? offsets : nullptr, src_row, d_o, dw, 0, 0, 1, false};
+                     E > 0 ? offsets : nullptr, src_row, d_o, dw, UINT32_MAX, 0, 0, 1, false};
   const double row_bytes = 16.0 * a.chunks;
   auto go = [&](int64_t main_blocks, int64_t others, auto kernel) {
     a.main_blocks = main_blocks;
@@ -737,8 +739,15 @@ bool launch_unpermute_bwd(int64_t T, int H, int k, int E, int64_t rows, bool f32
   // rows in token order do not alternate; dy is read twice, mostly from the
   // memory-side cache.  16384 tokens of 2048 202 us against 207 in one pass, 32768
   // 400 against 429, 16384 of 4096 393 against 437; 8192 of 2048 106 against 105, 4096
-  // 58 against 54, 16384 of 1024 113 against 104.
+  // 58 against 54, 16384 of 1024 113 against 104.  Where few slots are dispatched dy
+  // is much of the traffic and one pass takes less: 16384 of 2048 with a quarter of
+  // the slots 67 us against 79, with half 114 against 117; 65536 279 against 372 and
+  // 503 against 560; 16384 of 4096 135 against 161 and 252 against 243.  From five
+  // eighths on two passes are as fast or faster but for 65536 (606 and 665).  The
+  // number is known on the device: with fewer in use the first launch makes both
+  // and the second, which ends at once, costs 5 us in 62 (16384 tokens).
   const bool apart = d_o != nullptr && dw != nullptr && a.chunks >= 256 && T * k * row_bytes >= 256.0 * 1024 * 1024;
+  if (apart) a.apart = static_cast<uint32_t>(T * k / 8 * 5);
   auto scatter = [&] {
     const bool lines = by_lines(T, k, a.chunks);
     auto type = [&](auto elem) {
@@ -749,8 +758,10 @@ bool launch_unpermute_bwd(int64_t T, int H, int k, int E, int64_t rows, bool f32
     else type(uint16_t{});
     return launch_ok("unpermute_bwd");
   };
-  if (dw == nullptr) return scatter();
-  if (apart) a.d_o = nullptr;
+  if (dw == nullptr) {
+    a.apart = 0;
+    return scatter();
+  }
   // Four chunks a lane in flight where the row has as many: 16384 tokens of 128 37
   // us with a wave to an entry, 14 with 16 lanes; 256 39 and 24, 512 62 and 53; 640
   // 75 and with 32 lanes 66, 768 81 and 78, 1024 103 and 105.
@@ -768,10 +779,9 @@ bool launch_unpermute_bwd(int64_t T, int H, int k, int E, int64_t rows, bool f32
     if (f32) shape(float{}, nt);
     else shape(uint16_t{}, nt);
   };
-  if (streams(T * k * row_bytes * (a.d_o != nullptr ? 2 : 1))) types(std::true_type{});
+  if (streams(T * k * row_bytes * (d_o != nullptr ? 2 : 1))) types(std::true_type{});
   else types(std::false_type{});
   if (!launch_ok("unpermute_bwd")) return false;
-  a.d_o = d_o;
   return !apart || scatter();
 }
 
