@@ -87,6 +87,7 @@ typedef enum {
   W4A4_WS_QUANTIZE_PERMUTE_DOMAIN = 4,  /* w4a4_quantize_permute_domain, any group_rows; H = K */
   W4A4_WS_MX8_BACKWARD = 5,             /* w4a4_mx8_expert_bwd */
   W4A4_WS_RMSNORM_BACKWARD = 6,         /* w4a4_add_rmsnorm_bwd with dgamma; I, E, k, row_align unused */
+  /* 7 has never named a workspace */
   W4A4_WS_PERMUTE = 8,                  /* w4a4_permute_fwd: T, E and k; the others unused (0 bytes for few tokens) */
   W4A4_WS_BACKWARD_CKPT = 9             /* w4a4_expert_bwd_ckpt */
 } w4a4_workspace_kind;

@@ -21,6 +21,11 @@
 // instead, so that those are streamed and the tokens' come from the memory-side
 // cache, took 140 for 101 (the copy) and 220 for 207 (both gradients in one).
 // One token takes 3.4 us sorted, 48 3.3 combined, 61 4.2 for the gradients.
+//
+// The quantising permute's routing (quantize.hip) and the expert path's own
+// gather, scatter and pad rows (elementwise.hip) are not built on these: they take
+// bf16 rows of calls whose every slot is dispatched, quantise in the same pass,
+// and their layout, which is the same, is pinned by their own tests.
 
 #include <algorithm>
 #include <type_traits>
@@ -97,7 +102,7 @@ __device__ __forceinline__ bool in_range(int e, int E) { return static_cast<uint
 // Per chunk of 1024 entries, one thread each: an entry's rank within the chunk
 // among those of its expert (ascending t * k + j, also where a token names an
 // expert twice), parked in row_map, and the chunk's counts.  The waves' counts
-// per expert meet in LDS.  Count and scan take 4.3 to 4.9 us each for 131072
+// per expert meet in LDS.  Count and scan take 3.4 to 4.9 us each for 131072
 // entries of 128 experts; adding the chunks' counts up in every workgroup of the
 // copy instead of a scan saves nothing there and costs 14 us with rows of 256
 // bytes.
@@ -135,7 +140,9 @@ inline uint32_t count_lds_bytes(int E) { return static_cast<uint32_t>(kRankChunk
 // counts of expert e (the first kKeep stay in registers), the segments of an
 // expert are scanned in LDS, the chunks' running sums written over the counts,
 // and the experts' padded totals scanned by a thread each.  cols: E rounded up
-// to a power of two.
+// to a power of two.  131072 entries take 4.3 us with 32 experts, 4.6 with 128, and
+// with more, whose segments are longer than kKeep, 10.5 with 256, 22 with 512 and
+// 47 with 1024.
 constexpr int kScanThreads = 1024;
 __global__ void __launch_bounds__(kScanThreads)
 permute_scan_kernel(int32_t* __restrict__ counts, int n_chunks, int E, int cols, int align,
@@ -248,8 +255,10 @@ __device__ __forceinline__ void clear_pad_rows(const PermuteArgs& a, int r0, int
 // start, so that only a row's own ends are written in parts.  A lane's chunk then
 // differs from destination to destination: each loads its own, all before the
 // first is stored (from the caches after the first).  16384 tokens of 2056 with 5
-// experts each 88 us against 103 (of 2048: 71), 6760 of 6008 94 against 121; not
-// worth it with one destination (16384 of 2056 34 against 31), short rows (16384
+// experts each 88 us against 103 (of 2048: 71), 6760 of 6008 94 against 121; writes
+// of less than 64 bytes are 2.2% of all against 5.0 (of 2048: 0.7).  With half of the
+// slots dispatched 50 us against 58, with a quarter 38 against 35; not worth it
+// with one destination (16384 of 2056 34 against 31), short rows (16384
 // of 264 with 5 23.6 against 22.8), what the caches hold (2000 of 2056 with 5 17.0
 // against 16.2) and in the one launch for few tokens (2500 of 4104 40 against 36).
 bool by_lines(int64_t T, int k, int chunks) {
@@ -420,12 +429,17 @@ clear_offsets_kernel(int32_t* offsets, int n) {
 }
 
 // ------------------------------------------------------------ back to tokens
-// NT: expert rows loaded past the caches, where streams() says so of their bytes:
-// 16384 tokens of 2048 with 8 experts each combined in 102 us against 110, 2048 of
-// them in 14.4 against 13.1; the gradients 208 against 221, 28 against 24.  A
-// choice at run time around each load keeps a lane's loads from being in flight
-// together (110 us for 102), so both kernels are built both ways.  Tokens' rows
-// are loaded through the caches: past them the sort takes as long (110 us).
+// NT: expert rows loaded past the caches, where streams() says so of the bytes of
+// all slots: 16384 tokens of 2048 with 8 experts each combined in 102 us against
+// 111, 2048 of them in 14.4 against 13.1; dp of 16384 in 100 against 109; both
+// gradients in one pass of 8000 in 99 against 104, of 2048 in 28 against 24.  How
+// many slots are dispatched is not known on the host: with a quarter of them the
+// rule takes the slower side in between (8192 combined 18.4 us against 16.1, the
+// gradients of 6144 25.4 against 22.9), and the faster one from there on (16384
+// combined 33.8 against 37.5).  A choice at run time around each load keeps a lane's
+// loads from being in flight together (110 us for 102), so both kernels are built
+// both ways.  Tokens' rows are loaded through the caches: past them the sort takes
+// as long (110 us).
 template <bool NT>
 __device__ __forceinline__ u32x4_t load16(const u32x4_t* p) {
   if constexpr (NT) return __builtin_nontemporal_load(p);
@@ -589,7 +603,8 @@ unpermute_bwd_entries_kernel(UnpermuteBwdArgs a) {
   else if (threadIdx.x % LANES == 0) a.dw[i] = 0.0f;
 }
 
-// do by itself: a workgroup per token, dy read once from memory.
+// do by itself: a workgroup per token, dy read once from memory (16384 tokens
+// with 8 experts each 17 us with rows of up to 128, 26 with 512, 101 with 2048).
 template <typename T, bool LINES>
 __global__ void __launch_bounds__(kThreads)
 unpermute_bwd_scatter_kernel(UnpermuteBwdArgs a) {
