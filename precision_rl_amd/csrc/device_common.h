@@ -44,9 +44,11 @@ __device__ __forceinline__ float sigmoid_fast(float x) {
 
 // Gradients of a = gate s up, s = sigmoid(gate), for da.  Products from the bounded
 // factor outwards: da up or da gate alone can pass the range where the result is
-// 0 or moderate, and infinity times 0 is NaN.
+// 0 or moderate, and infinity times 0 is NaN.  s (1 + gate (1 - s)) reaches 1.0998,
+// so dgate is made of its half: no product passes the range but where the result
+// does.
 __device__ __forceinline__ void swiglu_grad(float da, float gate, float up, float s, float& dgate, float& dup) {
-  dgate = da * (up * (s * (1.0f + gate * (1.0f - s))));
+  dgate = 2.0f * (da * (up * (s * (0.5f + gate * fmaf(-0.5f, s, 0.5f)))));
   dup = da * (gate * s);
 }
 
