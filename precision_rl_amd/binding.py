@@ -706,8 +706,9 @@ def w4a4_unpermute_bwd(dy, o, perm, topk_w, do=True, dtopk_w=True, out=None):
     """Gradients of ``w4a4_unpermute_fwd`` for dy [T, H], the gradient of y (a column slice will do): do [rows, H]
     (the type of dy; do[row_map[t, j]] = topk_w[t, j] dy[t], pad rows zero, rows from offsets[E] on not written)
     and dtopk_w [T, k] float32 (<dy[t], o[row_map[t, j]]>, 0 where not dispatched).  o: the forward's; None will do
-    without dtopk_w.  perm: the dict of ``w4a4_permute_fwd`` (or of a quantise-and-permute call).  Returns a dict of
-    what `do` and `dtopk_w` ask for; tensors of `out` are used where given."""
+    without dtopk_w.  perm: the dict of ``w4a4_permute_fwd`` (or of a quantise-and-permute call); where o holds fewer
+    rows than that call's (those in use), with its src_row cut to as many.  Returns a dict of what `do` and `dtopk_w`
+    ask for; tensors of `out` are used where given."""
     (T, H), dev = _matrix(dy, "dy")
     row_map, offsets, src_row = perm["row_map"], perm["offsets"], perm["src_row"]
     k = _row(row_map)[1]
